@@ -24,8 +24,11 @@ EP_FLAG_BAD_EXPERT = 1
 EP_FLAG_OVERFLOW = 2
 EP_FLAG_BAD_ROW = 4
 EP_FLAG_TIMEOUT = 8
+EP_FLAG_BAD_LOGIT = 16
 
 LAYOUT_KINDS = {"contiguous": 0, "masked": 1}
+LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 _lib = None
 
@@ -71,6 +74,9 @@ def load():
                                     i64, P, P, sz, P], i32),
         "ep_combine": ([P, P, P, i64, i64, i32, i64, P, P, P], i32),
         "ep_combine_fp8": ([P, P, P, P, i64, i64, i32, i64, P, P, P], i32),
+        "ep_route": ([P, i32, P, i64, i32, i32, i32, i32, i32, i32, ctypes.c_float, P, P, P, P], i32),
+        "ep_group_gemm_fp8": ([P, P, i64, i64, P, P, i64, i32, P, P, i32, i32, P, P, P], i32),
+        "ep_group_gemm_swiglu_fp8": ([P, P, i64, i64, P, P, i64, i32, P, P, i32, i32, P, P, P, P], i32),
         "ep_status_read": ([P, P, P], i32),
         "ep_pipeline_create": ([i32, ctypes.POINTER(ctypes.c_void_p)], i32),
         "ep_pipeline_destroy": ([P], i32),
@@ -424,6 +430,129 @@ def combine_reduce(partial, rl, T, out=None, status=None):
     return out
 
 
+def _on_current(device, fn, *args):
+    """Call `fn` with `device` current, skipping the switch when it already is."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="softmax",
+          renormalize=True, scale=1.0, topk_idx=None, topk_w=None, status=None):
+    """Top-k experts of ``logits`` [T, E] (float32 or bf16) and their weights
+    (see ``ep_route``).  ``bias`` [E] float32 is added for the choice only;
+    with ``groups_per_token`` < ``groups`` a token's experts come from that
+    many groups of E / groups consecutive experts.  Returns (topk_idx int32
+    [T, k], topk_w float32 [T, k]), as ``layout`` and ``combine`` take them."""
+    if logits.dtype not in LOGIT_TYPES:
+        raise ValueError("logits must be float32 or bfloat16, got %s" % logits.dtype)
+    _check_dev("logits", logits, logits.dtype)
+    if scoring not in SCORES:
+        raise ValueError("scoring must be one of %s" % ", ".join(sorted(SCORES)))
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _check_dev("bias", bias, torch.float32, dev)
+        if tuple(bias.shape) != (E,):
+            raise ValueError("bias must be [E]")
+    if topk_idx is None:
+        topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+    for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32)):
+        _check_dev(name, t, dt, dev)
+        if tuple(t.shape) != (T, k):
+            raise ValueError("%s must be [T, k]" % name)
+    _rc("ep_route", _on_current(
+        dev, load().ep_route, logits.data_ptr(), LOGIT_TYPES[logits.dtype],
+        None if bias is None else bias.data_ptr(), T, E, k, groups,
+        groups if groups_per_token is None else groups_per_token, SCORES[scoring],
+        1 if renormalize else 0, scale, topk_idx.data_ptr(), topk_w.data_ptr(),
+        None if status is None else status.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+    return topk_idx, topk_w
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_group_gemm(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, kind):
+    """Types, devices and shapes of an expert product; returns (rows, K, E, weight rows)."""
+    _check_dev("a_q", a_q, torch.uint8)
+    dev = a_q.device
+    _check_dev("a_scale", a_scale, torch.float32, dev)
+    _check_dev("w_q", w_q, torch.uint8, dev)
+    _check_dev("w_scale", w_scale, torch.float32, dev)
+    _check_dev("expert_counts", expert_counts, torch.int32, dev)
+    if expert_offsets is not None:
+        _check_dev("expert_offsets", expert_offsets, torch.int32, dev)
+    if kind not in LAYOUT_KINDS:
+        raise ValueError("kind must be one of %s" % ", ".join(sorted(LAYOUT_KINDS)))
+    if a_q.dim() != 2 or w_q.dim() != 3:
+        raise ValueError("a_q must be [rows, K] and w_q [E, N, K]")
+    rows, K = a_q.shape
+    E, n, wk = w_q.shape
+    if wk != K:
+        raise ValueError("a_q has %d channels, w_q %d" % (K, wk))
+    if tuple(a_scale.shape) != (rows, K // 128):
+        raise ValueError("a_scale must be [rows, K/128]")
+    if tuple(w_scale.shape) != (E, (n + 127) // 128, K // 128):
+        raise ValueError("w_scale must be [E, ceil(N/128), K/128]")
+    if expert_counts.numel() < E or (expert_offsets is not None and expert_offsets.numel() < E):
+        raise ValueError("expert_counts and expert_offsets need an entry per expert")
+    return rows, K, E, n
+
+
+def group_gemm_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, kind="contiguous",
+                   capacity=0, out=None, status=None):
+    """Product of every expert's rows of the dispatched FP8 buffer ``a_q`` [rows, K]
+    (``a_scale`` [rows, K/128]) with its weight ``w_q`` [E, N, K] (``w_scale``
+    [E, ceil(N/128), K/128]) into ``out`` [rows, N] bf16 (see
+    ``ep_group_gemm_fp8``).  Counts and offsets are the layout's; rows that
+    belong to no expert keep what ``out`` held."""
+    rows, K, E, N = _check_group_gemm(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, kind)
+    dev = a_q.device
+    if out is None:
+        out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
+    _check_dev("out", out, torch.bfloat16, dev)
+    if tuple(out.shape) != (rows, N):
+        raise ValueError("out must be [rows, N]")
+    _rc("ep_group_gemm_fp8", _on_current(
+        dev, load().ep_group_gemm_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K, w_q.data_ptr(),
+        w_scale.data_ptr(), N, E, expert_counts.data_ptr(), _addr(expert_offsets),
+        LAYOUT_KINDS[kind], capacity, out.data_ptr(), _addr(status),
+        torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets,
+                          kind="contiguous", capacity=0, out_q=None, out_scale=None, status=None):
+    """First product of gated experts with SwiGLU and the FP8 cast in its
+    epilogue (see ``ep_group_gemm_swiglu_fp8``): ``w_q`` [E, 2I, K] holds the
+    gate rows, then the up rows.  Returns (out_q uint8 [rows, I], out_scale
+    float32 [rows, I/128]), the input of a ``group_gemm_fp8``."""
+    rows, K, E, n = _check_group_gemm(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, kind)
+    dev = a_q.device
+    if n % 2 != 0:
+        raise ValueError("w_q must hold as many gate as up rows")
+    inner = n // 2
+    if out_q is None:
+        out_q = torch.empty(rows, inner, dtype=torch.uint8, device=dev)
+    if out_scale is None:
+        out_scale = torch.empty(rows, inner // 128, dtype=torch.float32, device=dev)
+    _check_dev("out_q", out_q, torch.uint8, dev)
+    _check_dev("out_scale", out_scale, torch.float32, dev)
+    if tuple(out_q.shape) != (rows, inner) or tuple(out_scale.shape) != (rows, inner // 128):
+        raise ValueError("out_q must be [rows, I] and out_scale [rows, I/128]")
+    _rc("ep_group_gemm_swiglu_fp8", _on_current(
+        dev, load().ep_group_gemm_swiglu_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K,
+        w_q.data_ptr(), w_scale.data_ptr(), inner, E, expert_counts.data_ptr(),
+        _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, out_q.data_ptr(), out_scale.data_ptr(),
+        _addr(status), torch.cuda.current_stream(dev).cuda_stream))
+    return out_q, out_scale
+
+
 def status_read(status):
     """Synchronise the current stream and return the device status word."""
     flags = ctypes.c_uint32(0)
@@ -512,6 +641,9 @@ ep_layout_static_ws = layout_static_ws
 ep_dispatch = dispatch
 ep_dispatch_fp8 = dispatch_fp8
 ep_combine = combine
+ep_route = route
+ep_group_gemm_fp8 = group_gemm_fp8
+ep_group_gemm_swiglu_fp8 = group_gemm_swiglu_fp8
 ep_rank_layout = rank_layout
 ep_expand = expand
 ep_expand_fp8 = expand_fp8

@@ -181,6 +181,71 @@ int ep_dispatch_fp8(const void* x, int64_t T, int64_t H, int k, const int32_t* d
 
 namespace {
 
+// Common checks of the two expert products; `w_rows` is N, or 2 * N for the
+// SwiGLU form.
+int check_group_gemm_args(const uint8_t* a_q, const float* a_scale, int64_t rows, int64_t K,
+                          const uint8_t* w_q, const float* w_scale, int64_t N, int64_t w_rows,
+                          int E, const int32_t* expert_counts, const int32_t* expert_offsets,
+                          int kind, int capacity, const uint32_t* status) {
+    if (rows < 0 || rows > (int64_t)INT32_MAX || K <= 0 || N <= 0 || E < 1 || E > EP_MAX_EXPERTS)
+        return EP_ERR_INVALID_ARG;
+    if (K > (int64_t)INT32_MAX || N > (int64_t)INT32_MAX / 2 || w_rows > (int64_t)INT32_MAX / E)
+        return EP_ERR_INVALID_ARG;
+    if (kind != EP_LAYOUT_CONTIGUOUS && kind != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
+    if (kind == EP_LAYOUT_MASKED && (capacity < 0 || (int64_t)E * capacity > rows))
+        return EP_ERR_INVALID_ARG;
+    if (K % 128 != 0) return EP_ERR_ALIGNMENT;
+    if (!expert_counts || !w_q || !w_scale) return EP_ERR_INVALID_ARG;
+    if (kind == EP_LAYOUT_CONTIGUOUS && !expert_offsets) return EP_ERR_INVALID_ARG;
+    if (rows > 0 && (!a_q || !a_scale)) return EP_ERR_INVALID_ARG;
+    if (!aligned(a_q, 16) || !aligned(w_q, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(expert_counts, 4) || !aligned(expert_offsets, 4) || !aligned(status, 4))
+        return EP_ERR_ALIGNMENT;
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ep_group_gemm_fp8(const uint8_t* a_q, const float* a_scale, int64_t rows, int64_t K,
+                      const uint8_t* w_q, const float* w_scale, int64_t N, int E,
+                      const int32_t* expert_counts, const int32_t* expert_offsets, int kind,
+                      int capacity, void* out, uint32_t* status, void* stream) {
+    const int rc = check_group_gemm_args(a_q, a_scale, rows, K, w_q, w_scale, N, N, E,
+                                         expert_counts, expert_offsets, kind, capacity, status);
+    if (rc != EP_OK) return rc;
+    if (N % 8 != 0) return EP_ERR_ALIGNMENT;
+    if (rows == 0) return EP_OK;
+    if (!out) return EP_ERR_INVALID_ARG;
+    if (!aligned(out, 16)) return EP_ERR_ALIGNMENT;
+    return cuda_status(ep::launch_group_gemm(a_q, a_scale, rows, K, w_q, w_scale, N, E,
+                                             expert_counts, expert_offsets, kind, capacity, out,
+                                             nullptr, nullptr, status, as_stream(stream)));
+}
+
+int ep_group_gemm_swiglu_fp8(const uint8_t* a_q, const float* a_scale, int64_t rows, int64_t K,
+                             const uint8_t* w_q, const float* w_scale, int64_t I, int E,
+                             const int32_t* expert_counts, const int32_t* expert_offsets,
+                             int kind, int capacity, uint8_t* out_q, float* out_scale,
+                             uint32_t* status, void* stream) {
+    const int rc = check_group_gemm_args(a_q, a_scale, rows, K, w_q, w_scale, I, 2 * I, E,
+                                         expert_counts, expert_offsets, kind, capacity, status);
+    if (rc != EP_OK) return rc;
+    if (I % 128 != 0) return EP_ERR_ALIGNMENT;
+    if (rows == 0) return EP_OK;
+    if (!out_q || !out_scale) return EP_ERR_INVALID_ARG;
+    if (!aligned(out_q, 16) || !aligned(out_scale, 4)) return EP_ERR_ALIGNMENT;
+    return cuda_status(ep::launch_group_gemm(a_q, a_scale, rows, K, w_q, w_scale, I, E,
+                                             expert_counts, expert_offsets, kind, capacity,
+                                             nullptr, out_q, out_scale, status,
+                                             as_stream(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
 // ep_layout then ep_dispatch (fp8: ep_dispatch_fp8) on one status word, as a
 // single launch when the fused kernel covers the shape.
 int layout_dispatch_checked(bool fp8, const int32_t* topk_idx, int64_t T, int k, int E, int R,
@@ -269,6 +334,28 @@ int ep_combine_fp8(const uint8_t* y_q, const float* y_scale, const float* topk_w
         return EP_ERR_ALIGNMENT;
     return cuda_status(ep::launch_combine_fp8(y_q, y_scale, topk_w, dst_row, T, H, k, rows, out,
                                               status, as_stream(stream)));
+}
+
+int ep_route(const void* logits, int logits_type, const float* bias, int64_t T, int E, int k,
+             int groups, int groups_per_token, int scoring, int renormalize, float scale,
+             int32_t* topk_idx, float* topk_w, uint32_t* status, void* stream) {
+    if (T < 0 || E < 1 || E > EP_MAX_EXPERTS || k < 1 || k > EP_MAX_TOPK || k > E ||
+        T > (int64_t)INT32_MAX / k)
+        return EP_ERR_INVALID_ARG;
+    if (groups < 1 || groups > EP_MAX_GROUPS || E % groups != 0 || groups_per_token < 1 ||
+        groups_per_token > groups)
+        return EP_ERR_INVALID_ARG;
+    if ((logits_type != EP_TYPE_F32 && logits_type != EP_TYPE_BF16) ||
+        (scoring != EP_SCORE_SOFTMAX && scoring != EP_SCORE_SIGMOID))
+        return EP_ERR_INVALID_ARG;
+    if (T == 0) return EP_OK;
+    if (!logits || !topk_idx || !topk_w) return EP_ERR_INVALID_ARG;
+    if (!aligned(logits, logits_type == EP_TYPE_F32 ? 4 : 2) || !aligned(bias, 4) ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(status, 4))
+        return EP_ERR_ALIGNMENT;
+    return cuda_status(ep::launch_route(logits, logits_type, bias, T, E, k, groups,
+                                        groups_per_token, scoring, renormalize, scale, topk_idx,
+                                        topk_w, status, as_stream(stream)));
 }
 
 size_t ep_rank_layout_workspace_bytes(int64_t T, int k, int E, int R) {

@@ -65,6 +65,7 @@ extern "C" {
 
 #define EP_MAX_TOPK 32
 #define EP_MAX_EXPERTS 1024
+#define EP_MAX_GROUPS 32       /* groups of experts that ep_route() can choose among */
 #define EP_STATIC_WS_BYTES (2u << 20) /* scratch held by ep_layout_static_ws() */
 
 typedef enum {
@@ -82,10 +83,14 @@ enum {
     EP_FLAG_BAD_ROW = 4u,    /* dispatch/combine: dst_row outside [-1, rows): skipped */
     EP_FLAG_TIMEOUT = 8u     /* layout: a block of the one-launch cluster layout waited
                                 over a second for the others' totals and gave up; the
-                                outputs are incomplete (not expected on a working GPU) */
+                                outputs are incomplete (not expected on a working GPU) */,
+    EP_FLAG_BAD_LOGIT = 16u  /* ep_route: a logit (or logit + bias) is NaN: that expert
+                                was passed over */
 };
 
 typedef enum { EP_LAYOUT_CONTIGUOUS = 0, EP_LAYOUT_MASKED = 1 } ep_layout_kind_t;
+typedef enum { EP_TYPE_F32 = 0, EP_TYPE_BF16 = 1 } ep_type_t;           /* of ep_route's logits */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t; /* of ep_route's weights */
 
 /* Library version, (major << 16) | minor. */
 EP_API int ep_version(void);
@@ -100,6 +105,41 @@ EP_API int ep_last_cuda_error(void);
 /* Bytes of device workspace ep_layout() needs for these sizes (0 when T == 0).
  * with_rank_counts: non-zero if rank_token_counts will be requested. */
 EP_API size_t ep_layout_workspace_bytes(int64_t T, int k, int E, int R, int with_rank_counts);
+
+/*
+ * ep_route -- the router's choice: the exact top-k route and weights that the
+ * calls below take (PR #1238 "What changed": BF16 input with an exact top-k
+ * route and weights).  For each token:
+ *     key[e] = fl32(logits[t, e] + bias[e])    (bias: for the choice only)
+ *   - An expert whose key is NaN (EP_FLAG_BAD_LOGIT) or -inf is not eligible.
+ *   - groups_per_token < groups: only the experts of the groups_per_token
+ *     groups with the largest best key stay eligible, ties to the lower
+ *     group; group g is experts [g*E/groups, (g+1)*E/groups), so groups = R
+ *     limits a token to that many virtual ranks.
+ *   - topk_idx[t, :] = the k eligible experts with the largest keys, in
+ *     decreasing order, ties to the lower id.  Places left over when fewer
+ *     than k are eligible hold id -1 and weight 0.
+ *   - topk_w[t, j], from the chosen experts' logits l_j without the bias:
+ *       SOFTMAX, renormalize:  exp(l_j) / sum of exp(l) over the chosen
+ *       SOFTMAX:               exp(l_j) / sum of exp(l) over all E experts
+ *                              whose logit is not NaN
+ *       SIGMOID, renormalize:  sigmoid(l_j) / sum over the chosen (0 if the
+ *                              sum is 0)
+ *       SIGMOID:               sigmoid(l_j)
+ *     times `scale`; computed in fp32, with the largest logit subtracted
+ *     first in a softmax (several logits of +inf share it equally).
+ *
+ *  logits    [T, E] float32 or bf16 (logits_type), row-major, aligned to the type.
+ *  bias      [E] float32 or NULL.
+ *  topk_idx  [T, k] int32 out;  topk_w  [T, k] float32 out.
+ *  status    NULL or the status word: bits are OR-ed into it, as by ep_dispatch
+ *            (ep_layout zeroes the word it is given).
+ * Limits: 1 <= k <= min(E, EP_MAX_TOPK), E <= EP_MAX_EXPERTS, T*k < 2^31,
+ * groups <= EP_MAX_GROUPS divides E, 1 <= groups_per_token <= groups.
+ */
+EP_API int ep_route(const void* logits, int logits_type, const float* bias, int64_t T, int E,
+                    int k, int groups, int groups_per_token, int scoring, int renormalize,
+                    float scale, int32_t* topk_idx, float* topk_w, uint32_t* status, void* stream);
 
 /*
  * ep_layout -- routing layout: per-expert counts, exclusive scan, stable slot.
@@ -258,6 +298,53 @@ EP_API int ep_layout_dispatch_fp8(const int32_t* topk_idx, int64_t T, int k, int
                                   int32_t* dst_row, int32_t* rank_token_counts, uint8_t* recv_q,
                                   float* recv_scale, int64_t rows, uint32_t* status,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ep_group_gemm_fp8 -- the experts' product over a dispatched FP8 buffer (the
+ * expert compute that stands between the PR's dispatch and combine), the
+ * input being what ep_dispatch_fp8 wrote and the output what ep_combine
+ * reads.  For row r of expert e:
+ *     out[r, n] = bf16_rne( sum over b < K/128 of
+ *                   a_scale[r, b] * w_scale[e, n/128, b]
+ *                   * sum over k in block b of e4m3(a_q[r, k]) * e4m3(w_q[e, n, k]) )
+ * Products and both sums are held in fp32; the order of the sums is fixed,
+ * so the same inputs give the same bits.
+ *
+ *  a_q       [rows, K] uint8 e4m3 codes, 16-byte aligned;  a_scale [rows, K/128] float32.
+ *  w_q       [E, N, K] uint8 e4m3 codes, 16-byte aligned, K innermost;
+ *  w_scale   [E, ceil(N/128), K/128] float32: one scale per 128 x 128 block.
+ *  expert_counts, expert_offsets, kind, capacity: the layout's, on the device.
+ *            Contiguous: expert e has rows [expert_offsets[e], expert_offsets[e]
+ *            + expert_counts[e]) (also of ep_layout_aligned).  Masked: the
+ *            first min(expert_counts[e], capacity) rows from e*capacity
+ *            (expert_offsets may be NULL; rows >= E*capacity).
+ *            A contiguous segment outside [0, rows) is cut to it and raises
+ *            EP_FLAG_BAD_ROW.  Rows of no segment are neither read nor written.
+ *  out       [rows, N] bf16, 16-byte aligned.
+ * Limits: K % 128 == 0; N % 8 == 0; rows < 2^31; E * N < 2^31.
+ */
+EP_API int ep_group_gemm_fp8(const uint8_t* a_q, const float* a_scale, int64_t rows, int64_t K,
+                             const uint8_t* w_q, const float* w_scale, int64_t N, int E,
+                             const int32_t* expert_counts, const int32_t* expert_offsets,
+                             int kind, int capacity, void* out, uint32_t* status, void* stream);
+
+/*
+ * ep_group_gemm_swiglu_fp8 -- the first product of a gated expert with its
+ * activation and the FP8 cast in the epilogue, so that its output is the
+ * input of a second ep_group_gemm_fp8.  w_q is [E, 2*I, K]: rows [0, I) of an
+ * expert are the gate, rows [I, 2*I) the up projection; w_scale is
+ * [E, 2*I/128, K/128].  With y as above (in fp32, not rounded):
+ *     h[r, i] = y[r, i] / (1 + exp(-y[r, i])) * y[r, I + i]            (fp32)
+ * and out_q [rows, I], out_scale [rows, I/128] are the cast of h per row and
+ * 128 channels, step by step that of ep_dispatch_fp8.
+ * Limits: as above, and I % 128 == 0; E * 2*I < 2^31.
+ */
+EP_API int ep_group_gemm_swiglu_fp8(const uint8_t* a_q, const float* a_scale, int64_t rows,
+                                    int64_t K, const uint8_t* w_q, const float* w_scale,
+                                    int64_t I, int E, const int32_t* expert_counts,
+                                    const int32_t* expert_offsets, int kind, int capacity,
+                                    uint8_t* out_q, float* out_scale, uint32_t* status,
+                                    void* stream);
 
 /*
  * ep_combine -- weighted top-k reduction back into token order (the combine
