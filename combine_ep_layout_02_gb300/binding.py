@@ -77,6 +77,8 @@ def load():
         "ep_route": ([P, i32, P, i64, i32, i32, i32, i32, i32, i32, ctypes.c_float, P, P, P, P], i32),
         "ep_group_gemm_fp8": ([P, P, i64, i64, P, P, i64, i32, P, P, i32, i32, P, P, P], i32),
         "ep_group_gemm_swiglu_fp8": ([P, P, i64, i64, P, P, i64, i32, P, P, i32, i32, P, P, P, P], i32),
+        "ep_moe_few_workspace_bytes": ([i64, i32, i32], sz),
+        "ep_moe_few": ([P, i64, i32, i32, P, P, P, P, P, P, i32, i32, P, P, P, sz, P], i32),
         "ep_status_read": ([P, P, P], i32),
         "ep_pipeline_create": ([i32, ctypes.POINTER(ctypes.c_void_p)], i32),
         "ep_pipeline_destroy": ([P], i32),
@@ -553,6 +555,49 @@ def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offs
     return out_q, out_scale
 
 
+MOE_FEW_MAX_TOKENS = 64
+
+
+def moe_few_workspace_bytes(T, k, inner):
+    return int(load().ep_moe_few_workspace_bytes(T, k, inner))
+
+
+def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, workspace=None, status=None):
+    """The whole expert layer for at most ``MOE_FEW_MAX_TOKENS`` tokens in two
+    kernels (see ``ep_moe_few``): ``x`` [T, H] bf16, the route ``topk_idx`` /
+    ``topk_w`` [T, k], the experts' first (``w13_q`` [E, 2I, H]) and second
+    (``w2_q`` [E, H, I]) FP8 weights with a scale per 128 x 128 block.
+    Returns out [T, H] bf16."""
+    _check_dev("x", x, torch.bfloat16)
+    dev = x.device
+    for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32),
+                        ("w13_q", w13_q, torch.uint8), ("w13_scale", w13_scale, torch.float32),
+                        ("w2_q", w2_q, torch.uint8), ("w2_scale", w2_scale, torch.float32)):
+        _check_dev(name, t, dt, dev)
+    T, H = x.shape
+    k = topk_idx.shape[1]
+    E, n, inner = w13_q.shape[0], w13_q.shape[1], w2_q.shape[2]
+    if topk_idx.shape != topk_w.shape or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx and topk_w must be [T, k]")
+    if w13_q.shape[2] != H or n != 2 * inner or tuple(w2_q.shape) != (E, H, inner):
+        raise ValueError("w13_q must be [E, 2I, H] and w2_q [E, H, I]")
+    if tuple(w13_scale.shape) != (E, n // 128, H // 128) or tuple(w2_scale.shape) != (E, H // 128, inner // 128):
+        raise ValueError("w13_scale must be [E, 2I/128, H/128] and w2_scale [E, H/128, I/128]")
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _check_dev("out", out, torch.bfloat16, dev)
+    if out.shape != x.shape:
+        raise ValueError("out must be [T, H]")
+    if workspace is None:
+        workspace = torch.empty(moe_few_workspace_bytes(T, k, inner), dtype=torch.uint8, device=dev)
+    _rc("ep_moe_few", _on_current(
+        dev, load().ep_moe_few, x.data_ptr(), T, H, k, topk_idx.data_ptr(), topk_w.data_ptr(),
+        w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_scale.data_ptr(), inner, E,
+        out.data_ptr(), _addr(status), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
 def status_read(status):
     """Synchronise the current stream and return the device status word."""
     flags = ctypes.c_uint32(0)
@@ -644,6 +689,7 @@ ep_combine = combine
 ep_route = route
 ep_group_gemm_fp8 = group_gemm_fp8
 ep_group_gemm_swiglu_fp8 = group_gemm_swiglu_fp8
+ep_moe_few = moe_few
 ep_rank_layout = rank_layout
 ep_expand = expand
 ep_expand_fp8 = expand_fp8

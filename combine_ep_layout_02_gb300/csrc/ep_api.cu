@@ -358,6 +358,33 @@ int ep_route(const void* logits, int logits_type, const float* bias, int64_t T, 
                                         topk_w, status, as_stream(stream)));
 }
 
+size_t ep_moe_few_workspace_bytes(int64_t T, int k, int I) {
+    if (T <= 0 || k < 1 || I < 1) return 0;
+    return ep::moe_few_h_bytes(T, k, I) + ((size_t)T * k * (I / 128) * 4 + 255) / 256 * 256;
+}
+
+int ep_moe_few(const void* x, int64_t T, int H, int k, const int32_t* topk_idx,
+               const float* topk_w, const uint8_t* w13_q, const float* w13_scale,
+               const uint8_t* w2_q, const float* w2_scale, int I, int E, void* out,
+               uint32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || T > EP_MOE_FEW_MAX_TOKENS || H <= 0 || H > EP_MOE_FEW_MAX_WIDTH || I <= 0 ||
+        I > EP_MOE_FEW_MAX_WIDTH || k < 1 || k > EP_MAX_TOPK || E < 1 || E > EP_MAX_EXPERTS)
+        return EP_ERR_INVALID_ARG;
+    if (H % 128 != 0 || I % 128 != 0) return EP_ERR_ALIGNMENT;
+    if (T == 0) return EP_OK;
+    if (!x || !topk_idx || !topk_w || !w13_q || !w13_scale || !w2_q || !w2_scale || !out)
+        return EP_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < ep_moe_few_workspace_bytes(T, k, I))
+        return EP_ERR_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w13_q, 32) || !aligned(w2_q, 32) ||
+        !aligned(workspace, 16) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        !aligned(w13_scale, 4) || !aligned(w2_scale, 4) || !aligned(status, 4))
+        return EP_ERR_ALIGNMENT;
+    return cuda_status(ep::launch_moe_few(x, (int)T, H, k, topk_idx, topk_w, w13_q, w13_scale,
+                                          w2_q, w2_scale, I, E, out, status, workspace,
+                                          as_stream(stream)));
+}
+
 size_t ep_rank_layout_workspace_bytes(int64_t T, int k, int E, int R) {
     if (T <= 0 || k < 1 || E < 1 || R < 1) return 0;
     return ep::rank_keys_bytes(T, k) + ep_layout_workspace_bytes(T, k, R, 1, 0);

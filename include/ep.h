@@ -65,6 +65,8 @@ extern "C" {
 
 #define EP_MAX_TOPK 32
 #define EP_MAX_EXPERTS 1024
+#define EP_MOE_FEW_MAX_TOKENS 64   /* tokens of one ep_moe_few() call */
+#define EP_MOE_FEW_MAX_WIDTH 16384 /* H and I of ep_moe_few() */
 #define EP_MAX_GROUPS 32       /* groups of experts that ep_route() can choose among */
 #define EP_STATIC_WS_BYTES (2u << 20) /* scratch held by ep_layout_static_ws() */
 
@@ -384,6 +386,39 @@ EP_API int ep_combine(const void* y, const float* topk_w, const int32_t* dst_row
 EP_API int ep_combine_fp8(const uint8_t* y_q, const float* y_scale, const float* topk_w,
                           const int32_t* dst_row, int64_t T, int64_t H, int k, int64_t rows,
                           void* out, uint32_t* status, void* stream);
+
+/*
+ * ep_moe_few -- the whole expert layer for up to EP_MOE_FEW_MAX_TOKENS tokens
+ * in two kernels (the low-latency end of the Decode-like profile, where a
+ * token's experts' weights are read for one or a few rows each): no dispatch
+ * buffer, no layout.  For token t:
+ *     x8     = the FP8 cast of x[t] (ep_dispatch_fp8's)
+ *     h8_j   = the FP8 cast of SwiGLU of the first product of expert
+ *              e = topk_idx[t, j] (ep_group_gemm_swiglu_fp8's)
+ *     y_j    = its second product (ep_group_gemm_fp8's) in fp32, not rounded
+ *     out[t] = bf16_rne( sum over j with a valid expert of topk_w[t, j] * y_j )
+ * which is the chain dispatch_fp8, group_gemm_swiglu_fp8, group_gemm_fp8,
+ * combine without the bf16 rounding of each y_j.  All sums are held in fp32
+ * in a fixed order: the same inputs give the same bits.  An id of -1 is a
+ * dropped pair; other ids outside [0, E) are skipped and raise
+ * EP_FLAG_BAD_EXPERT.  A token without a valid pair gives +0.
+ *
+ *  x          [T, H] bf16, 16-byte aligned;  topk_idx [T, k] int32;  topk_w [T, k] float32.
+ *  w13_q      [E, 2*I, H] e4m3 codes (gate rows, then up rows), 32-byte aligned;
+ *  w13_scale  [E, 2*I/128, H/128] float32.
+ *  w2_q       [E, H, I] e4m3 codes, 32-byte aligned;  w2_scale [E, H/128, I/128] float32.
+ *  out        [T, H] bf16, 16-byte aligned.
+ *  workspace  ep_moe_few_workspace_bytes(T, k, I) bytes, 16-byte aligned, no
+ *             initialisation needed.
+ *  status     NULL or the status word; bits are OR-ed into it.
+ * Limits: T <= EP_MOE_FEW_MAX_TOKENS; H, I multiples of 128, at most
+ * EP_MOE_FEW_MAX_WIDTH; k <= EP_MAX_TOPK; E <= EP_MAX_EXPERTS.
+ */
+EP_API size_t ep_moe_few_workspace_bytes(int64_t T, int k, int I);
+EP_API int ep_moe_few(const void* x, int64_t T, int H, int k, const int32_t* topk_idx,
+                      const float* topk_w, const uint8_t* w13_q, const float* w13_scale,
+                      const uint8_t* w2_q, const float* w2_scale, int I, int E, void* out,
+                      uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Two-stage (rank, then expert) form of dispatch and combine -- the shape of

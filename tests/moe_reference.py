@@ -41,13 +41,16 @@ def weights64(q, scale):
 
 
 def quantise_f32(x):
-    """The FP8 cast of bf16 or float32 rows by its fp32 definition: (codes'
-    values times nothing, as float64; scales float32)."""
+    """The FP8 cast of bf16 or float32 rows by its fp32 definition: (the codes'
+    values as float64; scales float32).  Both divisions are of two tensors:
+    with a Python number on either side torch multiplies by a reciprocal,
+    which is not the IEEE quotient."""
     f = x.float()
     b = f.view(*f.shape[:-1], -1, 128)
     a = b.abs().amax(-1).clamp_min(1e-4)
-    v = (b * (448.0 / a).unsqueeze(-1)).clamp(-448.0, 448.0)
-    return v.to(torch.float8_e4m3fn).double().view(f.shape), a / 448.0
+    c = torch.full_like(a, 448.0)
+    v = (b * (c / a).unsqueeze(-1)).clamp(-448.0, 448.0)
+    return v.to(torch.float8_e4m3fn).double().view(f.shape), a / c
 
 
 def segments(counts, offsets, kind, capacity, rows):

@@ -56,3 +56,22 @@ def test_group_gemm_argument_validation(lib, swiglu):
     assert call(status=off(2)) == 2
     if swiglu:
         assert call(scale=None) == 1 and call(scale=off(2)) == 2
+
+
+def test_moe_few_argument_validation(lib):
+    def call(x=FAKE, T=4, H=256, k=2, idx=FAKE, w=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, I=128, E=8, out=FAKE,
+             status=None, ws=FAKE, wsb=1 << 20):
+        return lib.ep_moe_few(x, T, H, k, idx, w, w13, s13, w2, s2, I, E, out, status, ws, wsb, None)
+    assert call(T=0) == 0
+    assert call(T=-1) == 1 and call(T=65) == 1
+    assert call(H=0) == 1 and call(H=16512) == 1 and call(I=0) == 1 and call(I=16512) == 1
+    assert call(k=0) == 1 and call(k=33) == 1 and call(E=0) == 1 and call(E=1025) == 1
+    assert call(H=200) == 2 and call(I=64) == 2
+    for name in ("x", "idx", "w", "w13", "s13", "w2", "s2", "out"):
+        assert call(**{name: None}) == 1, name
+    for name, n in (("x", 8), ("idx", 2), ("w", 2), ("w13", 16), ("s13", 2), ("w2", 16), ("s2", 2), ("out", 8),
+                    ("status", 2), ("ws", 8)):
+        assert call(**{name: off(n)}) == 2, name
+    need = lib.ep_moe_few_workspace_bytes(4, 2, 128)
+    assert need >= 4 * 2 * 128 + 4 * 2 * 4 and lib.ep_moe_few_workspace_bytes(0, 2, 128) == 0
+    assert call(ws=None) == 3 and call(wsb=need - 1) == 3
