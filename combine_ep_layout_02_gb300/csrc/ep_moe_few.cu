@@ -137,8 +137,6 @@ struct Stage {  // one block of weights in flight
     float s_lo, s_hi;
 };
 
-__device__ __forceinline__ float2 ldf2(const float* p) { return make_float2(p[0], p[1]); }
-
 // ---- up -------------------------------------------------------------------
 
 struct UpShared {
