@@ -9,61 +9,102 @@
 //           e4m3 cast of ep_dispatch_fp8 per row and 128 channels of h.
 //
 // A tile is 128 rows of one expert by 256 weight rows (swiglu: 128 gate rows
-// and the 128 up rows of the same channels).  The scales are fp32 and differ
-// per row and block of 128, so that the tensor core cannot apply them: it
-// makes each block's sum (four tcgen05.mma of K = 32 into one of two TMEM
-// buffers), and eight warps read that sum back, scale it and add it into
-// fp32 registers while the next block's MMAs run.  A TMEM lane is a row, so
-// the row's scale is one value per thread.
+// and the 128 up rows of the same channels).  The scales are fp32 and differ per row and block of 128, so that the tensor
+// core cannot apply them: it makes each block's sum (four tcgen05.mma of
+// K = 32 into one of two TMEM buffers), and eight warps read that sum back,
+// scale it and add it into fp32 registers while the next block's MMAs run.
+// A TMEM lane is a row, so the row's scale is one value per thread.
 //
 // One persistent block per SM: warp 0 issues the TMA loads (128-byte swizzle,
-// four stages), warp 1 the MMAs, warps 4-11 scale, add and write the output.
-// The block is launched with 168 registers a thread; the first warpgroup
-// leaves 112 of them to the other two, which need 128 for the sums alone.
+// four stages), warp 1 the MMAs, warps 2 and 3 bring the scales into shared
+// memory, and warps 4-11 scale, add and write the output.  The block is
+// launched with 168 registers a thread; the first warpgroup leaves 80 of them
+// to the other two, which need 128 for the sums alone.
 #include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kBlockK = 128;
+#ifndef GG_CHUNK
+#define GG_CHUNK 16
+#endif
+constexpr int kRowsM = 128;                     // rows of a tile
+constexpr int kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
-constexpr int kABytes = kTileM * kBlockK, kBBytes = kTileN * kBlockK;
-constexpr int kARows = 32;  // rows per TMA box of A: rows past the segment's end are not read
-constexpr int kThreads = 384;
-constexpr int kIssueRegs = 56, kAddRegs = 224;  // 128 * 56 + 256 * 224 = 384 * 168
-constexpr int kAddThreads = 256;
+constexpr int kABytes = kRowsM * kBlockK, kBBytes = kTileN * kBlockK;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kARows = 32;                      // rows per TMA box of A: rows past the segment's end are not read
+#ifndef GG_WARPS
+#define GG_WARPS 8
+#endif
+#ifndef GG_BUFS
+#define GG_BUFS 2
+#endif
+constexpr int kAddWarps = GG_WARPS;             // warps that scale and add
+constexpr int kBufs = GG_BUFS;
+constexpr int kAddThreads = kAddWarps * 32;
+constexpr int kThreads = 128 + kAddThreads;
+#ifndef GG_IR
+#define GG_IR 72
+#define GG_AR 216
+#endif
+constexpr int kIssueRegs = GG_IR, kAddRegs = GG_AR;
+constexpr int kShares = kAddWarps / 4;          // column shares of a tile
+constexpr int kCols = kTileN / kShares;         // columns of a share
+constexpr int kChunk = GG_CHUNK;                // columns per TMEM load
+constexpr int kAhead = 16;                      // blocks whose scales are brought together
 
 struct Shared {
-    alignas(8) uint64_t full[kStages], empty[kStages], sum_full[2], sum_empty[2], swap, drain;
+    alignas(8) uint64_t full[kStages], empty[kStages], sum_full[2], sum_empty[2];
+    uint64_t scale_full[2], scale_empty[2], swap, drain;
     uint32_t tmem;
     int gave_up;
-    float amax[2][kTileM];  // swiglu: the two halves' row maxima
+    // weight scales of the tile's two blocks of 128 weight rows and row scales;
+    // a row past the last lets the reader run one block ahead
+    alignas(8) float2 sw[2][kAhead + 1];
+    float sa[2][kAhead + 1][kRowsM + 1];
+    int4 tile[2];                     // the tile that each scale buffer belongs to
+    float amax[kShares][kRowsM];      // swiglu: the shares' row maxima
     int first[EP_MAX_EXPERTS], count[EP_MAX_EXPERTS];
-    int tiles[EP_MAX_EXPERTS + 1];  // exclusive scan of the experts' row tiles
+    int tiles[EP_MAX_EXPERTS + 1];    // exclusive scan of the experts' row tiles
 };
 
 struct Tile {
-    int e, n0;     // expert, first output channel
+    int e, n0;      // expert, first output channel
     int row, rows;  // first row, valid rows (1..128)
 };
 
-// Tile `i` of the sequence: a row tile's column tiles follow one another.
-__device__ __forceinline__ Tile find_tile(const Shared& sh, int E, int64_t i, int ntiles, int width) {
-    const int m = (int)(i / ntiles);
-    int lo = 0, hi = E;  // the last expert with tiles[e] <= m
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.tiles[mid] <= m) lo = mid;
-        else hi = mid;
+// The tiles of a block, one after another, as a whole warp walks them: a row
+// tile's column tiles follow one another, and the block takes every step-th.
+struct Walk {
+    uint32_t m, n;    // row tile and column tile
+    uint32_t dm, dn;  // a step, split in the same way
+    int e;            // an expert at or before the row tile's
+    __device__ Walk(uint32_t first, uint32_t step, uint32_t ntiles)
+        : m(first / ntiles), n(first % ntiles), dm(step / ntiles), dn(step % ntiles), e(0) {}
+    __device__ __forceinline__ void next(uint32_t ntiles) {
+        m += dm;
+        n += dn;
+        if (n >= ntiles) {
+            n -= ntiles;
+            ++m;
+        }
     }
-    const int r0 = (m - sh.tiles[lo]) * kTileM;
-    Tile t;
-    t.e = lo;
-    t.n0 = (int)(i % ntiles) * width;
-    t.row = sh.first[lo] + r0;
-    t.rows = min(kTileM, sh.count[lo] - r0);
-    return t;
-}
+    // Expert e has the row tiles [tiles[e], tiles[e + 1]): 32 experts at a look.
+    __device__ __forceinline__ Tile tile(const Shared& sh, int E, int width) {
+        const int lane = threadIdx.x & 31;
+        unsigned past;
+        while ((past = __ballot_sync(kFullMask, sh.tiles[min(e + 1 + lane, E)] > (int)m)) == 0) e += 32;
+        e += __ffs(past) - 1;
+        const int r0 = ((int)m - sh.tiles[e]) * kRowsM;
+        Tile t;
+        t.e = e;
+        t.n0 = (int)n * width;
+        t.row = sh.first[e] + r0;
+        t.rows = min(kRowsM, sh.count[e] - r0);
+        return t;
+    }
+};
 
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -75,10 +116,11 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                   float* __restrict__ out_scale, uint32_t* __restrict__ status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    Shared& sh = *reinterpret_cast<Shared*>(stages + kStages * (kABytes + kBBytes));
+    Shared& sh = *reinterpret_cast<Shared*>(stages + kStages * kStageBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     const uint32_t sum_full = smem_addr(sh.sum_full), sum_empty = smem_addr(sh.sum_empty);
+    const uint32_t scale_full = smem_addr(sh.scale_full), scale_empty = smem_addr(sh.scale_empty);
     const uint32_t swap = smem_addr(&sh.swap), drain = smem_addr(&sh.drain);
     volatile int* gave_up = &sh.gave_up;
 
@@ -92,7 +134,9 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sum_full + 8 * i, 1);
-            mbar_init(sum_empty + 8 * i, kAddThreads / 32);
+            mbar_init(sum_empty + 8 * i, kAddWarps);
+            mbar_init(scale_full + 8 * i, 2);
+            mbar_init(scale_empty + 8 * i, kAddWarps);
         }
         mbar_init(swap, kAddThreads);
         mbar_init(drain, 1);
@@ -113,7 +157,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
     if (warp == 0) {
         int base = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
-            const int n = e0 + lane < E ? (sh.count[e0 + lane] + kTileM - 1) / kTileM : 0;
+            const int n = e0 + lane < E ? (sh.count[e0 + lane] + kRowsM - 1) / kRowsM : 0;
             int s = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -130,176 +174,240 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
     const uint32_t tmem = sh.tmem;
     const int width = SWIGLU ? 128 : kTileN;  // output channels per tile
     const int ntiles = (N + width - 1) / width;
-    const int64_t total = (int64_t)sh.tiles[E] * ntiles;
-    const int wrows = SWIGLU ? 2 * N : N;  // weight rows per expert
+    const uint32_t total = (uint32_t)sh.tiles[E] * ntiles;  // at most an output row's tiles each
+    const int wrows = SWIGLU ? 2 * N : N;     // weight rows per expert
+    const int wblocks = (wrows + 127) / 128;  // and blocks of 128 of them
+    const uint32_t step = gridDim.x;
 
     if (warp < 4) {
-      registers_down<kIssueRegs>();
-      if (warp == 0 && lane == 0) {
-        // ---- loads
-        uint32_t it = 0;
-        bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const Tile t = find_tile(sh, E, i, ntiles, width);
-            const int boxes = (t.rows + kARows - 1) / kARows;
-            const bool second = SWIGLU || t.n0 + 128 < N;
-            const uint32_t bytes = boxes * kARows * kBlockK + (second ? kBBytes : kBBytes / 2);
-            const int w0 = t.e * wrows + t.n0, w1 = SWIGLU ? w0 + N : w0 + 128;
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (!mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, gave_up)) {
-                    ok = false;
-                    break;
+        registers_down<kIssueRegs>();
+        if (warp == 0) {
+            // ---- loads
+            uint32_t it = 0;
+            bool ok = true;
+            Walk walk(blockIdx.x, step, ntiles);
+            for (uint32_t i = blockIdx.x; i < total && ok; i += step, walk.next(ntiles)) {
+                const Tile t = walk.tile(sh, E, width);
+                const bool second = SWIGLU || t.n0 + 128 < N;  // the tile has a second 128 weight rows
+                const int boxes = (t.rows + kARows - 1) / kARows;
+                const uint32_t bytes = boxes * kARows * kBlockK + (second ? kBBytes : kBBytes / 2);
+                const int w0 = t.e * wrows + t.n0, w1 = w0 + (SWIGLU ? N : 128);
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = smem_addr(stages) + s * kStageBytes;
+                    if (elect_one()) {
+                        mbar_expect_tx(full + 8 * s, bytes);
+                        for (int j = 0; j < boxes; ++j)
+                            tma_load_2d(a + j * kARows * kBlockK, &a_map, kb * kBlockK, t.row + j * kARows,
+                                        full + 8 * s);
+                        tma_load_2d(a + kABytes, &w_map, kb * kBlockK, w0, full + 8 * s);
+                        if (second)
+                            tma_load_2d(a + kABytes + kBBytes / 2, &w_map, kb * kBlockK, w1, full + 8 * s);
+                    }
+                    __syncwarp();
                 }
-                const uint32_t a = smem_addr(stages) + s * (kABytes + kBBytes), b = a + kABytes;
-                mbar_expect_tx(full + 8 * s, bytes);
-                for (int j = 0; j < boxes; ++j)
-                    tma_load_2d(a + j * kARows * kBlockK, &a_map, kb * kBlockK, t.row + j * kARows, full + 8 * s);
-                tma_load_2d(b, &w_map, kb * kBlockK, w0, full + 8 * s);
-                if (second) tma_load_2d(b + kBBytes / 2, &w_map, kb * kBlockK, w1, full + 8 * s);
             }
-        }
-        if (!ok) {  // given up: this block's copies in flight end before it does
-            const uint64_t start = global_ns();
-            for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
-                while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) &&
-                       global_ns() - start < 1000000000ull) {
-                }
-        }
-      } else if (warp == 1 && lane == 0) {
-        // ---- MMAs
-        uint32_t it = 0;
-        bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const Tile t = find_tile(sh, E, i, ntiles, width);
-            const uint32_t instr = SWIGLU || t.n0 + 128 < N ? e4m3_instr_desc(kTileM, kTileN)
-                                                            : e4m3_instr_desc(kTileM, kTileN / 2);
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const uint32_t s = it % kStages, b = it & 1;
-                if (!mbar_wait(sum_empty + 8 * b, ((it >> 1) & 1) ^ 1, gave_up) ||
-                    !mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a = smem_addr(stages) + s * (kABytes + kBBytes);
-                const uint64_t da = operand_desc(a), db = operand_desc(a + kABytes);
+            if (!ok) {  // given up: the copies in flight end before the block does
+                const uint64_t start = global_ns();
+                for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
+                    while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) &&
+                           global_ns() - start < 1000000000ull) {
+                    }
+            }
+        } else if (warp == 1) {
+            // ---- MMAs
+            uint32_t it = 0;
+            bool ok = true;
+            const uint32_t instr = e4m3_instr_desc(kRowsM, kTileN);
+            for (uint32_t i = blockIdx.x; i < total && ok; i += step) {
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t s = it % kStages, b = it & 1;
+                    // the operands are there long before the sums have room
+                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up) ||
+                        !mbar_wait(sum_empty + 8 * b, ((it >> 1) & 1) ^ 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_addr(stages) + s * kStageBytes;
+                    const uint64_t da = operand_desc(a), db = operand_desc(a + kABytes);
+                    if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_f8(tmem + b * kTileN, da + 2 * j, db + 2 * j, instr, j > 0);
-                mma_commit(empty + 8 * s);
-                mma_commit(sum_full + 8 * b);
+                        for (int j = 0; j < 4; ++j)
+                            mma_f8(tmem + b * kTileN, da + 2 * j, db + 2 * j, instr, j > 0);
+                        mma_commit(sum_full + 8 * b);
+                        mma_commit(empty + 8 * s);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
+                if (elect_one()) mma_commit(drain);
+                __syncwarp();
+                const uint64_t start = global_ns();
+                while (!mbar_try_wait(drain, 0) && global_ns() - start < 1000000000ull) {
+                }
+            }
+        } else if (warp >= 2) {
+            // ---- scales: 16 blocks of K at a time, whole lines of each row
+            uint32_t c = 0;
+            bool ok = true;
+            const int kl = lane & 15, side = lane >> 4;
+            Walk walk(blockIdx.x, step, ntiles);
+            for (uint32_t i = blockIdx.x; i < total && ok; i += step, walk.next(ntiles)) {
+                const Tile t = walk.tile(sh, E, width);
+                const int live = t.rows;
+                const float* src = a_scale + (int64_t)(t.row) * nk;
+                const int nb = t.n0 / 128 + (side == 0 ? 0 : SWIGLU ? N / 128 : 1);
+                const float* wsrc = w_scale + ((int64_t)t.e * wblocks + min(nb, wblocks - 1)) * nk;
+                for (int k0 = 0; k0 < nk; k0 += kAhead, ++c) {
+                    const uint32_t b = c & 1;
+                    if (!mbar_wait(scale_empty + 8 * b, ((c >> 1) & 1) ^ 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    if (warp == 2 && lane == 0) sh.tile[b] = make_int4(t.e, t.n0, t.row, t.rows);
+                    const bool in = k0 + kl < nk;
+                    if (warp == 2) (side ? sh.sw[b][kl].y : sh.sw[b][kl].x) = in ? __ldg(wsrc + k0 + kl) : 0.0f;
+                    for (int r0 = 0; r0 < kRowsM && r0 < live; r0 += 32) {
+                        float v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int r = r0 + j * 4 + (warp - 2) * 2 + side;
+                            v[j] = in && r < live ? __ldg(src + (int64_t)r * nk + k0 + kl) : 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sh.sa[b][kl][r0 + j * 4 + (warp - 2) * 2 + side] = v[j];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(scale_full + 8 * b);
+                }
             }
         }
-        if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
-            mma_commit(drain);
-            const uint64_t start = global_ns();
-            while (!mbar_try_wait(drain, 0) && global_ns() - start < 1000000000ull) {
-            }
-        }
-      }
     } else {
         registers_up<kAddRegs>();
         // ---- scale, add, write
-        const int half = (warp - 4) >> 2;         // columns [128 half, +128), swiglu: 64 gate and 64 up
+        const int share = (warp - 4) >> 2;        // columns [kCols * share, +kCols), swiglu: half of them up
         const int quarter = warp & 3;             // the TMEM lanes that this warp may read
-        const int r = quarter * 32 + lane;        // row of the tile
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const int wblocks = (wrows + 127) / 128;  // blocks of 128 weight rows per expert
-        uint32_t it = 0, swaps = 0;
+        const int r = quarter * 32 + lane;        // row of the block
+        // this warp's lanes, at its share's first column
+        const uint32_t lanes =
+            tmem + ((uint32_t)(quarter * 32) << 16) + share * (SWIGLU ? kCols / 2 : kCols);
+        constexpr int kChunks = kCols / kChunk;
+        // chunk c of the share: the up half of a swiglu share lies 128 columns after its gate half
+        auto column = [](int c) { return c * kChunk + (SWIGLU && c >= kChunks / 2 ? 128 - kCols / 2 : 0); };
+        uint32_t buf = 0, parity = 0;  // the sum at hand: 8 x buffer, and its barrier's phase
+        uint32_t c16 = 0, swaps = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const Tile t = find_tile(sh, E, i, ntiles, width);
+        for (uint32_t i = blockIdx.x; i < total && ok; i += step) {
+            if (!mbar_wait(scale_full + 8 * (c16 & 1), (c16 >> 1) & 1, gave_up)) break;
+            const int4 info = sh.tile[c16 & 1];
+            const Tile t{info.x, info.y, info.z, info.w};
             const bool live = r < t.rows;
             // warps whose rows or columns all lie outside only pass the buffers on
-            const bool work = quarter * 32 < t.rows && (SWIGLU || half == 0 || t.n0 + 128 < N);
+            const bool work = quarter * 32 < t.rows && (SWIGLU || t.n0 + share * kCols < N);
             const int64_t row = t.row + r;
-            const float* sa = a_scale + (live ? row * nk : (int64_t)t.row * nk);
-            const int nb = t.n0 / 128;
-            const float* sb0 = w_scale + ((int64_t)t.e * wblocks + (SWIGLU ? nb : min(nb + half, wblocks - 1))) * nk;
-            const float* sb1 = SWIGLU ? sb0 + (int64_t)(N / 128) * nk : sb0;
-            uint64_t acc[64];
+            uint64_t acc[kCols / 2];  // pairs of columns
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0;
-            float va = __ldg(sa), v0 = __ldg(sb0), v1 = __ldg(sb1);
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                const float s0 = __fmul_rn(va, v0), s1 = SWIGLU ? __fmul_rn(va, v1) : s0;
-                if (kb + 1 < nk) {  // the next block's scales, loaded behind this one's sum
-                    va = __ldg(sa + kb + 1);
-                    v0 = __ldg(sb0 + kb + 1);
-                    if (SWIGLU) v1 = __ldg(sb1 + kb + 1);
-                }
-                const uint32_t b = it & 1;
-                if (!mbar_wait(sum_full + 8 * b, (it >> 1) & 1, gave_up)) {
+            for (int c = 0; c < kCols / 2; ++c) acc[c] = 0;
+            for (int k0 = 0; k0 < nk && ok; k0 += kAhead, ++c16) {
+                const uint32_t sbuf = c16 & 1;
+                if (k0 > 0 && !mbar_wait(scale_full + 8 * sbuf, (c16 >> 1) & 1, gave_up)) {
                     ok = false;
                     break;
                 }
-                if (work) {
-                    tc_fence_after();
-                    const uint32_t from = lanes + b * kTileN;
-                    const uint64_t p0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
-                    const uint64_t p1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
-                    auto column = [&](int c) {
-                        return from + (SWIGLU ? (c < 4 ? half * 64 + c * 16 : 128 + half * 64 + (c - 4) * 16)
-                                              : half * 128 + c * 16);
-                    };
-                    uint32_t v[2][16];
-                    tmem_load16(v[0], column(0));
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        tmem_wait16(v[c & 1]);
-                        if (c < 7) tmem_load16(v[(c + 1) & 1], column(c + 1));
-                        else tc_fence_before();
-                        if (c == 7) {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(sum_empty + 8 * b);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            fma2(acc[c * 8 + j], pack2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), c < 4 ? p0 : p1);
+                const float* pa = &sh.sa[sbuf][0][r];
+                const float2* pw = sh.sw[sbuf];
+                float va = *pa;
+                float2 w = *pw;
+                const int n = min(kAhead, nk - k0);
+#pragma unroll 1
+                for (int kc = 0; kc < n; ++kc) {
+                    const float s0 = __fmul_rn(va, SWIGLU || share * kCols < 128 ? w.x : w.y);
+                    const float s1 = SWIGLU ? __fmul_rn(va, w.y) : s0;
+                    const uint64_t p0 = pack2(s0, s0), p1 = SWIGLU ? pack2(s1, s1) : p0;
+                    pa += kRowsM + 1;
+                    ++pw;
+                    va = *pa;  // the next block's, read behind this one's sum
+                    w = *pw;
+                    if (!mbar_wait(sum_full + buf, parity, gave_up)) {
+                        ok = false;
+                        break;
                     }
-                } else if (lane == 0) {
-                    mbar_arrive(sum_empty + 8 * b);
+                    if (work) {
+                        tc_fence_after();
+                        const uint32_t from = lanes + buf * (kTileN / 8);
+                        uint32_t v[kBufs][kChunk];
+                        if (kBufs == 2) tmem_load(v[0], from);
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (kBufs == 1) tmem_load(v[0], from + column(c));
+                            tmem_wait();
+                            if (c + 1 < kChunks) {
+                                if (kBufs == 2) tmem_load(v[(c + 1) % kBufs], from + column(c + 1));
+                            } else {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(sum_empty + buf);
+                            }
+#pragma unroll
+                            for (int j = 0; j < kChunk / 2; ++j)
+                                fma2(acc[c * kChunk / 2 + j], v[c % kBufs][2 * j], v[c % kBufs][2 * j + 1],
+                                     c < kChunks / 2 ? p0 : p1);
+                        }
+                    } else if (lane == 0) {
+                        mbar_arrive(sum_empty + buf);
+                    }
+                    parity ^= buf >> 3;
+                    buf ^= 8;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scale_empty + 8 * sbuf);
             }
             if (!ok) break;
             if (!SWIGLU) {
                 if (work && live) {
-                    uint16_t* o = out + row * N + t.n0 + half * 128;
-                    const int left = N - t.n0 - half * 128;  // a multiple of 8
+                    uint16_t* o = out + row * N + t.n0 + share * kCols;
+                    const int left = N - t.n0 - share * kCols;  // a multiple of 8
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < kCols / 8; ++c) {
                         if (c * 8 < left) {
-                            const uint4 q = make_uint4(pack_bf16x2_rn(lo2(acc[4 * c]), hi2(acc[4 * c])),
-                                                       pack_bf16x2_rn(lo2(acc[4 * c + 1]), hi2(acc[4 * c + 1])),
-                                                       pack_bf16x2_rn(lo2(acc[4 * c + 2]), hi2(acc[4 * c + 2])),
-                                                       pack_bf16x2_rn(lo2(acc[4 * c + 3]), hi2(acc[4 * c + 3])));
-                            st_v4(o + c * 8, q);
+                            uint32_t q[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) q[j] = pack_bf16x2_rn(lo2(acc[4 * c + j]), hi2(acc[4 * c + j]));
+                            st_v4(o + c * 8, make_uint4(q[0], q[1], q[2], q[3]));
                         }
                     }
                 }
             } else {
-                float h[64], amax = 0.0f;
+                constexpr int kH = kCols / 2;
+                float h[kH], amax = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    h[2 * c] = swiglu(lo2(acc[c]), lo2(acc[32 + c]));
-                    h[2 * c + 1] = swiglu(hi2(acc[c]), hi2(acc[32 + c]));
+                for (int c = 0; c < kH / 2; ++c) {
+                    h[2 * c] = swiglu(lo2(acc[c]), lo2(acc[kH / 2 + c]));
+                    h[2 * c + 1] = swiglu(hi2(acc[c]), hi2(acc[kH / 2 + c]));
                     amax = fmaxf(amax, fmaxf(fabsf(h[2 * c]), fabsf(h[2 * c + 1])));
                 }
-                sh.amax[half][r] = amax;
+                sh.amax[share][r] = amax;
                 mbar_arrive(swap);
                 if (!mbar_wait(swap, swaps & 1, gave_up)) break;
                 ++swaps;
-                const float a = fmaxf(fmaxf(sh.amax[0][r], sh.amax[1][r]), 1e-4f);
-                // both halves have read the maxima before either writes the next tile's
+                float a = 1e-4f;
+#pragma unroll
+                for (int j = 0; j < kShares; ++j) a = fmaxf(a, sh.amax[j][r]);
+                // all have read the maxima before any writes the next tile's
                 mbar_arrive(swap);
                 if (!mbar_wait(swap, swaps & 1, gave_up)) break;
                 ++swaps;
                 if (live) {
                     const float inv = __fdiv_rn(448.0f, a);
-                    uint8_t* o = out_q + row * N + t.n0 + half * 64;
+                    uint8_t* o = out_q + row * N + t.n0 + share * kH;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kH / 16; ++c) {
                         uint32_t q[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -309,7 +417,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                         }
                         st_v4(o + c * 16, make_uint4(q[0], q[1], q[2], q[3]));
                     }
-                    if (half == 0) out_scale[row * (N / 128) + nb] = __fdiv_rn(a, 448.0f);
+                    if (share == 0) out_scale[row * (N / 128) + t.n0 / 128] = __fdiv_rn(a, 448.0f);
                 }
             }
         }
@@ -320,7 +428,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-constexpr size_t kSmem = 1024 + kStages * (kABytes + kBBytes) + sizeof(Shared);
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + sizeof(Shared);
 static_assert(kSmem <= 227 * 1024, "");
 
 }  // namespace
@@ -337,15 +445,15 @@ cudaError_t launch_group_gemm(const uint8_t* a_q, const float* a_scale, int64_t 
     err = byte_matrix_map(&w_map, w_q, (int64_t)E * (swiglu ? 2 * N : N), K, 128);
     if (err != cudaSuccess) return err;
     static std::atomic<int> sm_cache[64];
-    int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
-    if (sms <= 0) sms = 1;
+    const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
     static std::atomic<uint64_t> configured[2];
     auto kernel = swiglu ? group_gemm_kernel<true> : group_gemm_kernel<false>;
     err = raise_smem_limit(kernel, kSmem, configured[swiglu]);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kernel, dim3((unsigned)sms), dim3(kThreads), kSmem, stream, a_map, w_map,
-                      a_scale, w_scale, rows, (int)(K / 128), (int)N, E, counts, offsets, kind,
-                      capacity, static_cast<uint16_t*>(out), out_q, out_scale, status);
+    return launch_pdl(kernel, dim3((unsigned)(sms > 0 ? sms : 1)), dim3(kThreads), kSmem, stream,
+                      a_map, w_map, a_scale, w_scale, rows, (int)(K / 128), (int)N, E, counts,
+                      offsets, kind, capacity, static_cast<uint16_t*>(out), out_q, out_scale,
+                      status);
 }
 
 }  // namespace ep
