@@ -360,7 +360,7 @@ int ep_route(const void* logits, int logits_type, const float* bias, int64_t T, 
 
 size_t ep_moe_few_workspace_bytes(int64_t T, int k, int I) {
     if (T <= 0 || k < 1 || I < 1) return 0;
-    return ep::moe_few_h_bytes(T, k, I) + ((size_t)T * k * (I / 128) * 4 + 255) / 256 * 256;
+    return ep::moe_few_bytes(T, k, I);
 }
 
 int ep_moe_few(const void* x, int64_t T, int H, int k, const int32_t* topk_idx,

@@ -447,9 +447,8 @@ cudaError_t launch_group_gemm(const uint8_t* a_q, const float* a_scale, int64_t 
                               int capacity, void* out, uint8_t* out_q, float* out_scale,
                               uint32_t* status, cudaStream_t stream);
 
-// the whole expert layer for a few tokens; workspace: moe_few_h_bytes() of
-// codes, then T * k * I/128 scales
-size_t moe_few_h_bytes(int64_t T, int k, int I);
+// the whole expert layer for a few tokens; workspace: moe_few_bytes()
+size_t moe_few_bytes(int64_t T, int k, int I);
 cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* topk_idx,
                            const float* topk_w, const uint8_t* w13, const float* s13,
                            const uint8_t* w2, const float* s2, int I, int E, void* out,

@@ -1,42 +1,42 @@
 // ep_moe_few.cu -- the whole expert layer for a few tokens in two kernels:
 //   up    x's FP8 cast, the gate and up products of every routed expert,
-//         SwiGLU and the FP8 cast of h, per (expert, 128 columns of I)
+//         SwiGLU and the FP8 cast of h, per (expert, 128 channels of I)
 //   down  the second products and the weighted sum over a token's experts
 // for tokens whose experts' weights are nearly all read for one to eight rows
 // each, so that the time is that of streaming the weights once.
 //
-// Mathematics: each weight tile of 16 rows is the A operand of an e4m3
+// Mathematics: a tile of 16 weight rows is the A operand of an e4m3
 // mma.m16n8k32 and up to 8 of the expert's tokens are its 8 columns (a "group":
 // an expert with more tokens is several groups, whose later readings of the
-// weights come from L2).  Four MMAs make one 128-channel block, whose sum is
-// then scaled by a_scale * w_scale and added in fp32.  The order of k inside
-// a block is free as long as both operands agree on it, so that each lane
-// loads 32 consecutive bytes of two weight rows straight into its A
-// registers, and the same 32 bytes of its token into B.
+// weights come from L2).  Four MMAs make the sum of one block of 128 channels,
+// which is then scaled by a_scale * w_scale and added in fp32.  Tensor cores
+// of the fifth generation would need 128 rows by at least 8 columns per
+// instruction and a trip through TMEM per block; the work here is 2 % of what
+// mma.sync delivers, and the memory is what has to be kept busy.
 //
-// up: a tile holds 8 gate rows and the 8 up rows of the same columns, so that
-// a lane's accumulators are the gate and up values of the same h.  A block's
-// 16 warps take the 16 tiles of 128 columns; the FP8 cast of h needs only the
-// warps' maxima.  With few items the 128 columns are shared by a cluster of C
-// blocks, each splitting K over C warps per tile; the maxima meet in
-// distributed shared memory.
-// down: a block owns 16 output channels for all groups; its warps take equal
-// shares of the (group, 128-channel block) sequence, add weighted results per
-// token in shared memory of their own and the block adds the warps' sums in
-// order, so that the result never depends on timing.
-#include <cooperative_groups.h>
+// Both kernels are a ring of TMA stages in shared memory, filled by one warp
+// as far ahead as the ring reaches, across items, and emptied by the others.
+//   up: a stage is one block of K of 128 gate and 128 up rows (32 KB).  Each
+//   of 16 warps owns 8 channels: its tile is their 8 gate and 8 up rows, so
+//   that a lane's accumulators are the gate and up values of the same h, and
+//   the FP8 cast of the 128 channels needs only the warps' maxima.
+//   down: a block owns 32 output channels (16 if H is small) for all groups;
+//   a stage is 16 KB of one group's weight rows with its tokens' codes and
+//   scales.  Each warp adds its blocks' weighted results per token in shared
+//   memory of its own, and the block adds the warps' sums in order: the
+//   result never depends on timing.
+// An SM can draw more than twice its share of the memory's bandwidth, so that
+// neither kernel needs its items to divide evenly over the SMs.
 #include <stddef.h>
 
-#include "ep_internal.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
-constexpr int kCols = 8;    // tokens per group: columns of one MMA
-constexpr int kDepth = 4;   // 128-channel blocks of weights that a warp has in flight
+constexpr int kCols = 8;  // tokens per group: columns of one MMA
 constexpr int kMaxPairs = EP_MOE_FEW_MAX_TOKENS * EP_MAX_TOPK;
+constexpr int kSmemLimit = 227 * 1024;
 
 // The groups of a route, built by every block for itself.
 struct Groups {
@@ -49,11 +49,49 @@ struct Groups {
     uint16_t seen[EP_MAX_EXPERTS];
 };
 
+// Up to 32 pairs: one per lane, ranked by (expert, pair).
+__device__ void build_groups_warp(Groups& g, const int32_t* __restrict__ topk_idx, int P, int E,
+                                  uint32_t* status, bool report) {
+    const int lane = threadIdx.x & 31;
+    const int e = lane < P ? __ldg(topk_idx + lane) : -1;
+    const bool live = e >= 0 && e < E;
+    if (report) warp_flag(status, !live && e != -1, EP_FLAG_BAD_EXPERT);
+    const int key = live ? e : EP_MAX_EXPERTS;
+    int at = 0;
+    for (int q = 0; q < P; ++q) {
+        const int other = __shfl_sync(kFullMask, key, q);
+        at += other < key || (other == key && q < lane);
+    }
+    if (live) {
+        g.pair[at] = (uint16_t)lane;
+        g.seen[at] = (uint16_t)e;
+    }
+    const int n = __popc(__ballot_sync(kFullMask, live));
+    __syncwarp();
+    const int se = lane < n ? g.seen[lane] : -1;  // the lane-th pair in that order
+    const unsigned peers = __match_any_sync(kFullMask, se);
+    const int in = __popc(peers & lanemask_lt());
+    const bool head = lane < n && in % kCols == 0;
+    const unsigned heads = __ballot_sync(kFullMask, head);
+    if (head) {
+        const int grp = __popc(heads & lanemask_lt());
+        g.expert[grp] = (uint16_t)se;
+        g.first[grp] = (uint16_t)lane;
+        g.size[grp] = (uint8_t)min(kCols, __popc(peers) - in);
+    }
+    if (lane == 0) g.count = __popc(heads);
+}
+
 // Fills `g` (shared); all threads of the block call it.  One warp does the
 // work: at most 2,048 ids, 32 at a time.
 __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, int P, int E,
                              uint32_t* status, bool report) {
-    for (int e = threadIdx.x; e < E; e += kThreads) g.start[e] = g.seen[e] = 0;
+    if (P <= 32) {
+        if (threadIdx.x < 32) build_groups_warp(g, topk_idx, P, E, status, report);
+        __syncthreads();
+        return;
+    }
+    for (int e = threadIdx.x; e < E; e += blockDim.x) g.start[e] = g.seen[e] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -113,162 +151,209 @@ __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, in
 }
 
 // p += A (16 x 32, e4m3, row) * B (32 x 8, e4m3, column), fp32.
-__device__ __forceinline__ void mma_e4m3(float (&p)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_e4m3(float (&p)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(p[0]), "+f"(p[1]), "+f"(p[2]), "+f"(p[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One 128-channel block: lo / hi are a lane's 32 bytes of weight rows g and
-// g + 8, b those of its column.
-__device__ __forceinline__ void block_product(float (&p)[4], const Vec32& lo, const Vec32& hi,
-                                              const uint4& b0, const uint4& b1) {
+// Four 8 x 16-byte matrices, one row address per lane.
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// The sum of one block of 128 channels.  a_row: this lane's weight row (of
+// matrix lane / 8: rows 0-7, 8-15, and the same again), 128 bytes with TMA's
+// 128-byte swizzle (16-byte chunk c of row r at c ^ (r % 8)); b_row: the 128
+// bytes of token lane % 8.
+__device__ __forceinline__ void block_product(float (&p)[4], uint32_t a_row, uint32_t b_row) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t r = lane & 7, hi = lane >> 4, quad = lane >> 3;
+    uint32_t b[8];
+    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(b), b_row + quad * 16);
+    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(b + 4), b_row + 64 + quad * 16);
     p[0] = p[1] = p[2] = p[3] = 0.0f;
-    mma_e4m3(p, lo.lo.x, hi.lo.x, lo.lo.y, hi.lo.y, b0.x, b0.y);
-    mma_e4m3(p, lo.lo.z, hi.lo.z, lo.lo.w, hi.lo.w, b0.z, b0.w);
-    mma_e4m3(p, lo.hi.x, hi.hi.x, lo.hi.y, hi.hi.y, b1.x, b1.y);
-    mma_e4m3(p, lo.hi.z, hi.hi.z, lo.hi.w, hi.hi.w, b1.z, b1.w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t a[4];
+        load_matrices(a, a_row + (((2 * j + hi) ^ r) << 4));
+        mma_e4m3(p, a, b[2 * j], b[2 * j + 1]);
+    }
 }
 
-struct Stage {  // one block of weights in flight
-    Vec32 lo, hi;
-    float s_lo, s_hi;
+// Ring of TMA stages: the filling warp's side.
+struct Fill {
+    uint32_t full, empty, stages;  // barrier addresses, their number
+    uint32_t s = 0, phase = 1;     // phase: of `empty`, passed at once in the first round
+    uint32_t issued = 0;
+    __device__ __forceinline__ bool wait(volatile int* gave_up) { return mbar_wait(empty + 8 * s, phase, gave_up); }
+    __device__ __forceinline__ void next() {
+        ++issued;
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    // Given up: wait, for at most a second, for the copies still in flight.
+    __device__ void drain() {
+        const uint64_t start = global_ns();
+        const uint32_t n = issued < stages ? issued : stages;
+        for (uint32_t i = issued - n; i < issued; ++i)
+            while (!mbar_try_wait(full + 8 * (i % stages), (i / stages) & 1) &&
+                   global_ns() - start < 1000000000ull) {
+            }
+    }
+};
+
+// A barrier of the consuming warps that gives up like every other wait.
+struct WarpsBarrier {
+    uint32_t bar, phase = 0;
+    __device__ __forceinline__ bool sync(volatile int* gave_up) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+        const bool ok = mbar_wait(bar, phase, gave_up);
+        phase ^= 1;
+        return ok;
+    }
 };
 
 // ---- up -------------------------------------------------------------------
 
+constexpr int kUpWarps = 16;
+constexpr int kUpStage = 2 * 128 * 128;  // one block of K of 128 gate and 128 up rows
+constexpr int kUpMaxStages = 6;
+
 struct UpShared {
+    uint64_t full[kUpMaxStages], empty[kUpMaxStages], sync;
+    int gave_up;
+    float amax[2][kUpWarps][kCols];  // [item parity][warp][column]
     Groups g;
-    float amax[2][kWarps][kCols];     // [item parity][rank * tiles + tile][column]
-    alignas(16) float part[kWarps][32][4];  // partial sums of the warps that share a tile
 };
 
-static_assert(offsetof(UpShared, part) % 16 == 0 && offsetof(UpShared, amax) % 4 == 0, "");
-
-template <int C>
-__global__ void __launch_bounds__(kThreads, 1)
-few_up_kernel(const uint16_t* __restrict__ x, int T, int H, int k,
-              const int32_t* __restrict__ topk_idx, const uint8_t* __restrict__ w13,
-              const float* __restrict__ s13, int I, int E, uint8_t* __restrict__ hq,
-              float* __restrict__ hs, uint32_t* __restrict__ status) {
-    namespace cg = cooperative_groups;
-    constexpr int kTiles = kWarps / C;  // M tiles of a block: 8 columns of I each
-    extern __shared__ __align__(16) uint8_t smem[];
-    UpShared& sh = *reinterpret_cast<UpShared*>(smem);
-    const int stride = H + 16;  // 16 bytes of padding: a quarter-warp's rows meet all banks
-    uint8_t* xq = smem + (sizeof(UpShared) + 15) / 16 * 16;
-    float* xs = reinterpret_cast<float*>(xq + kCols * stride);
+__global__ void __launch_bounds__((kUpWarps + 1) * 32, 1)
+few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restrict__ x, int T,
+              int H, int k, const int32_t* __restrict__ topk_idx, const float* __restrict__ s13,
+              int I, int E, int stages, uint8_t* __restrict__ hq, float* __restrict__ hs,
+              int hs_stride, uint32_t* __restrict__ status) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* xq = ring + stages * kUpStage;
+    const int stride = H + 16;  // 16 bytes of padding: eight tokens' chunks meet all banks
+    const int held = min(T, kCols);
+    UpShared& sh = *reinterpret_cast<UpShared*>(xq + held * stride);
+    float* xs = reinterpret_cast<float*>(&sh + 1);
     const int nk = H / 128, nb = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = lane >> 2, q4 = lane & 3;
-    const int rank = C > 1 ? (int)(blockIdx.x % C) : 0;
-    const int worker = blockIdx.x / C, workers = gridDim.x / C;
-    const int tile = warp % kTiles, ks = warp / kTiles;
-
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
+    volatile int* gave_up = &sh.gave_up;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kUpWarps);
+        }
+        mbar_init(smem_addr(&sh.sync), kUpWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.gave_up = 0;
+        tma_prefetch_map(&w_map);
+    }
     pdl_wait();
     pdl_trigger();
     build_groups(sh.g, topk_idx, T * k, E, status, blockIdx.x == 0);
-    const int items = sh.g.count * nb;  // (group, block of 128 columns)
-    const int mine = worker < items ? (items - worker + workers - 1) / workers : 0;
-    const int steps = (nk + C - 1) / C;  // blocks of K per warp and item
-    const int total = mine * steps;
+    const int items = sh.g.count * nb;  // (group, block of 128 channels)
 
-    // load side
-    int l_item = worker, l_step = 0;
-    const uint8_t* l_w = nullptr;
-    const float* l_s = nullptr;
-    auto load = [&](Stage& st, int s) {
-        if (s >= total) return;
-        if (l_step == 0) {
-            const int e = sh.g.expert[l_item / nb], b = l_item % nb;
-            l_w = w13 + ((int64_t)e * 2 * I + b * 128 + (rank * kTiles + tile) * 8 + row) * H + q4 * 32;
-            l_s = s13 + ((int64_t)e * 2 * nb + b) * nk;
+    if (warp == kUpWarps) {
+        Fill fill{full, empty, (uint32_t)stages};
+        bool ok = true;
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const int gate = sh.g.expert[item / nb] * 2 * I + item % nb * 128;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!(ok = fill.wait(gave_up))) break;
+                if (elect_one()) {
+                    const uint32_t bar = full + 8 * fill.s, to = smem_addr(ring) + fill.s * kUpStage;
+                    mbar_expect_tx(bar, kUpStage);
+                    tma_load_2d(to, &w_map, kb * 128, gate, bar);
+                    tma_load_2d(to + kUpStage / 2, &w_map, kb * 128, gate + I, bar);
+                }
+                __syncwarp();
+                fill.next();
+            }
         }
-        const int kb = ks * steps + l_step;
-        if (kb < nk) {
-            st.lo = ld_stream_v8(l_w + kb * 128);
-            st.hi = ld_stream_v8(l_w + (int64_t)I * H + kb * 128);
-            st.s_lo = __ldg(l_s + kb);
-            st.s_hi = __ldg(l_s + (int64_t)nb * nk + kb);
-        }
-        if (++l_step == steps) {
-            l_step = 0;
-            l_item += workers;
-        }
-    };
-    Stage st[kDepth];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(st[d], d);
-
-    int item = worker, step = 0, have = -1;  // `have`: the group whose x is in shared memory
-    int parity = 0;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s0 = 0; s0 < total; s0 += kDepth) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (s0 + d >= total) break;  // block-uniform
-            const int grp = item / nb, n = sh.g.size[grp];
-            if (step == 0 && grp != have) {
-                __syncthreads();  // the previous group's reads are done
-                // one warp per token: the cast of ep_dispatch_fp8; unused columns are zero
-                if (warp < kCols) {
-                    const int t = warp < n ? sh.g.pair[sh.g.first[grp] + warp] / k : 0;
+        if (!ok) fill.drain();
+    } else {
+        WarpsBarrier barrier{smem_addr(&sh.sync)};
+        const int row = lane >> 2, q4 = lane & 3;
+        // matrices 0 and 2: this warp's gate rows, 1 and 3: its up rows
+        const uint32_t a_lane = smem_addr(ring) + ((lane >> 3) & 1) * (kUpStage / 2) + (warp * 8 + (lane & 7)) * 128;
+        const uint32_t b_lane = smem_addr(xq) + min(lane & 7, held - 1) * stride;
+        const float* x0 = xs + min(2 * q4, held - 1) * nk;  // the scales of this lane's two tokens
+        const float* x1 = xs + min(2 * q4 + 1, held - 1) * nk;
+        uint32_t s = 0, phase = 0, parity = 0;
+        int have = -1;  // the group whose x is in shared memory
+        bool ok = true;
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const int grp = item / nb, b = item % nb, n = sh.g.size[grp], first = sh.g.first[grp];
+            const float* sg = s13 + ((int64_t)sh.g.expert[grp] * 2 * nb + b) * nk;
+            const float* su = sg + (int64_t)nb * nk;
+            if (grp != have) {
+                if (!(ok = barrier.sync(gave_up))) break;  // the previous group's reads are done
+                // one warp per token and half of its channels: the cast of ep_dispatch_fp8
+                const int t = sh.g.pair[first + min(warp >> 1, n - 1)] / k;
+                if ((warp >> 1) < n) {
                     const uint16_t* src = x + (int64_t)t * H;
-                    for (int c0 = 0; c0 < H; c0 += 1024) {
-                        uint4 a[2], b[2];
+                    uint8_t* to = xq + (warp >> 1) * stride;
+                    for (int c0 = (warp & 1) * 1024; c0 < H; c0 += 2048) {
+                        uint4 a[2], q[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int c = c0 + u * 512 + lane * 16;
-                            a[u] = b[u] = make_uint4(0, 0, 0, 0);
-                            if (warp < n && c < H) {
+                            a[u] = q[u] = make_uint4(0, 0, 0, 0);
+                            if (c < H) {
                                 a[u] = __ldg(reinterpret_cast<const uint4*>(src + c));
-                                b[u] = __ldg(reinterpret_cast<const uint4*>(src + c + 8));
+                                q[u] = __ldg(reinterpret_cast<const uint4*>(src + c + 8));
                             }
                         }
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int c = c0 + u * 512 + lane * 16;
-                            const Fp8Group f = quantize16(a[u], b[u]);
+                            const Fp8Group f = quantize16(a[u], q[u]);
                             if (c < H) {
-                                *reinterpret_cast<uint4*>(xq + warp * stride + c) = f.q;
-                                if ((lane & 7) == 0) xs[warp * nk + (c >> 7)] = f.sf;
+                                *reinterpret_cast<uint4*>(to + c) = f.q;
+                                if ((lane & 7) == 0) xs[(warp >> 1) * nk + (c >> 7)] = f.sf;
                             }
                         }
                     }
                 }
                 have = grp;
-                __syncthreads();
+                if (!(ok = barrier.sync(gave_up))) break;
             }
-            const int kb = ks * steps + step;
-            if (kb < nk) {
-                const uint4* bp = reinterpret_cast<const uint4*>(xq + row * stride + kb * 128 + q4 * 32);
-                float p[4];
-                block_product(p, st[d].lo, st[d].hi, bp[0], bp[1]);
-                const float x0 = xs[(2 * q4) * nk + kb], x1 = xs[(2 * q4 + 1) * nk + kb];
-                acc[0] = __fmaf_rn(p[0], __fmul_rn(x0, st[d].s_lo), acc[0]);
-                acc[1] = __fmaf_rn(p[1], __fmul_rn(x1, st[d].s_lo), acc[1]);
-                acc[2] = __fmaf_rn(p[2], __fmul_rn(x0, st[d].s_hi), acc[2]);
-                acc[3] = __fmaf_rn(p[3], __fmul_rn(x1, st[d].s_hi), acc[3]);
-            }
-            load(st[d], s0 + d + kDepth);
-            if (++step < steps) continue;
-            // the item is done
-            if (C > 1) {
-                *reinterpret_cast<float4*>(sh.part[warp][lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                __syncthreads();
-                if (ks == 0) {
-#pragma unroll
-                    for (int i = 1; i < C; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(sh.part[i * kTiles + tile][lane]);
-                        acc[0] = __fadd_rn(acc[0], v.x);
-                        acc[1] = __fadd_rn(acc[1], v.y);
-                        acc[2] = __fadd_rn(acc[2], v.z);
-                        acc[3] = __fadd_rn(acc[3], v.w);
-                    }
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float vg = 0.0f, vu = 0.0f;  // the weights' scales, a block per lane
+            for (int kb = 0; kb < nk; ++kb) {
+                if (kb % 32 == 0 && kb + lane < nk) {
+                    vg = __ldg(sg + kb + lane);
+                    vu = __ldg(su + kb + lane);
                 }
+                if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
+                float p[4];
+                block_product(p, a_lane + s * kUpStage, b_lane + kb * 128);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * s);
+                if (++s == (uint32_t)stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                const float wg = __shfl_sync(kFullMask, vg, kb % 32), wu = __shfl_sync(kFullMask, vu, kb % 32);
+                const float c0 = x0[kb], c1 = x1[kb];
+                acc[0] = __fmaf_rn(p[0], __fmul_rn(c0, wg), acc[0]);
+                acc[1] = __fmaf_rn(p[1], __fmul_rn(c1, wg), acc[1]);
+                acc[2] = __fmaf_rn(p[2], __fmul_rn(c0, wu), acc[2]);
+                acc[3] = __fmaf_rn(p[3], __fmul_rn(c1, wu), acc[3]);
             }
+            if (!ok) break;
             float h[2], m[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -278,138 +363,195 @@ few_up_kernel(const uint16_t* __restrict__ x, int T, int H, int k,
                 m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], 8));
                 m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], 16));
             }
-            const int slot = rank * kTiles + tile;
-            if (ks == 0 && lane < 4) {
-                if (C == 1) {
-                    sh.amax[parity][slot][2 * lane] = m[0];
-                    sh.amax[parity][slot][2 * lane + 1] = m[1];
-                } else {
-                    for (int r = 0; r < C; ++r) {
-                        float* to = cg::this_cluster().map_shared_rank(&sh.amax[parity][slot][2 * lane], r);
-                        to[0] = m[0];
-                        to[1] = m[1];
-                    }
-                }
+            if (lane < 4) {
+                sh.amax[parity][warp][2 * lane] = m[0];
+                sh.amax[parity][warp][2 * lane + 1] = m[1];
             }
-            if (C == 1) __syncthreads();
-            else cg::this_cluster().sync();
-            if (ks == 0) {
-                const int b = item % nb;
+            if (!(ok = barrier.sync(gave_up))) break;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = 2 * q4 + i;
-                    float a = 1e-4f;
+            for (int i = 0; i < 2; ++i) {
+                const int col = 2 * q4 + i;
+                float a = 1e-4f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) a = fmaxf(a, sh.amax[parity][w][col]);
-                    if (col < n) {
-                        const int pair = sh.g.pair[sh.g.first[grp] + col];
-                        const float inv = __fdiv_rn(448.0f, a);
-                        hq[(int64_t)pair * I + b * 128 + slot * 8 + row] =
-                            (uint8_t)cvt_e4m3x2_rn_sat(__fmul_rn(h[i], inv), 0.0f);
-                        if (slot == 0 && row == 0) hs[(int64_t)pair * nb + b] = __fdiv_rn(a, 448.0f);
-                    }
+                for (int w = 0; w < kUpWarps; ++w) a = fmaxf(a, sh.amax[parity][w][col]);
+                if (col < n) {
+                    const int pair = sh.g.pair[first + col];
+                    const float inv = __fdiv_rn(448.0f, a);
+                    hq[(int64_t)pair * I + b * 128 + warp * 8 + row] =
+                        (uint8_t)cvt_e4m3x2_rn_sat(__fmul_rn(h[i], inv), 0.0f);
+                    if (warp == 0 && row == 0) hs[(int64_t)pair * hs_stride + b] = __fdiv_rn(a, 448.0f);
                 }
             }
             parity ^= 1;  // the next item's maxima go to the other buffer
-            acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-            step = 0;
-            item += workers;
         }
     }
-    // a block of a cluster must not exit while another still writes its maxima:
-    // the last item's cluster barrier came after those writes
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.gave_up && status) atomicOr(status, EP_FLAG_TIMEOUT);
 }
 
 // ---- down -----------------------------------------------------------------
 
-__global__ void __launch_bounds__(kThreads, 1)
-few_down_kernel(const uint8_t* __restrict__ hq, const float* __restrict__ hs, int T, int H, int k,
+constexpr int kDownWarps = 8;
+constexpr int kDownMaxStages = 8;
+constexpr int kDownW = 16 * 1024;                 // weight bytes of a stage: 16 MT rows, 8 / MT blocks of K
+constexpr int kScaleRow = 8;                      // floats per token of a stage
+
+template <int MT>
+struct DownStage {
+    static constexpr int kRows = 16 * MT;         // output channels
+    static constexpr int kBlocks = 8 / MT;        // blocks of K
+    static constexpr int kRow = kBlocks * 128 + 16;  // a token's codes, padded against bank conflicts
+    static constexpr int kStages = MT == 1 ? 6 : kDownMaxStages;
+    static constexpr int kBytes = (kDownW + kCols * kRow + kCols * kScaleRow * 4 + 1023) / 1024 * 1024;
+};
+
+struct DownShared {
+    uint64_t full[kDownMaxStages], empty[kDownMaxStages], sync;
+    int gave_up;
+    Groups g;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+template <int MT>
+__global__ void __launch_bounds__((kDownWarps + 1) * 32, 1)
+few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ hq,
+                const float* __restrict__ hs, int hs_stride, int T, int H, int k,
                 const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
-                const uint8_t* __restrict__ w2, const float* __restrict__ s2, int I, int E,
-                uint16_t* __restrict__ out) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Groups& g = *reinterpret_cast<Groups*>(smem);
-    // [parity][warp][token][16 channels]
-    float* slabs = reinterpret_cast<float*>(smem + (sizeof(Groups) + 15) / 16 * 16);
+                const float* __restrict__ s2, int I, int E, uint16_t* __restrict__ out,
+                uint32_t* __restrict__ status) {
+    using St = DownStage<MT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    float* slabs = reinterpret_cast<float*>(ring + St::kStages * St::kBytes);  // [warp][token][16 channels]
+    DownShared& sh = *reinterpret_cast<DownShared*>(slabs + kDownWarps * T * 16);
     const int nk = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = lane >> 2, q4 = lane & 3;
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
+    volatile int* gave_up = &sh.gave_up;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < St::kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kDownWarps);
+        }
+        mbar_init(smem_addr(&sh.sync), kDownWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.gave_up = 0;
+        tma_prefetch_map(&w_map);
+    }
     // The route and the weights are older than the up kernel, which let this
     // one start only after all earlier work had completed.
-    build_groups(g, topk_idx, T * k, E, nullptr, false);
-    const int tiles = H / 16;
-    const int mine = (int)blockIdx.x < tiles ? (tiles - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    const int units = g.count * nk;  // (group, block of K), the same for every tile
-    const int u0 = (int)((int64_t)units * warp / kWarps), u1 = (int)((int64_t)units * (warp + 1) / kWarps);
-    const int per = u1 - u0;
-    const int total = mine * per;
+    build_groups(sh.g, topk_idx, T * k, E, nullptr, false);
+    const int tiles = H / St::kRows;
+    const int per_group = (nk + St::kBlocks - 1) / St::kBlocks;  // stages
+    const int groups = sh.g.count;
 
-    int l_tile = blockIdx.x, l_u = u0, l_grp = u0 / nk, l_kb = u0 % nk;
-    auto load = [&](Stage& st, int s) {
-        if (s >= total) return;
-        const int e = g.expert[l_grp];
-        const uint8_t* w = w2 + ((int64_t)e * H + l_tile * 16 + row) * I + l_kb * 128 + q4 * 32;
-        st.lo = ld_stream_v8(w);
-        st.hi = ld_stream_v8(w + 8 * (int64_t)I);
-        st.s_lo = __ldg(s2 + ((int64_t)e * (H / 128) + l_tile / 8) * nk + l_kb);
-        ++l_u;
-        if (++l_kb == nk) {
-            l_kb = 0;
-            ++l_grp;
-        }
-        if (l_u == u1) {
-            l_u = u0;
-            l_grp = u0 / nk;
-            l_kb = u0 % nk;
-            l_tile += gridDim.x;
-        }
-    };
-    Stage st[kDepth];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(st[d], d);
-    const int slab_n = T * 16;
-    for (int i = threadIdx.x; i < 2 * kWarps * slab_n; i += kThreads) slabs[i] = 0.0f;
-    __syncthreads();
-    pdl_wait();
-    pdl_trigger();
-
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int s = 0;
-    for (int i = 0; i < mine; ++i) {
-        const int tile = blockIdx.x + i * gridDim.x;
-        float* slab = slabs + ((i & 1) * kWarps + warp) * slab_n;
-        int grp = u0 / nk, kb = u0 % nk;
-        for (int u = u0; u < u1; u += 1, ++s) {
-            const int n = g.size[grp], first = g.first[grp];
-            uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-            if (row < n) {
-                const uint4* bp = reinterpret_cast<const uint4*>(
-                    hq + (int64_t)g.pair[first + row] * I + kb * 128 + q4 * 32);
-                b0 = bp[0];
-                b1 = bp[1];
+    if (warp == kDownWarps) {
+        Fill fill{full, empty, (uint32_t)St::kStages};
+        // a stage's tokens: their codes and scales, one lane each
+        auto load_tokens = [&](uint32_t s, int grp, int b0) {
+            if (lane < sh.g.size[grp]) {
+                const int pair = sh.g.pair[sh.g.first[grp] + lane];
+                const uint32_t to = smem_addr(ring) + s * St::kBytes + kDownW, bar = full + 8 * s;
+                const int blocks = min(St::kBlocks, nk - b0);
+                bulk_load(to + lane * St::kRow, hq + (int64_t)pair * I + b0 * 128, blocks * 128, bar);
+                bulk_load(to + kCols * St::kRow + lane * kScaleRow * 4, hs + (int64_t)pair * hs_stride + b0,
+                          St::kBlocks * 4, bar);
             }
-            float x0 = 0.0f, x1 = 0.0f;
-            if (2 * q4 < n) x0 = hs[(int64_t)g.pair[first + 2 * q4] * nk + kb];
-            if (2 * q4 + 1 < n) x1 = hs[(int64_t)g.pair[first + 2 * q4 + 1] * nk + kb];
-            Stage cur;
-#pragma unroll
-            for (int d = 0; d < kDepth; ++d)
-                if (s % kDepth == d) {
-                    cur = st[d];
-                    load(st[d], s + kDepth);
+        };
+        bool ok = true, up_done = false;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int grp = 0; grp < groups && ok; ++grp) {
+                const int n = sh.g.size[grp];
+                const int wrow = sh.g.expert[grp] * H + tile * St::kRows;
+                for (int j = 0; j < per_group; ++j) {
+                    if (!up_done && fill.issued == St::kStages) {
+                        // the first round's weights are on their way: now h
+                        pdl_wait();
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                        for (uint32_t i = 0; i < St::kStages; ++i)
+                            load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * St::kBlocks);
+                        up_done = true;
+                    }
+                    if (!(ok = fill.wait(gave_up))) break;
+                    const int b0 = j * St::kBlocks;
+                    if (elect_one()) {
+                        const uint32_t bar = full + 8 * fill.s;
+                        mbar_expect_tx(bar, kDownW + n * (min(St::kBlocks, nk - b0) * 128 + St::kBlocks * 4));
+                        tma_load_3d(smem_addr(ring) + fill.s * St::kBytes, &w_map, 0, wrow, b0, bar);
+                    }
+                    __syncwarp();
+                    if (up_done) load_tokens(fill.s, grp, b0);
+                    fill.next();
                 }
-            float p[4];
-            block_product(p, cur.lo, cur.hi, b0, b1);
-            acc[0] = __fmaf_rn(p[0], __fmul_rn(x0, cur.s_lo), acc[0]);
-            acc[1] = __fmaf_rn(p[1], __fmul_rn(x1, cur.s_lo), acc[1]);
-            acc[2] = __fmaf_rn(p[2], __fmul_rn(x0, cur.s_lo), acc[2]);
-            acc[3] = __fmaf_rn(p[3], __fmul_rn(x1, cur.s_lo), acc[3]);
-            if (++kb == nk || u + 1 == u1) {
-                // this warp's share of the group: weight it into its tokens, one
-                // column after another (a token may hold an expert twice)
+            }
+        }
+        if (!up_done) {
+            pdl_wait();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            for (uint32_t i = 0; i < fill.issued; ++i)
+                load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * St::kBlocks);
+        }
+        if (!ok) fill.drain();
+    } else {
+        const int slab_n = T * 16;
+        for (int i = threadIdx.x; i < kDownWarps * slab_n; i += kDownWarps * 32) slabs[i] = 0.0f;
+        pdl_wait();
+        WarpsBarrier barrier{smem_addr(&sh.sync)};
+        const int row = lane >> 2, q4 = lane & 3;
+        const int m = warp % MT, q = warp / MT;  // rows 16 m of the tile, block q of a stage
+        const uint32_t a_lane = smem_addr(ring) + q * St::kRows * 128 + (m * 16 + (lane & 15)) * 128;
+        const uint32_t b_lane = smem_addr(ring) + kDownW + (lane & 7) * St::kRow + q * 128;
+        const uint8_t* c_base = ring + kDownW + kCols * St::kRow + q * 4;  // scales
+        float* slab = slabs + warp * slab_n;
+        uint32_t s = 0, phase = 0;
+        bool ok = barrier.sync(gave_up);
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const float* ws = s2 + (int64_t)(tile * St::kRows / 128) * nk;  // of expert 0
+            const int64_t ws_step = (int64_t)(H / 128) * nk;
+            // the weights' scales, a block of K per lane: this group's and the next two's
+            auto scales = [&](int grp) {
+                return grp < groups && lane < nk ? __ldg(ws + sh.g.expert[grp] * ws_step + lane) : 0.0f;
+            };
+            float w0 = scales(0), w1 = scales(1), w2 = scales(2);
+            for (int grp = 0; grp < groups && ok; ++grp) {
+                const int n = sh.g.size[grp], first = sh.g.first[grp];
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int j = 0; j < per_group; ++j) {
+                    const int kb = j * St::kBlocks + q;
+                    if (kb >= 32 && kb - q == (kb - q) / 32 * 32)  // beyond the 32 blocks at hand
+                        w0 = kb - q + lane < nk ? __ldg(ws + sh.g.expert[grp] * ws_step + kb - q + lane) : 0.0f;
+                    if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
+                    const float w = __shfl_sync(kFullMask, w0, kb % 32);
+                    if (kb < nk) {
+                        float p[4];
+                        block_product(p, a_lane + s * St::kBytes, b_lane + s * St::kBytes);
+                        const uint8_t* c = c_base + s * St::kBytes;
+                        const float c0 = __fmul_rn(*reinterpret_cast<const float*>(c + 2 * q4 * kScaleRow * 4), w);
+                        const float c1 = __fmul_rn(*reinterpret_cast<const float*>(c + (2 * q4 + 1) * kScaleRow * 4), w);
+                        acc[0] = __fmaf_rn(p[0], c0, acc[0]);
+                        acc[1] = __fmaf_rn(p[1], c1, acc[1]);
+                        acc[2] = __fmaf_rn(p[2], c0, acc[2]);
+                        acc[3] = __fmaf_rn(p[3], c1, acc[3]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + 8 * s);
+                    if (++s == St::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                // weight this warp's share into its tokens, one column after
+                // another (a token may hold an expert twice)
                 for (int c = 0; c < n; ++c) {
                     if (c / 2 == q4) {
-                        const int pair = g.pair[first + c];
+                        const int pair = sh.g.pair[first + c];
                         const float wt = __ldg(topk_w + pair);
                         float* o = slab + pair / k * 16 + row;
                         o[0] = __fmaf_rn(wt, acc[c & 1], o[0]);
@@ -417,61 +559,57 @@ few_down_kernel(const uint8_t* __restrict__ hq, const float* __restrict__ hs, in
                     }
                     __syncwarp();
                 }
-                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                kb = 0;
-                ++grp;
+                w0 = w1;
+                w1 = w2;
+                w2 = scales(grp + 3);
             }
-        }
-        __syncthreads();
-        // add the warps' sums in order, clear them for the tile after the next
-        float* all = slabs + (i & 1) * kWarps * slab_n;
-        for (int v = threadIdx.x; v < slab_n / 2; v += kThreads) {
-            float a = 0.0f, b = 0.0f;
-            for (int w = 0; w < kWarps; ++w) {
-                float2* p2 = reinterpret_cast<float2*>(all + w * slab_n) + v;
-                const float2 f = *p2;
-                a = __fadd_rn(a, f.x);
-                b = __fadd_rn(b, f.y);
-                *p2 = make_float2(0.0f, 0.0f);
+            if (!ok || !(ok = barrier.sync(gave_up))) break;
+            // add the warps' sums in order and clear them
+            for (int v = threadIdx.x; v < MT * slab_n / 2; v += kDownWarps * 32) {
+                const int t = v / (8 * MT), ch = v % (8 * MT) * 2;  // token, channel of the tile
+                float a = 0.0f, b = 0.0f;
+#pragma unroll
+                for (int w = ch / 16; w < kDownWarps; w += MT) {
+                    float2* p2 = reinterpret_cast<float2*>(slabs + w * slab_n + t * 16 + ch % 16);
+                    a = __fadd_rn(a, p2->x);
+                    b = __fadd_rn(b, p2->y);
+                    *p2 = make_float2(0.0f, 0.0f);
+                }
+                *reinterpret_cast<uint32_t*>(out + (int64_t)t * H + tile * St::kRows + ch) = pack_bf16x2_rn(a, b);
             }
-            const int t = v / 8, c = v % 8 * 2;
-            *reinterpret_cast<uint32_t*>(out + (int64_t)t * H + tile * 16 + c) = pack_bf16x2_rn(a, b);
+            ok = barrier.sync(gave_up);
         }
-        // the slabs of this parity are next touched two tiles on, after another barrier
     }
+    pdl_trigger();
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.gave_up && status) atomicOr(status, EP_FLAG_TIMEOUT);
 }
 
-size_t up_smem(int H) {
-    return (sizeof(UpShared) + 15) / 16 * 16 + (size_t)kCols * (H + 16) + (size_t)kCols * (H / 128) * 4;
+size_t up_rest(int T, int H) {  // shared memory besides the ring
+    const int held = T < kCols ? T : kCols;
+    return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4;
 }
-size_t down_smem(int T) { return (sizeof(Groups) + 15) / 16 * 16 + (size_t)2 * kWarps * T * 16 * 4; }
+template <int MT>
+size_t down_smem(int T) {
+    return 1024 + (size_t)DownStage<MT>::kStages * DownStage<MT>::kBytes + (size_t)kDownWarps * T * 16 * 4 + sizeof(DownShared);
+}
+static_assert(1024 + kCols * (EP_MOE_FEW_MAX_WIDTH + 16) + sizeof(UpShared) +
+                      kCols * (EP_MOE_FEW_MAX_WIDTH / 128) * 4 + 2 * kUpStage <= kSmemLimit,
+              "at least two stages at the widest");
+static_assert(1024 + DownStage<1>::kStages * DownStage<1>::kBytes + kDownWarps * EP_MOE_FEW_MAX_TOKENS * 64 + sizeof(DownShared) <=
+                  kSmemLimit, "");
+static_assert(1024 + DownStage<2>::kStages * DownStage<2>::kBytes + kDownWarps * EP_MOE_FEW_MAX_TOKENS * 64 + sizeof(DownShared) <=
+                  kSmemLimit, "");
 
-template <int C>
-cudaError_t launch_up(int blocks, const void* x, int T, int H, int k, const int32_t* topk_idx,
-                      const uint8_t* w13, const float* s13, int I, int E, uint8_t* hq, float* hs,
-                      uint32_t* status, cudaStream_t stream) {
-    static std::atomic<uint64_t> configured{0};
-    cudaError_t err = raise_smem_limit(few_up_kernel<C>, up_smem(EP_MOE_FEW_MAX_WIDTH), configured);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = up_smem(H);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {C, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, few_up_kernel<C>, static_cast<const uint16_t*>(x), T, H, k,
-                              topk_idx, w13, s13, I, E, hq, hs, status);
-}
+int hs_stride_of(int I) { return (I / 128 + 7) / 8 * 8; }  // a stage's scales are copied as whole 32 bytes
 
 }  // namespace
 
 size_t moe_few_h_bytes(int64_t T, int k, int I) { return ((size_t)T * k * I + 255) / 256 * 256; }
+size_t moe_few_bytes(int64_t T, int k, int I) {
+    return moe_few_h_bytes(T, k, I) + ((size_t)T * k * hs_stride_of(I) * 4 + 255) / 256 * 256;
+}
 
 cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* topk_idx,
                            const float* topk_w, const uint8_t* w13, const float* s13,
@@ -483,31 +621,37 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     if (sms <= 0) sms = 1;
     uint8_t* hq = static_cast<uint8_t*>(workspace);
     float* hs = reinterpret_cast<float*>(hq + moe_few_h_bytes(T, k, I));
-    // Blocks per 128 columns: the C that leaves the fewest idle blocks in the
-    // last round of items (at most one expert per pair), 1 where equal.
-    const int64_t items = (int64_t)(T * k < E ? T * k : E) * (I / 128);
-    int C = 1;
-    double best = 1e30;
-    for (int c = 1; c <= 4; c *= 2) {
-        const double rounds = (double)((items * c + sms - 1) / sms) / c;
-        if (rounds < best * 0.999) {
-            best = rounds;
-            C = c;
-        }
-    }
-    const int blocks = (int)(items * C < sms ? items * C : sms / C * C);
-    cudaError_t err =
-        C == 1   ? launch_up<1>(blocks, x, T, H, k, topk_idx, w13, s13, I, E, hq, hs, status, stream)
-        : C == 2 ? launch_up<2>(blocks, x, T, H, k, topk_idx, w13, s13, I, E, hq, hs, status, stream)
-                 : launch_up<4>(blocks, x, T, H, k, topk_idx, w13, s13, I, E, hq, hs, status, stream);
+    const int hs_stride = hs_stride_of(I);
+
+    CUtensorMap w13_map, w2_map;
+    cudaError_t err = byte_matrix_map(&w13_map, w13, (int64_t)E * 2 * I, H, 128);
     if (err != cudaSuccess) return err;
-    static std::atomic<uint64_t> configured{0};
-    err = raise_smem_limit(few_down_kernel, down_smem(EP_MOE_FEW_MAX_TOKENS), configured);
+    static std::atomic<uint64_t> configured[3];
+    err = raise_smem_limit(few_up_kernel, kSmemLimit, configured[0]);
     if (err != cudaSuccess) return err;
-    const int tiles = H / 16;
-    return launch_pdl(few_down_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads),
-                      down_smem(T), stream, hq, hs, T, H, k, topk_idx, topk_w, w2, s2, I, E,
-                      static_cast<uint16_t*>(out));
+    const size_t rest = up_rest(T, H);
+    int stages = (int)((kSmemLimit - rest) / kUpStage);
+    if (stages > kUpMaxStages) stages = kUpMaxStages;
+    // at most one group per pair and 128 channels (an expert with more than 8
+    // tokens has as many groups as its pairs need)
+    const int64_t items = (int64_t)T * k * (I / 128);
+    err = launch_pdl(few_up_kernel, dim3((unsigned)(items < sms ? items : sms)), dim3((kUpWarps + 1) * 32),
+                     rest + (size_t)stages * kUpStage, stream, w13_map, static_cast<const uint16_t*>(x), T,
+                     H, k, topk_idx, s13, I, E, stages, hq, hs, hs_stride, status);
+    if (err != cudaSuccess) return err;
+
+    // Output channels per block: 32, or 16 where that leaves fewer than 64
+    // blocks, the number that can draw nearly the whole bandwidth.
+    const int mt = H / 32 >= 64 ? 2 : 1;
+    const int tiles = H / (16 * mt);
+    err = byte_blocks_map(&w2_map, w2, (int64_t)E * H, I, 16 * mt, 8 / mt);
+    if (err != cudaSuccess) return err;
+    auto kernel = mt == 2 ? few_down_kernel<2> : few_down_kernel<1>;
+    err = raise_smem_limit(kernel, kSmemLimit, configured[mt]);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3((kDownWarps + 1) * 32),
+                      mt == 2 ? down_smem<2>(T) : down_smem<1>(T), stream, w2_map, hq, hs, hs_stride, T,
+                      H, k, topk_idx, topk_w, s2, I, E, static_cast<uint16_t*>(out), status);
 }
 
 }  // namespace ep

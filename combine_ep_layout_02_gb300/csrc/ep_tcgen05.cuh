@@ -99,6 +99,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -221,5 +229,10 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, ui
 // box_rows x 128 bytes with the 128-byte swizzle; rows past the end read 0.
 cudaError_t byte_matrix_map(CUtensorMap* map, const void* base, int64_t rows, int64_t width,
                             int box_rows);
+
+// The same matrix as [width / 128][rows][128 bytes]: boxes of `blocks`
+// successive 128-byte columns of box_rows rows, column by column.
+cudaError_t byte_blocks_map(CUtensorMap* map, const void* base, int64_t rows, int64_t width,
+                            int box_rows, int blocks);
 
 }  // namespace ep
