@@ -20,11 +20,11 @@
 //   of 16 warps owns 8 channels: its tile is their 8 gate and 8 up rows, so
 //   that a lane's accumulators are the gate and up values of the same h, and
 //   the FP8 cast of the 128 channels needs only the warps' maxima.
-//   down: a block owns 32 output channels (16 if H is small) for all groups;
-//   a stage is 16 KB of one group's weight rows with its tokens' codes and
-//   scales.  Each warp adds its blocks' weighted results per token in shared
-//   memory of its own, and the block adds the warps' sums in order: the
-//   result never depends on timing.
+//   down: a block owns 16 output channels for all groups; a stage is eight
+//   blocks of K of one group's 16 weight rows (16 KB) with its tokens' codes
+//   and scales.  The warps take the stages in turn, each adds its weighted
+//   results per token in shared memory of its own, and the block adds the
+//   warps' sums in order: the result never depends on timing.
 // An SM can draw more than twice its share of the memory's bandwidth, so that
 // neither kernel needs its items to divide evenly over the SMs.
 #include <stddef.h>
@@ -44,6 +44,7 @@ struct Groups {
     uint16_t expert[kMaxPairs];  // per group
     uint16_t first[kMaxPairs];   // its first entry of `pair`, and their number
     uint8_t size[kMaxPairs];
+    uint8_t twice[kMaxPairs];    // whether two of its pairs belong to one token
     uint16_t pair[kMaxPairs];    // pairs t * k + j ordered by expert, then by pair
     uint16_t start[EP_MAX_EXPERTS];
     uint16_t seen[EP_MAX_EXPERTS];
@@ -82,12 +83,26 @@ __device__ void build_groups_warp(Groups& g, const int32_t* __restrict__ topk_id
     if (lane == 0) g.count = __popc(heads);
 }
 
+// Marks the groups that hold a token twice: its pairs follow one another.
+__device__ void mark_twice(Groups& g, int k) {
+    for (int i = threadIdx.x & 31; i < g.count; i += 32) {
+        bool twice = false;
+        for (int j = 1; j < g.size[i]; ++j)
+            twice |= g.pair[g.first[i] + j - 1] / k == g.pair[g.first[i] + j] / k;
+        g.twice[i] = twice;
+    }
+}
+
 // Fills `g` (shared); all threads of the block call it.  One warp does the
 // work: at most 2,048 ids, 32 at a time.
-__device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, int P, int E,
+__device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, int P, int k, int E,
                              uint32_t* status, bool report) {
     if (P <= 32) {
-        if (threadIdx.x < 32) build_groups_warp(g, topk_idx, P, E, status, report);
+        if (threadIdx.x < 32) {
+            build_groups_warp(g, topk_idx, P, E, status, report);
+            __syncwarp();
+            mark_twice(g, k);
+        }
         __syncthreads();
         return;
     }
@@ -146,6 +161,7 @@ __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, in
             }
             __syncwarp();
         }
+        mark_twice(g, k);
     }
     __syncthreads();
 }
@@ -262,7 +278,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     }
     pdl_wait();
     pdl_trigger();
-    build_groups(sh.g, topk_idx, T * k, E, status, blockIdx.x == 0);
+    build_groups(sh.g, topk_idx, T * k, k, E, status, blockIdx.x == 0);
     const int items = sh.g.count * nb;  // (group, block of 128 channels)
 
     if (warp == kUpWarps) {
@@ -392,22 +408,17 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
 
 // ---- down -----------------------------------------------------------------
 
-constexpr int kDownWarps = 8;
-constexpr int kDownMaxStages = 8;
-constexpr int kDownW = 16 * 1024;                 // weight bytes of a stage: 16 MT rows, 8 / MT blocks of K
-constexpr int kScaleRow = 8;                      // floats per token of a stage
-
-template <int MT>
-struct DownStage {
-    static constexpr int kRows = 16 * MT;         // output channels
-    static constexpr int kBlocks = 8 / MT;        // blocks of K
-    static constexpr int kRow = kBlocks * 128 + 16;  // a token's codes, padded against bank conflicts
-    static constexpr int kStages = MT == 1 ? 6 : kDownMaxStages;
-    static constexpr int kBytes = (kDownW + kCols * kRow + kCols * kScaleRow * 4 + 1023) / 1024 * 1024;
-};
+constexpr int kDownWarps = 6;
+constexpr int kDownStages = kDownWarps;           // a warp's stages always lie in the same place
+constexpr int kDownRows = 16;                     // output channels of a block
+constexpr int kDownBlocks = 8;                    // blocks of K of a stage
+constexpr int kDownW = kDownRows * kDownBlocks * 128;
+constexpr int kTokenRow = kDownBlocks * 128 + 16;  // a token's codes, padded against bank conflicts
+constexpr int kScaleRow = kDownBlocks;            // its scales
+constexpr int kDownStage = (kDownW + kCols * kTokenRow + kCols * kScaleRow * 4 + 1023) / 1024 * 1024;
 
 struct DownShared {
-    uint64_t full[kDownMaxStages], empty[kDownMaxStages], sync;
+    uint64_t full[kDownStages], empty[kDownStages], sync;
     int gave_up;
     Groups g;
 };
@@ -419,26 +430,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-template <int MT>
 __global__ void __launch_bounds__((kDownWarps + 1) * 32, 1)
 few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ hq,
                 const float* __restrict__ hs, int hs_stride, int T, int H, int k,
                 const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
                 const float* __restrict__ s2, int I, int E, uint16_t* __restrict__ out,
                 uint32_t* __restrict__ status) {
-    using St = DownStage<MT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    float* slabs = reinterpret_cast<float*>(ring + St::kStages * St::kBytes);  // [warp][token][16 channels]
-    DownShared& sh = *reinterpret_cast<DownShared*>(slabs + kDownWarps * T * 16);
+    float* slabs = reinterpret_cast<float*>(ring + kDownStages * kDownStage);  // [warp][token][16 channels]
+    DownShared& sh = *reinterpret_cast<DownShared*>(slabs + kDownWarps * T * kDownRows);
     const int nk = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     volatile int* gave_up = &sh.gave_up;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < St::kStages; ++i) {
+        for (int i = 0; i < kDownStages; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kDownWarps);
+            mbar_init(empty + 8 * i, 1);
         }
         mbar_init(smem_addr(&sh.sync), kDownWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -447,44 +456,46 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
     }
     // The route and the weights are older than the up kernel, which let this
     // one start only after all earlier work had completed.
-    build_groups(sh.g, topk_idx, T * k, E, nullptr, false);
-    const int tiles = H / St::kRows;
-    const int per_group = (nk + St::kBlocks - 1) / St::kBlocks;  // stages
+    build_groups(sh.g, topk_idx, T * k, k, E, nullptr, false);
+    const int tiles = H / kDownRows;
+    const int per_group = (nk + kDownBlocks - 1) / kDownBlocks;  // stages
     const int groups = sh.g.count;
 
     if (warp == kDownWarps) {
-        Fill fill{full, empty, (uint32_t)St::kStages};
+        Fill fill{full, empty, (uint32_t)kDownStages};
         // a stage's tokens: their codes and scales, one lane each
         auto load_tokens = [&](uint32_t s, int grp, int b0) {
             if (lane < sh.g.size[grp]) {
                 const int pair = sh.g.pair[sh.g.first[grp] + lane];
-                const uint32_t to = smem_addr(ring) + s * St::kBytes + kDownW, bar = full + 8 * s;
-                const int blocks = min(St::kBlocks, nk - b0);
-                bulk_load(to + lane * St::kRow, hq + (int64_t)pair * I + b0 * 128, blocks * 128, bar);
-                bulk_load(to + kCols * St::kRow + lane * kScaleRow * 4, hs + (int64_t)pair * hs_stride + b0,
-                          St::kBlocks * 4, bar);
+                const uint32_t to = smem_addr(ring) + s * kDownStage + kDownW, bar = full + 8 * s;
+                bulk_load(to + lane * kTokenRow, hq + (int64_t)pair * I + b0 * 128,
+                          min(kDownBlocks, nk - b0) * 128, bar);
+                bulk_load(to + kCols * kTokenRow + lane * kScaleRow * 4, hs + (int64_t)pair * hs_stride + b0,
+                          kScaleRow * 4, bar);
             }
+        };
+        // the first round's weights are on their way: now h
+        auto first_tokens = [&]() {
+            pdl_wait();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            for (uint32_t i = 0; i < fill.issued; ++i)
+                load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * kDownBlocks);
         };
         bool ok = true, up_done = false;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             for (int grp = 0; grp < groups && ok; ++grp) {
                 const int n = sh.g.size[grp];
-                const int wrow = sh.g.expert[grp] * H + tile * St::kRows;
-                for (int j = 0; j < per_group; ++j) {
-                    if (!up_done && fill.issued == St::kStages) {
-                        // the first round's weights are on their way: now h
-                        pdl_wait();
-                        asm volatile("fence.proxy.async.global;" ::: "memory");
-                        for (uint32_t i = 0; i < St::kStages; ++i)
-                            load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * St::kBlocks);
+                const int wrow = sh.g.expert[grp] * H + tile * kDownRows;
+                for (int b0 = 0; b0 < nk; b0 += kDownBlocks) {
+                    if (!up_done && fill.issued == kDownStages) {
+                        first_tokens();
                         up_done = true;
                     }
                     if (!(ok = fill.wait(gave_up))) break;
-                    const int b0 = j * St::kBlocks;
                     if (elect_one()) {
                         const uint32_t bar = full + 8 * fill.s;
-                        mbar_expect_tx(bar, kDownW + n * (min(St::kBlocks, nk - b0) * 128 + St::kBlocks * 4));
-                        tma_load_3d(smem_addr(ring) + fill.s * St::kBytes, &w_map, 0, wrow, b0, bar);
+                        mbar_expect_tx(bar, kDownW + n * (min(kDownBlocks, nk - b0) * 128 + kScaleRow * 4));
+                        tma_load_3d(smem_addr(ring) + fill.s * kDownStage, &w_map, 0, wrow, b0, bar);
                     }
                     __syncwarp();
                     if (up_done) load_tokens(fill.s, grp, b0);
@@ -492,90 +503,92 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                 }
             }
         }
-        if (!up_done) {
-            pdl_wait();
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            for (uint32_t i = 0; i < fill.issued; ++i)
-                load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * St::kBlocks);
-        }
+        if (!up_done) first_tokens();
         if (!ok) fill.drain();
     } else {
-        const int slab_n = T * 16;
+        const int slab_n = T * kDownRows;
         for (int i = threadIdx.x; i < kDownWarps * slab_n; i += kDownWarps * 32) slabs[i] = 0.0f;
         pdl_wait();
         WarpsBarrier barrier{smem_addr(&sh.sync)};
         const int row = lane >> 2, q4 = lane & 3;
-        const int m = warp % MT, q = warp / MT;  // rows 16 m of the tile, block q of a stage
-        const uint32_t a_lane = smem_addr(ring) + q * St::kRows * 128 + (m * 16 + (lane & 15)) * 128;
-        const uint32_t b_lane = smem_addr(ring) + kDownW + (lane & 7) * St::kRow + q * 128;
-        const uint8_t* c_base = ring + kDownW + kCols * St::kRow + q * 4;  // scales
+        const uint32_t a_lane = smem_addr(ring) + (lane & 15) * 128;
+        const uint32_t b_lane = smem_addr(ring) + kDownW + (lane & 7) * kTokenRow;
+        const uint8_t* c_lane = ring + kDownW + kCols * kTokenRow + 2 * q4 * kScaleRow * 4;  // two tokens' scales
         float* slab = slabs + warp * slab_n;
-        uint32_t s = 0, phase = 0;
+        const uint32_t per_tile = groups * per_group;  // stages
+        const uint32_t s = warp;
+        uint32_t base = 0, at = warp, phase = 0;  // stages before this tile; this warp's next
         bool ok = barrier.sync(gave_up);
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            const float* ws = s2 + (int64_t)(tile * St::kRows / 128) * nk;  // of expert 0
-            const int64_t ws_step = (int64_t)(H / 128) * nk;
-            // the weights' scales, a block of K per lane: this group's and the next two's
-            auto scales = [&](int grp) {
-                return grp < groups && lane < nk ? __ldg(ws + sh.g.expert[grp] * ws_step + lane) : 0.0f;
-            };
-            float w0 = scales(0), w1 = scales(1), w2 = scales(2);
-            for (int grp = 0; grp < groups && ok; ++grp) {
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, base += per_tile) {
+            const float* ws = s2 + (int64_t)(tile * kDownRows / 128) * nk;  // of expert 0
+            // this warp's stages: every sixth of the block's sequence
+            for (; at < base + per_tile; at += kDownWarps) {
+                const uint32_t u = at - base;
+                const int grp = u / per_group, b0 = u % per_group * kDownBlocks;
                 const int n = sh.g.size[grp], first = sh.g.first[grp];
+                // read behind the wait: the weights' scales, a block per lane,
+                // and the two columns' tokens and weights
+                const int b = min(b0 + (lane & 7), nk - 1);
+                const float wl = __ldg(ws + (int64_t)sh.g.expert[grp] * (H / 128) * nk + b);
+                const int pair0 = sh.g.pair[first + min(2 * q4, n - 1)], pair1 = sh.g.pair[first + min(2 * q4 + 1, n - 1)];
+                const float wt0 = __ldg(topk_w + pair0), wt1 = __ldg(topk_w + pair1);
+                if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
+                phase ^= 1;
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int j = 0; j < per_group; ++j) {
-                    const int kb = j * St::kBlocks + q;
-                    if (kb >= 32 && kb - q == (kb - q) / 32 * 32)  // beyond the 32 blocks at hand
-                        w0 = kb - q + lane < nk ? __ldg(ws + sh.g.expert[grp] * ws_step + kb - q + lane) : 0.0f;
-                    if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
-                    const float w = __shfl_sync(kFullMask, w0, kb % 32);
-                    if (kb < nk) {
+                const uint32_t a = a_lane + s * kDownStage, t = b_lane + s * kDownStage;
+                const float* c = reinterpret_cast<const float*>(c_lane + s * kDownStage);
+#pragma unroll
+                for (int j = 0; j < kDownBlocks; ++j) {
+                    if (b0 + j < nk) {  // warp-uniform
                         float p[4];
-                        block_product(p, a_lane + s * St::kBytes, b_lane + s * St::kBytes);
-                        const uint8_t* c = c_base + s * St::kBytes;
-                        const float c0 = __fmul_rn(*reinterpret_cast<const float*>(c + 2 * q4 * kScaleRow * 4), w);
-                        const float c1 = __fmul_rn(*reinterpret_cast<const float*>(c + (2 * q4 + 1) * kScaleRow * 4), w);
+                        block_product(p, a + j * kDownRows * 128, t + j * 128);
+                        const float w = __shfl_sync(kFullMask, wl, j);
+                        const float c0 = __fmul_rn(c[j], w), c1 = __fmul_rn(c[kScaleRow + j], w);
                         acc[0] = __fmaf_rn(p[0], c0, acc[0]);
                         acc[1] = __fmaf_rn(p[1], c1, acc[1]);
                         acc[2] = __fmaf_rn(p[2], c0, acc[2]);
                         acc[3] = __fmaf_rn(p[3], c1, acc[3]);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty + 8 * s);
-                    if (++s == St::kStages) {
-                        s = 0;
-                        phase ^= 1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * s);
+                float* o0 = slab + pair0 / k * kDownRows + row;
+                float* o1 = slab + pair1 / k * kDownRows + row;
+                if (!sh.g.twice[grp]) {  // every column has a token of its own
+                    if (2 * q4 < n) {
+                        o0[0] = __fmaf_rn(wt0, acc[0], o0[0]);
+                        o0[8] = __fmaf_rn(wt0, acc[2], o0[8]);
+                    }
+                    if (2 * q4 + 1 < n) {
+                        o1[0] = __fmaf_rn(wt1, acc[1], o1[0]);
+                        o1[8] = __fmaf_rn(wt1, acc[3], o1[8]);
+                    }
+                } else {  // one column after another
+                    for (int col = 0; col < n; ++col) {
+                        if (col / 2 == q4) {
+                            float* o = col & 1 ? o1 : o0;
+                            const float wt = col & 1 ? wt1 : wt0;
+                            o[0] = __fmaf_rn(wt, col & 1 ? acc[1] : acc[0], o[0]);
+                            o[8] = __fmaf_rn(wt, col & 1 ? acc[3] : acc[2], o[8]);
+                        }
+                        __syncwarp();
                     }
                 }
-                // weight this warp's share into its tokens, one column after
-                // another (a token may hold an expert twice)
-                for (int c = 0; c < n; ++c) {
-                    if (c / 2 == q4) {
-                        const int pair = sh.g.pair[first + c];
-                        const float wt = __ldg(topk_w + pair);
-                        float* o = slab + pair / k * 16 + row;
-                        o[0] = __fmaf_rn(wt, acc[c & 1], o[0]);
-                        o[8] = __fmaf_rn(wt, acc[2 + (c & 1)], o[8]);
-                    }
-                    __syncwarp();
-                }
-                w0 = w1;
-                w1 = w2;
-                w2 = scales(grp + 3);
+                __syncwarp();
             }
             if (!ok || !(ok = barrier.sync(gave_up))) break;
             // add the warps' sums in order and clear them
-            for (int v = threadIdx.x; v < MT * slab_n / 2; v += kDownWarps * 32) {
-                const int t = v / (8 * MT), ch = v % (8 * MT) * 2;  // token, channel of the tile
-                float a = 0.0f, b = 0.0f;
+            for (int v = threadIdx.x; v < slab_n / 2; v += kDownWarps * 32) {
+                float x = 0.0f, y = 0.0f;
 #pragma unroll
-                for (int w = ch / 16; w < kDownWarps; w += MT) {
-                    float2* p2 = reinterpret_cast<float2*>(slabs + w * slab_n + t * 16 + ch % 16);
-                    a = __fadd_rn(a, p2->x);
-                    b = __fadd_rn(b, p2->y);
+                for (int w = 0; w < kDownWarps; ++w) {
+                    float2* p2 = reinterpret_cast<float2*>(slabs + w * slab_n) + v;
+                    x = __fadd_rn(x, p2->x);
+                    y = __fadd_rn(y, p2->y);
                     *p2 = make_float2(0.0f, 0.0f);
                 }
-                *reinterpret_cast<uint32_t*>(out + (int64_t)t * H + tile * St::kRows + ch) = pack_bf16x2_rn(a, b);
+                *reinterpret_cast<uint32_t*>(out + (int64_t)(v / 8) * H + tile * kDownRows + v % 8 * 2) =
+                    pack_bf16x2_rn(x, y);
             }
             ok = barrier.sync(gave_up);
         }
@@ -590,17 +603,14 @@ size_t up_rest(int T, int H) {  // shared memory besides the ring
     const int held = T < kCols ? T : kCols;
     return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4;
 }
-template <int MT>
 size_t down_smem(int T) {
-    return 1024 + (size_t)DownStage<MT>::kStages * DownStage<MT>::kBytes + (size_t)kDownWarps * T * 16 * 4 + sizeof(DownShared);
+    return 1024 + (size_t)kDownStages * kDownStage + (size_t)kDownWarps * T * kDownRows * 4 + sizeof(DownShared);
 }
 static_assert(1024 + kCols * (EP_MOE_FEW_MAX_WIDTH + 16) + sizeof(UpShared) +
                       kCols * (EP_MOE_FEW_MAX_WIDTH / 128) * 4 + 2 * kUpStage <= kSmemLimit,
               "at least two stages at the widest");
-static_assert(1024 + DownStage<1>::kStages * DownStage<1>::kBytes + kDownWarps * EP_MOE_FEW_MAX_TOKENS * 64 + sizeof(DownShared) <=
-                  kSmemLimit, "");
-static_assert(1024 + DownStage<2>::kStages * DownStage<2>::kBytes + kDownWarps * EP_MOE_FEW_MAX_TOKENS * 64 + sizeof(DownShared) <=
-                  kSmemLimit, "");
+static_assert(1024 + kDownStages * kDownStage + kDownWarps * EP_MOE_FEW_MAX_TOKENS * kDownRows * 4 +
+                      sizeof(DownShared) <= kSmemLimit, "");
 
 int hs_stride_of(int I) { return (I / 128 + 7) / 8 * 8; }  // a stage's scales are copied as whole 32 bytes
 
@@ -626,7 +636,7 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     CUtensorMap w13_map, w2_map;
     cudaError_t err = byte_matrix_map(&w13_map, w13, (int64_t)E * 2 * I, H, 128);
     if (err != cudaSuccess) return err;
-    static std::atomic<uint64_t> configured[3];
+    static std::atomic<uint64_t> configured[2];
     err = raise_smem_limit(few_up_kernel, kSmemLimit, configured[0]);
     if (err != cudaSuccess) return err;
     const size_t rest = up_rest(T, H);
@@ -640,17 +650,13 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
                      H, k, topk_idx, s13, I, E, stages, hq, hs, hs_stride, status);
     if (err != cudaSuccess) return err;
 
-    // Output channels per block: 32, or 16 where that leaves fewer than 64
-    // blocks, the number that can draw nearly the whole bandwidth.
-    const int mt = H / 32 >= 64 ? 2 : 1;
-    const int tiles = H / (16 * mt);
-    err = byte_blocks_map(&w2_map, w2, (int64_t)E * H, I, 16 * mt, 8 / mt);
+    const int tiles = H / kDownRows;
+    err = byte_blocks_map(&w2_map, w2, (int64_t)E * H, I, kDownRows, kDownBlocks);
     if (err != cudaSuccess) return err;
-    auto kernel = mt == 2 ? few_down_kernel<2> : few_down_kernel<1>;
-    err = raise_smem_limit(kernel, kSmemLimit, configured[mt]);
+    err = raise_smem_limit(few_down_kernel, kSmemLimit, configured[1]);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3((kDownWarps + 1) * 32),
-                      mt == 2 ? down_smem<2>(T) : down_smem<1>(T), stream, w2_map, hq, hs, hs_stride, T,
+    return launch_pdl(few_down_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)),
+                      dim3((kDownWarps + 1) * 32), down_smem(T), stream, w2_map, hq, hs, hs_stride, T,
                       H, k, topk_idx, topk_w, s2, I, E, static_cast<uint16_t*>(out), status);
 }
 
