@@ -26,7 +26,8 @@
 //   results per token in shared memory of its own, and the block adds the
 //   warps' sums in order: the result never depends on timing.
 // An SM can draw more than twice its share of the memory's bandwidth, so that
-// neither kernel needs its items to divide evenly over the SMs.
+// neither kernel needs its items to divide evenly over the SMs.  Only where
+// there are fewer items than half the SMs do clusters of blocks share one.
 #include <stddef.h>
 
 #include "ep_tcgen05.cuh"
@@ -186,19 +187,28 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
 // matrix lane / 8: rows 0-7, 8-15, and the same again), 128 bytes with TMA's
 // 128-byte swizzle (16-byte chunk c of row r at c ^ (r % 8)); b_row: the 128
 // bytes of token lane % 8.
-__device__ __forceinline__ void block_product(float (&p)[4], uint32_t a_row, uint32_t b_row) {
+struct Operands {
+    uint32_t a[4][4], b[8];
+};
+__device__ __forceinline__ void load_operands(Operands& o, uint32_t a_row, uint32_t b_row) {
     const int lane = threadIdx.x & 31;
     const uint32_t r = lane & 7, hi = lane >> 4, quad = lane >> 3;
-    uint32_t b[8];
-    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(b), b_row + quad * 16);
-    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(b + 4), b_row + 64 + quad * 16);
-    p[0] = p[1] = p[2] = p[3] = 0.0f;
+    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(o.b), b_row + quad * 16);
+    load_matrices(*reinterpret_cast<uint32_t(*)[4]>(o.b + 4), b_row + 64 + quad * 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];
-        load_matrices(a, a_row + (((2 * j + hi) ^ r) << 4));
-        mma_e4m3(p, a, b[2 * j], b[2 * j + 1]);
-    }
+    for (int j = 0; j < 4; ++j) load_matrices(o.a[j], a_row + (((2 * j + hi) ^ r) << 4));
+}
+// Two chains of two MMAs, added at the end: half the latency of one of four.
+__device__ __forceinline__ void block_product(float (&p)[4], const Operands& o) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = q[i] = 0.0f;
+    mma_e4m3(p, o.a[0], o.b[0], o.b[1]);
+    mma_e4m3(q, o.a[1], o.b[2], o.b[3]);
+    mma_e4m3(p, o.a[2], o.b[4], o.b[5]);
+    mma_e4m3(q, o.a[3], o.b[6], o.b[7]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __fadd_rn(p[i], q[i]);
 }
 
 // Ring of TMA stages: the filling warp's side.
@@ -246,10 +256,14 @@ constexpr int kUpMaxStages = 6;
 struct UpShared {
     uint64_t full[kUpMaxStages], empty[kUpMaxStages], sync;
     int gave_up;
+    uint64_t part_full;
     float amax[2][kUpWarps][kCols];  // [item parity][warp][column]
     Groups g;
 };
 
+// C > 1: the C blocks of a cluster share each item's channels of K and the
+// first adds the others' sums in order; every cluster has at most one item.
+template <int C>
 __global__ void __launch_bounds__((kUpWarps + 1) * 32, 1)
 few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restrict__ x, int T,
               int H, int k, const int32_t* __restrict__ topk_idx, const float* __restrict__ s13,
@@ -260,8 +274,10 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     uint8_t* xq = ring + stages * kUpStage;
     const int stride = H + 16;  // 16 bytes of padding: eight tokens' chunks meet all banks
     const int held = min(T, kCols);
-    UpShared& sh = *reinterpret_cast<UpShared*>(xq + held * stride);
+    UpShared& sh = *reinterpret_cast<UpShared*>(xq + held * stride);  // 16-byte aligned
     float* xs = reinterpret_cast<float*>(&sh + 1);
+    // C > 1: the other blocks' sums [C - 1][warp][lane]
+    float4* part = reinterpret_cast<float4*>(((uintptr_t)(xs + held * (H / 128)) + 15) & ~(uintptr_t)15);
     const int nk = H / 128, nb = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
@@ -272,6 +288,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
             mbar_init(empty + 8 * i, kUpWarps);
         }
         mbar_init(smem_addr(&sh.sync), kUpWarps);
+        mbar_init(smem_addr(&sh.part_full), (C - 1) * kUpWarps + (C == 1));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.gave_up = 0;
         tma_prefetch_map(&w_map);
@@ -279,14 +296,19 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     pdl_wait();
     pdl_trigger();
     build_groups(sh.g, topk_idx, T * k, k, E, status, blockIdx.x == 0);
+    if (C > 1) cluster_sync();  // the first block's barrier is ready for the others
     const int items = sh.g.count * nb;  // (group, block of 128 channels)
+    const int worker = blockIdx.x / C, workers = gridDim.x / C;
+    // this block's blocks of K
+    const int rank = C > 1 ? (int)(blockIdx.x % C) : 0;
+    const int k0 = nk * rank / C, k1 = nk * (rank + 1) / C;
 
     if (warp == kUpWarps) {
         Fill fill{full, empty, (uint32_t)stages};
         bool ok = true;
-        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        for (int item = worker; item < items && ok; item += workers) {
             const int gate = sh.g.expert[item / nb] * 2 * I + item % nb * 128;
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = k0; kb < k1; ++kb) {
                 if (!(ok = fill.wait(gave_up))) break;
                 if (elect_one()) {
                     const uint32_t bar = full + 8 * fill.s, to = smem_addr(ring) + fill.s * kUpStage;
@@ -310,7 +332,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
         uint32_t s = 0, phase = 0, parity = 0;
         int have = -1;  // the group whose x is in shared memory
         bool ok = true;
-        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+        for (int item = worker; item < items && ok; item += workers) {
             const int grp = item / nb, b = item % nb, n = sh.g.size[grp], first = sh.g.first[grp];
             const float* sg = s13 + ((int64_t)sh.g.expert[grp] * 2 * nb + b) * nk;
             const float* su = sg + (int64_t)nb * nk;
@@ -321,13 +343,13 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 if ((warp >> 1) < n) {
                     const uint16_t* src = x + (int64_t)t * H;
                     uint8_t* to = xq + (warp >> 1) * stride;
-                    for (int c0 = (warp & 1) * 1024; c0 < H; c0 += 2048) {
+                    for (int c0 = k0 * 128 + (warp & 1) * 1024; c0 < k1 * 128; c0 += 2048) {
                         uint4 a[2], q[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int c = c0 + u * 512 + lane * 16;
                             a[u] = q[u] = make_uint4(0, 0, 0, 0);
-                            if (c < H) {
+                            if (c < k1 * 128) {
                                 a[u] = __ldg(reinterpret_cast<const uint4*>(src + c));
                                 q[u] = __ldg(reinterpret_cast<const uint4*>(src + c + 8));
                             }
@@ -336,7 +358,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                         for (int u = 0; u < 2; ++u) {
                             const int c = c0 + u * 512 + lane * 16;
                             const Fp8Group f = quantize16(a[u], q[u]);
-                            if (c < H) {
+                            if (c < k1 * 128) {
                                 *reinterpret_cast<uint4*>(to + c) = f.q;
                                 if ((lane & 7) == 0) xs[(warp >> 1) * nk + (c >> 7)] = f.sf;
                             }
@@ -348,21 +370,25 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
             }
             float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             float vg = 0.0f, vu = 0.0f;  // the weights' scales, a block per lane
-            for (int kb = 0; kb < nk; ++kb) {
-                if (kb % 32 == 0 && kb + lane < nk) {
-                    vg = __ldg(sg + kb + lane);
-                    vu = __ldg(su + kb + lane);
+            for (int kb = k0; kb < k1; ++kb) {
+                if ((kb - k0) % 32 == 0) {
+                    const int to = min(kb + lane, nk - 1);
+                    vg = __ldg(sg + to);
+                    vu = __ldg(su + to);
                 }
                 if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
+                Operands o;
+                load_operands(o, a_lane + s * kUpStage, b_lane + kb * 128);
                 float p[4];
-                block_product(p, a_lane + s * kUpStage, b_lane + kb * 128);
+                block_product(p, o);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + 8 * s);
                 if (++s == (uint32_t)stages) {
                     s = 0;
                     phase ^= 1;
                 }
-                const float wg = __shfl_sync(kFullMask, vg, kb % 32), wu = __shfl_sync(kFullMask, vu, kb % 32);
+                const float wg = __shfl_sync(kFullMask, vg, (kb - k0) % 32);
+                const float wu = __shfl_sync(kFullMask, vu, (kb - k0) % 32);
                 const float c0 = x0[kb], c1 = x1[kb];
                 acc[0] = __fmaf_rn(p[0], __fmul_rn(c0, wg), acc[0]);
                 acc[1] = __fmaf_rn(p[1], __fmul_rn(c1, wg), acc[1]);
@@ -370,6 +396,26 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 acc[3] = __fmaf_rn(p[3], __fmul_rn(c1, wu), acc[3]);
             }
             if (!ok) break;
+            if (C > 1) {
+                if (rank > 0) {  // hand the sums to the cluster's first block: nothing else to do
+                    const uint32_t to = cluster_addr(smem_addr(part + ((rank - 1) * kUpWarps + warp) * 32 + lane), 0);
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(acc[0]),
+                                 "f"(acc[1]), "f"(acc[2]), "f"(acc[3])
+                                 : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sh.part_full), 0));
+                    break;
+                }
+                if (!(ok = mbar_wait_cluster(smem_addr(&sh.part_full), 0, gave_up))) break;
+#pragma unroll
+                for (int r = 0; r < C - 1; ++r) {
+                    const float4 v = part[(r * kUpWarps + warp) * 32 + lane];
+                    acc[0] = __fadd_rn(acc[0], v.x);
+                    acc[1] = __fadd_rn(acc[1], v.y);
+                    acc[2] = __fadd_rn(acc[2], v.z);
+                    acc[3] = __fadd_rn(acc[3], v.w);
+                }
+            }
             float h[2], m[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -404,7 +450,32 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     __syncwarp();
     __syncthreads();
     if (threadIdx.x == 0 && sh.gave_up && status) atomicOr(status, EP_FLAG_TIMEOUT);
+    if (C > 1) cluster_sync();  // no block leaves while another may still write to it
 }
+
+template <int C>
+cudaError_t launch_up(int blocks, size_t smem, cudaStream_t stream, const CUtensorMap& w_map, const void* x,
+                      int T, int H, int k, const int32_t* topk_idx, const float* s13, int I, int E, int stages,
+                      uint8_t* hq, float* hs, int hs_stride, uint32_t* status) {
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t err = raise_smem_limit(few_up_kernel<C>, kSmemLimit, configured);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((kUpWarps + 1) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {C, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, few_up_kernel<C>, w_map, static_cast<const uint16_t*>(x), T, H, k,
+                              topk_idx, s13, I, E, stages, hq, hs, hs_stride, status);
+}
+
 
 // ---- down -----------------------------------------------------------------
 
@@ -430,7 +501,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-__global__ void __launch_bounds__((kDownWarps + 1) * 32, 1)
+__global__ void __launch_bounds__((kDownWarps + 2) * 32, 1)
 few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ hq,
                 const float* __restrict__ hs, int hs_stride, int T, int H, int k,
                 const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
@@ -458,52 +529,62 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
     // one start only after all earlier work had completed.
     build_groups(sh.g, topk_idx, T * k, k, E, nullptr, false);
     const int tiles = H / kDownRows;
-    const int per_group = (nk + kDownBlocks - 1) / kDownBlocks;  // stages
     const int groups = sh.g.count;
 
     if (warp == kDownWarps) {
+        // ---- weights, from before the up kernel has finished
         Fill fill{full, empty, (uint32_t)kDownStages};
-        // a stage's tokens: their codes and scales, one lane each
-        auto load_tokens = [&](uint32_t s, int grp, int b0) {
-            if (lane < sh.g.size[grp]) {
-                const int pair = sh.g.pair[sh.g.first[grp] + lane];
-                const uint32_t to = smem_addr(ring) + s * kDownStage + kDownW, bar = full + 8 * s;
-                bulk_load(to + lane * kTokenRow, hq + (int64_t)pair * I + b0 * 128,
-                          min(kDownBlocks, nk - b0) * 128, bar);
-                bulk_load(to + kCols * kTokenRow + lane * kScaleRow * 4, hs + (int64_t)pair * hs_stride + b0,
-                          kScaleRow * 4, bar);
-            }
-        };
-        // the first round's weights are on their way: now h
-        auto first_tokens = [&]() {
-            pdl_wait();
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            for (uint32_t i = 0; i < fill.issued; ++i)
-                load_tokens(i, (int)(i / per_group) % groups, (int)(i % per_group) * kDownBlocks);
-        };
-        bool ok = true, up_done = false;
+        bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            int n = 0, e = 0;
+            if (groups > 0) n = sh.g.size[0], e = sh.g.expert[0];
             for (int grp = 0; grp < groups && ok; ++grp) {
-                const int n = sh.g.size[grp];
-                const int wrow = sh.g.expert[grp] * H + tile * kDownRows;
+                const int tokens = n, wrow = e * H + tile * kDownRows;
+                if (grp + 1 < groups) n = sh.g.size[grp + 1], e = sh.g.expert[grp + 1];
                 for (int b0 = 0; b0 < nk; b0 += kDownBlocks) {
-                    if (!up_done && fill.issued == kDownStages) {
-                        first_tokens();
-                        up_done = true;
-                    }
                     if (!(ok = fill.wait(gave_up))) break;
                     if (elect_one()) {
                         const uint32_t bar = full + 8 * fill.s;
-                        mbar_expect_tx(bar, kDownW + n * (min(kDownBlocks, nk - b0) * 128 + kScaleRow * 4));
+                        mbar_expect_tx(bar, kDownW + tokens * (min(kDownBlocks, nk - b0) * 128 + kScaleRow * 4));
                         tma_load_3d(smem_addr(ring) + fill.s * kDownStage, &w_map, 0, wrow, b0, bar);
                     }
                     __syncwarp();
-                    if (up_done) load_tokens(fill.s, grp, b0);
                     fill.next();
                 }
             }
         }
-        if (!up_done) first_tokens();
+        if (!ok) fill.drain();
+    } else if (warp == kDownWarps + 1) {
+        // ---- h: a stage's tokens' codes and scales, one lane each
+        pdl_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        Fill fill{full, empty, (uint32_t)kDownStages};
+        bool ok = true;
+        const uint32_t to = smem_addr(ring) + kDownW + lane * kTokenRow;
+        const uint32_t to_s = smem_addr(ring) + kDownW + kCols * kTokenRow + lane * kScaleRow * 4;
+        int64_t pair = -1;  // this lane's pair of the group to come
+        auto look = [&](int grp) {
+            pair = grp < groups && lane < sh.g.size[grp] ? sh.g.pair[sh.g.first[grp] + lane] : -1;
+        };
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            look(0);
+            for (int grp = 0; grp < groups && ok; ++grp) {
+                const bool mine = pair >= 0;
+                const uint8_t* q = hq + pair * I;
+                const float* c = hs + pair * hs_stride;
+                look(grp + 1);
+                for (int b0 = 0; b0 < nk; b0 += kDownBlocks) {
+                    if (!(ok = fill.wait(gave_up))) break;
+                    if (mine) {
+                        const uint32_t at = fill.s * kDownStage, bar = full + 8 * fill.s;
+                        bulk_load(to + at, q + b0 * 128, min(kDownBlocks, nk - b0) * 128, bar);
+                        bulk_load(to_s + at, c + b0, kScaleRow * 4, bar);
+                    }
+                    __syncwarp();
+                    fill.next();
+                }
+            }
+        }
         if (!ok) fill.drain();
     } else {
         const int slab_n = T * kDownRows;
@@ -515,23 +596,44 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
         const uint32_t b_lane = smem_addr(ring) + kDownW + (lane & 7) * kTokenRow;
         const uint8_t* c_lane = ring + kDownW + kCols * kTokenRow + 2 * q4 * kScaleRow * 4;  // two tokens' scales
         float* slab = slabs + warp * slab_n;
-        const uint32_t per_tile = groups * per_group;  // stages
+        const int per_group = (nk + kDownBlocks - 1) / kDownBlocks;  // stages
+        const uint32_t per_tile = groups * per_group;
         const uint32_t s = warp;
         uint32_t base = 0, at = warp, phase = 0;  // stages before this tile; this warp's next
+        // What a stage needs besides its bytes: its first block of K, the
+        // weights' scales (block b0 + lane % 8), and this lane's two columns'
+        // tokens and weights.
+        struct Next {
+            int b0, n, t0, t1;
+            bool twice;
+            float scale, wt0, wt1;
+        };
+        auto look = [&](uint32_t u, const float* ws) {
+            Next x{};
+            if (u < per_tile) {
+                const int grp = u / per_group, first = sh.g.first[grp];
+                x.b0 = u % per_group * kDownBlocks;
+                x.n = sh.g.size[grp];
+                x.twice = sh.g.twice[grp];
+                x.scale = __ldg(ws + (int64_t)sh.g.expert[grp] * (H / 128) * nk + min(x.b0 + (lane & 7), nk - 1));
+                const int pair0 = sh.g.pair[first + min(2 * q4, x.n - 1)];
+                const int pair1 = sh.g.pair[first + min(2 * q4 + 1, x.n - 1)];
+                x.wt0 = __ldg(topk_w + pair0);
+                x.wt1 = __ldg(topk_w + pair1);
+                x.t0 = pair0 / k;
+                x.t1 = pair1 / k;
+            }
+            return x;
+        };
         bool ok = barrier.sync(gave_up);
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, base += per_tile) {
             const float* ws = s2 + (int64_t)(tile * kDownRows / 128) * nk;  // of expert 0
-            // this warp's stages: every sixth of the block's sequence
+            // this warp's stages: every sixth of the block's sequence; the next
+            // one's scalars are read behind the wait for this one
+            Next next = look(at - base, ws);
             for (; at < base + per_tile; at += kDownWarps) {
-                const uint32_t u = at - base;
-                const int grp = u / per_group, b0 = u % per_group * kDownBlocks;
-                const int n = sh.g.size[grp], first = sh.g.first[grp];
-                // read behind the wait: the weights' scales, a block per lane,
-                // and the two columns' tokens and weights
-                const int b = min(b0 + (lane & 7), nk - 1);
-                const float wl = __ldg(ws + (int64_t)sh.g.expert[grp] * (H / 128) * nk + b);
-                const int pair0 = sh.g.pair[first + min(2 * q4, n - 1)], pair1 = sh.g.pair[first + min(2 * q4 + 1, n - 1)];
-                const float wt0 = __ldg(topk_w + pair0), wt1 = __ldg(topk_w + pair1);
+                const Next now = next;
+                next = look(at + kDownWarps - base, ws);
                 if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
                 phase ^= 1;
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -539,10 +641,12 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                 const float* c = reinterpret_cast<const float*>(c_lane + s * kDownStage);
 #pragma unroll
                 for (int j = 0; j < kDownBlocks; ++j) {
-                    if (b0 + j < nk) {  // warp-uniform
+                    if (now.b0 + j < nk) {  // warp-uniform
+                        Operands o;
+                        load_operands(o, a + j * kDownRows * 128, t + j * 128);
                         float p[4];
-                        block_product(p, a + j * kDownRows * 128, t + j * 128);
-                        const float w = __shfl_sync(kFullMask, wl, j);
+                        block_product(p, o);
+                        const float w = __shfl_sync(kFullMask, now.scale, j);
                         const float c0 = __fmul_rn(c[j], w), c1 = __fmul_rn(c[kScaleRow + j], w);
                         acc[0] = __fmaf_rn(p[0], c0, acc[0]);
                         acc[1] = __fmaf_rn(p[1], c1, acc[1]);
@@ -552,22 +656,22 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + 8 * s);
-                float* o0 = slab + pair0 / k * kDownRows + row;
-                float* o1 = slab + pair1 / k * kDownRows + row;
-                if (!sh.g.twice[grp]) {  // every column has a token of its own
-                    if (2 * q4 < n) {
-                        o0[0] = __fmaf_rn(wt0, acc[0], o0[0]);
-                        o0[8] = __fmaf_rn(wt0, acc[2], o0[8]);
+                float* o0 = slab + now.t0 * kDownRows + row;
+                float* o1 = slab + now.t1 * kDownRows + row;
+                if (!now.twice) {  // every column has a token of its own
+                    if (2 * q4 < now.n) {
+                        o0[0] = __fmaf_rn(now.wt0, acc[0], o0[0]);
+                        o0[8] = __fmaf_rn(now.wt0, acc[2], o0[8]);
                     }
-                    if (2 * q4 + 1 < n) {
-                        o1[0] = __fmaf_rn(wt1, acc[1], o1[0]);
-                        o1[8] = __fmaf_rn(wt1, acc[3], o1[8]);
+                    if (2 * q4 + 1 < now.n) {
+                        o1[0] = __fmaf_rn(now.wt1, acc[1], o1[0]);
+                        o1[8] = __fmaf_rn(now.wt1, acc[3], o1[8]);
                     }
                 } else {  // one column after another
-                    for (int col = 0; col < n; ++col) {
+                    for (int col = 0; col < now.n; ++col) {
                         if (col / 2 == q4) {
                             float* o = col & 1 ? o1 : o0;
-                            const float wt = col & 1 ? wt1 : wt0;
+                            const float wt = col & 1 ? now.wt1 : now.wt0;
                             o[0] = __fmaf_rn(wt, col & 1 ? acc[1] : acc[0], o[0]);
                             o[8] = __fmaf_rn(wt, col & 1 ? acc[3] : acc[2], o[8]);
                         }
@@ -599,9 +703,10 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
     if (threadIdx.x == 0 && sh.gave_up && status) atomicOr(status, EP_FLAG_TIMEOUT);
 }
 
-size_t up_rest(int T, int H) {  // shared memory besides the ring
+size_t up_rest(int T, int H, int C) {  // shared memory besides the ring
     const int held = T < kCols ? T : kCols;
-    return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4;
+    return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4 +
+           (C > 1 ? 16 + (size_t)(C - 1) * kUpWarps * 32 * 16 : 0);
 }
 size_t down_smem(int T) {
     return 1024 + (size_t)kDownStages * kDownStage + (size_t)kDownWarps * T * kDownRows * 4 + sizeof(DownShared);
@@ -636,27 +741,30 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     CUtensorMap w13_map, w2_map;
     cudaError_t err = byte_matrix_map(&w13_map, w13, (int64_t)E * 2 * I, H, 128);
     if (err != cudaSuccess) return err;
-    static std::atomic<uint64_t> configured[2];
-    err = raise_smem_limit(few_up_kernel, kSmemLimit, configured[0]);
-    if (err != cudaSuccess) return err;
-    const size_t rest = up_rest(T, H);
-    int stages = (int)((kSmemLimit - rest) / kUpStage);
-    if (stages > kUpMaxStages) stages = kUpMaxStages;
     // at most one group per pair and 128 channels (an expert with more than 8
     // tokens has as many groups as its pairs need)
     const int64_t items = (int64_t)T * k * (I / 128);
-    err = launch_pdl(few_up_kernel, dim3((unsigned)(items < sms ? items : sms)), dim3((kUpWarps + 1) * 32),
-                     rest + (size_t)stages * kUpStage, stream, w13_map, static_cast<const uint16_t*>(x), T,
-                     H, k, topk_idx, s13, I, E, stages, hq, hs, hs_stride, status);
+    // Few items leave SMs without one: then several blocks share an item's K
+    // (not at widths where the tokens would leave the ring too few stages).
+    // One token, H = 2048, I = 1024, k = 8, 64 items: MEASURED_SPLIT.
+    const int C = H > 8192 || H < 1024 ? 1 : items * 4 <= sms ? 4 : items * 2 <= sms ? 2 : 1;
+    const size_t rest = up_rest(T, H, C);
+    int stages = (int)((kSmemLimit - rest) / kUpStage);
+    if (stages > kUpMaxStages) stages = kUpMaxStages;
+    const int blocks = C > 1 ? (int)items * C : (int)(items < sms ? items : sms);
+    const auto up = C == 4 ? launch_up<4> : C == 2 ? launch_up<2> : launch_up<1>;
+    err = up(blocks, rest + (size_t)stages * kUpStage, stream, w13_map, x, T, H, k, topk_idx, s13, I, E, stages,
+             hq, hs, hs_stride, status);
     if (err != cudaSuccess) return err;
 
     const int tiles = H / kDownRows;
     err = byte_blocks_map(&w2_map, w2, (int64_t)E * H, I, kDownRows, kDownBlocks);
     if (err != cudaSuccess) return err;
-    err = raise_smem_limit(few_down_kernel, kSmemLimit, configured[1]);
+    static std::atomic<uint64_t> configured{0};
+    err = raise_smem_limit(few_down_kernel, kSmemLimit, configured);
     if (err != cudaSuccess) return err;
     return launch_pdl(few_down_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                      dim3((kDownWarps + 1) * 32), down_smem(T), stream, w2_map, hq, hs, hs_stride, T,
+                      dim3((kDownWarps + 2) * 32), down_smem(T), stream, w2_map, hq, hs, hs_stride, T,
                       H, k, topk_idx, topk_w, s2, I, E, static_cast<uint16_t*>(out), status);
 }
 
