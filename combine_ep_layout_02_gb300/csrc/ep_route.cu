@@ -10,11 +10,12 @@
 //              times scale
 // A place without an eligible expert holds id -1 and weight 0.
 //
-// One warp per token, expert i * 32 + lane in register i.  A key becomes an
-// unsigned word of the same order (0: not eligible).  The k-th largest of the
+// One warp per token.  Where E is 32 times a register count, lane l holds the
+// experts [l * NV, (l + 1) * NV), read as whole vectors; otherwise register i
+// holds expert i * 32 + lane.  A key becomes an unsigned word of the same order (0: not eligible).  The k-th largest of the
 // 32 lanes' maxima is at most the k-th largest key, so that every choice is
 // among the keys that reach it: usually a dozen, which move one to a lane
-// (in the order of their ids) and are ranked against each other.  Where more
+// and are ranked against each other.  Where more
 // than 32 reach it (many equal keys, or k near 32) k rounds of a maximum over
 // the warp find the choices instead.
 //
@@ -33,17 +34,50 @@ __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_logit(const uint16_t* p) {
     return __uint_as_float((uint32_t)__ldg(p) << 16);
 }
-
-// Order-preserving word of a key; 0 for NaN and -inf (not eligible).  Adding
-// +0 first makes -0 and +0 one key, as they compare equal.
-__device__ __forceinline__ uint32_t ordered(float key) {
-    const uint32_t b = __float_as_uint(__fadd_rn(key, 0.0f));
-    if (!(key > -INFINITY)) return 0u;
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+// N values from p, aligned to all of them or to 16 bytes.
+template <int N>
+__device__ __forceinline__ void load_logits(float (&v)[N], const float* p) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p + i));
+            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_logits(float (&v)[N], const uint16_t* p) {
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + i));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i + 2 * j] = bf16lo_to_f32(w[j]), v[i + 2 * j + 1] = bf16hi_to_f32(w[j]);
+        }
+    } else if constexpr (N == 4) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        v[0] = bf16lo_to_f32(q.x), v[1] = bf16hi_to_f32(q.x), v[2] = bf16lo_to_f32(q.y), v[3] = bf16hi_to_f32(q.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = load_logit(p + i);
+    }
 }
 
-// The key of a non-zero word.
+// Order-preserving word of a key; 0 for NaN and -inf (not eligible).  Adding
+// +0 first makes -0 and +0 one key, as they compare equal; fmaxf turns a NaN
+// into -inf, whose word 0x007fffff is the origin.
+constexpr uint32_t kOrigin = 0x007fffffu;
+__device__ __forceinline__ uint32_t ordered(float key) {
+    const int32_t b = __float_as_int(fmaxf(__fadd_rn(key, 0.0f), -INFINITY));
+    return ((uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u)) - kOrigin;
+}
+// The key of a word.
 __device__ __forceinline__ float unordered(uint32_t w) {
+    w += kOrigin;
     return __uint_as_float((w & 0x80000000u) ? (w ^ 0x80000000u) : ~w);
 }
 
@@ -72,96 +106,119 @@ __device__ __forceinline__ float sigmoid(float l) {
     return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
 }
 
-template <int NV, typename L>
+template <int NV, bool FULL, typename L>
 __global__ void __launch_bounds__(kWarps * 32)
 route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64_t T, int E, int k,
              int groups, int groups_per_token, int scoring, int renormalize, float scale,
              int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
              uint32_t* __restrict__ status) {
-    __shared__ uint2 list[kWarps][32];  // candidates: key, id; the groups' best keys before that
+    // candidates as (word, ~id), in the order of the choice; the groups' best keys before that
+    __shared__ uint64_t list[kWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= T) return;  // warp-uniform
     const L* row = logits + t * E;
-    uint2* mine = list[warp];
+    uint64_t* mine = list[warp];
 
-    uint32_t key[NV];
-    bool bad = false;
+    auto id = [lane](int i) { return FULL ? lane * NV + i : i * 32 + lane; };
+    float v[NV];
+    if constexpr (FULL) {
+        load_logits<NV>(v, row + lane * NV);
+        if (bias) {
+            float w[NV];
+            load_logits<NV>(w, bias + lane * NV);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = __fadd_rn(v[i], w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = id(i) < E ? load_logit(row + id(i)) : -INFINITY;
+        if (bias) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (id(i) < E) v[i] = __fadd_rn(v[i], __ldg(bias + id(i)));
+        }
+    }
+    if (status) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) bad |= v[i] != v[i];
+        warp_flag(status, bad, EP_FLAG_BAD_LOGIT);
+    }
+    uint32_t key[NV], top = 0u;  // the largest key of this lane
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = i * 32 + lane;
-        float c = -INFINITY;
-        if (e < E) {
-            c = load_logit(row + e);
-            if (bias) c = __fadd_rn(c, __ldg(bias + e));
-        }
-        bad |= c != c;
-        key[i] = ordered(c);
+        key[i] = ordered(v[i]);
+        top = max(top, key[i]);
     }
-    warp_flag(status, bad, EP_FLAG_BAD_LOGIT);
 
+    bool in = true;  // FULL: whether the lane's experts are in a chosen group
     if (groups_per_token < groups) {
         const int per = E / groups;
         const uint32_t inverse = ((1u << 20) + per - 1) / per;
-        uint32_t best = 0u;  // lane g: the best key of group g
-        if (per % 32 == 0) {  // a register's 32 experts lie in one group
-            const int regs = per / 32;
-            int g = 0, left = regs;
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                m = max(m, key[i]);
-                if (--left == 0) {
-                    m = __reduce_max_sync(kFullMask, m);
-                    if (lane == g) best = m;
-                    ++g;
-                    left = regs;
-                    m = 0u;
-                }
-            }
+        const int span = per / NV;  // lanes of a group
+        const bool lanes = FULL && span * NV == per && (span & (span - 1)) == 0;
+        uint32_t best;  // lane g: the best key of group g
+        if (lanes) {
+            best = top;
+            for (int o = 1; o < span; o <<= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
+            best = __shfl_sync(kFullMask, best, (lane * span) & 31);
         } else {
-            mine[lane].x = 0u;
+            uint32_t* bests = reinterpret_cast<uint32_t*>(mine);
+            bests[lane] = 0u;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (key[i]) atomicMax(&mine[group_of(i * 32 + lane, inverse)].x, key[i]);
+                if (key[i]) atomicMax(bests + group_of(id(i), inverse), key[i]);
             __syncwarp();
-            best = mine[lane].x;
+            best = bests[lane];
             __syncwarp();
         }
         // a group's rank: how many are better, or as good and earlier
         int rank = 0;
+#pragma unroll 4
         for (int g = 0; g < groups; ++g) {
             const uint32_t other = __shfl_sync(kFullMask, best, g);
             rank += other > best || (other == best && g < lane);
         }
         const unsigned chosen = __ballot_sync(kFullMask, rank < groups_per_token);
+        if (lanes) {
+            in = (chosen >> (lane / span)) & 1u;
+            if (!in) top = 0u;
+        } else {
+            top = 0u;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int g = group_of(per % 32 == 0 ? i * 32 : i * 32 + lane, inverse);
-            if (!((chosen >> (g & 31)) & 1u)) key[i] = 0u;
+            for (int i = 0; i < NV; ++i) {
+                if (!((chosen >> (group_of(id(i), inverse) & 31)) & 1u)) key[i] = 0u;
+                top = max(top, key[i]);
+            }
         }
     }
 
-    uint32_t top = 0u;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) top = max(top, key[i]);
-    uint32_t reach = 1u;  // every eligible key, where there are fewer than k lanes with one
+    uint32_t reach = 0u;  // 0 at the end where fewer than k lanes have a key
+#pragma unroll 4
     for (int j = 0; j < k; ++j) {
-        const uint32_t m = __reduce_max_sync(kFullMask, top);
-        reach = max(m, 1u);
-        if (m == 0u) break;
-        if (top == m) top = 0u;
+        reach = __reduce_max_sync(kFullMask, top);
+        if (top == reach) top = 0u;
     }
-    int count = 0;
+    const uint32_t bar = in ? max(reach, 1u) : 0xffffffffu;  // no key is that large
+    int own = 0;  // candidates of this lane, then of the lanes up to it
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const unsigned b = __ballot_sync(kFullMask, key[i] >= reach);
-        const int at = count + __popc(b & lanemask_lt());
-        if (key[i] >= reach && at < 32) mine[at] = make_uint2(key[i], i * 32 + lane);
-        count += __popc(b);
+    for (int i = 0; i < NV; ++i) own += key[i] >= bar;
+    int at = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(kFullMask, at, o);
+        if (lane >= o) at += below;
+    }
+    const int count = __shfl_sync(kFullMask, at, 31);
+    if (count <= 32 && own > 0) {
+        at -= own;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] >= bar) mine[at++] = ((uint64_t)key[i] << 32) | ~(uint32_t)id(i);
     }
     __syncwarp();
 
@@ -170,14 +227,12 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
     if (count <= 32) {
         place = 32;
         if (lane < count) {
-            const uint2 c = mine[lane];
-            word = c.x;
+            const uint64_t c = mine[lane];
+            word = (uint32_t)(c >> 32);
             place = 0;
-            for (int q = 0; q < count; ++q) {
-                const uint32_t other = mine[q].x;
-                place += other > word || (other == word && q < lane);
-            }
-            idx = place < k ? (int)c.y : -1;
+#pragma unroll 4
+            for (int q = 0; q < count; ++q) place += mine[q] > c;
+            idx = place < k ? (int)~(uint32_t)c : -1;
         }
         const int found = min(count, k);
         if (idx < 0) place = lane >= found && lane < k ? lane : 32;  // places left over hold no candidate
@@ -185,17 +240,17 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
         for (int j = 0; j < k; ++j) {
             uint32_t m = 0u;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) m = max(m, key[i]);
+            for (int i = 0; i < NV; ++i) m = max(m, in ? key[i] : 0u);
             m = __reduce_max_sync(kFullMask, m);
             if (m == 0u) break;
             int e = INT32_MAX;
 #pragma unroll
             for (int i = NV - 1; i >= 0; --i)
-                if (key[i] == m) e = i * 32 + lane;
+                if (in && key[i] == m) e = id(i);
             e = __reduce_min_sync(kFullMask, e);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane == e) key[i] = 0u;
+                if (id(i) == e) key[i] = 0u;
             if (lane == j) {
                 idx = e;
                 word = m;
@@ -210,19 +265,21 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
         if (renormalize) {
             // the softmax over the chosen logits alone, so that nothing is lost
             // when a bias chooses experts far below the maximum
-            const float m = warp_max(l);
+            const float m = unordered(__reduce_max_sync(kFullMask, live ? ordered(l) : 0u));
             p = live ? expf(below(l, m)) : 0.0f;
+            const float s = warp_sum(p);  // 1 to k, or 0 without a choice
+            p = live ? __fdividef(p, s) : 0.0f;
         } else {
             float m = -INFINITY, s = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane < E) m = fmaxf(m, load_logit(row + i * 32 + lane));  // passes over a NaN
+                if (id(i) < E) m = fmaxf(m, load_logit(row + id(i)));  // passes over a NaN
             m = warp_max(m);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (i * 32 + lane < E) {
-                    const float v = load_logit(row + i * 32 + lane);
-                    if (v == v) s = __fadd_rn(s, expf(below(v, m)));
+                if (id(i) < E) {
+                    const float w = load_logit(row + id(i));
+                    if (w == w) s = __fadd_rn(s, expf(below(w, m)));
                 }
             }
             s = warp_sum(s);
@@ -230,10 +287,10 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
         }
     } else {
         p = live ? sigmoid(l) : 0.0f;
-    }
-    if (renormalize) {
-        const float s = warp_sum(p);
-        p = s > 0.0f ? __fdiv_rn(p, s) : 0.0f;
+        if (renormalize) {
+            const float s = warp_sum(p);
+            p = s > 0.0f ? __fdiv_rn(p, s) : 0.0f;
+        }
     }
     if (place < k) {
         topk_idx[t * k + place] = idx;
@@ -250,12 +307,17 @@ cudaError_t launch(const L* logits, const float* bias, int64_t T, int E, int k, 
         return launch_pdl(kernel, grid, block, 0, stream, logits, bias, T, E, k, groups,
                           groups_per_token, scoring, renormalize, scale, topk_idx, topk_w, status);
     };
-    if (E <= 32) return go(route_kernel<1, L>);
-    if (E <= 64) return go(route_kernel<2, L>);
-    if (E <= 128) return go(route_kernel<4, L>);
-    if (E <= 256) return go(route_kernel<8, L>);
-    if (E <= 512) return go(route_kernel<16, L>);
-    return go(route_kernel<32, L>);
+    // whole vectors per lane where a row is 32 lanes of them and lies on 16 bytes
+    const bool vectors = ((uintptr_t)logits | (uintptr_t)bias) % 16 == 0;
+    if (vectors && E == 128) return go(route_kernel<4, true, L>);
+    if (vectors && E == 256) return go(route_kernel<8, true, L>);
+    if (vectors && E == 512) return go(route_kernel<16, true, L>);
+    if (E <= 32) return go(route_kernel<1, false, L>);
+    if (E <= 64) return go(route_kernel<2, false, L>);
+    if (E <= 128) return go(route_kernel<4, false, L>);
+    if (E <= 256) return go(route_kernel<8, false, L>);
+    if (E <= 512) return go(route_kernel<16, false, L>);
+    return go(route_kernel<32, false, L>);
 }
 
 }  // namespace
