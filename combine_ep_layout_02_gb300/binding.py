@@ -432,6 +432,21 @@ def combine_reduce(partial, rl, T, out=None, status=None):
     return out
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device):
+    """The current stream's handle; without the Stream object where torch allows
+    it, which saves the smallest calls 2 us."""
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _on_current(device, fn, *args):
     """Call `fn` with `device` current, skipping the switch when it already is."""
     if torch.cuda.current_device() == device.index:
@@ -471,12 +486,8 @@ def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="sof
         None if bias is None else bias.data_ptr(), T, E, k, groups,
         groups if groups_per_token is None else groups_per_token, SCORES[scoring],
         1 if renormalize else 0, scale, topk_idx.data_ptr(), topk_w.data_ptr(),
-        None if status is None else status.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+        None if status is None else status.data_ptr(), _stream_of(dev)))
     return topk_idx, topk_w
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _check_group_gemm(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, kind):
@@ -524,7 +535,7 @@ def group_gemm_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, ki
         dev, load().ep_group_gemm_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K, w_q.data_ptr(),
         w_scale.data_ptr(), N, E, expert_counts.data_ptr(), _addr(expert_offsets),
         LAYOUT_KINDS[kind], capacity, out.data_ptr(), _addr(status),
-        torch.cuda.current_stream(dev).cuda_stream))
+        _stream_of(dev)))
     return out
 
 
@@ -551,7 +562,7 @@ def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offs
         dev, load().ep_group_gemm_swiglu_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K,
         w_q.data_ptr(), w_scale.data_ptr(), inner, E, expert_counts.data_ptr(),
         _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, out_q.data_ptr(), out_scale.data_ptr(),
-        _addr(status), torch.cuda.current_stream(dev).cuda_stream))
+        _addr(status), _stream_of(dev)))
     return out_q, out_scale
 
 
@@ -594,7 +605,7 @@ def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, wor
         dev, load().ep_moe_few, x.data_ptr(), T, H, k, topk_idx.data_ptr(), topk_w.data_ptr(),
         w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_scale.data_ptr(), inner, E,
         out.data_ptr(), _addr(status), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream))
+        workspace.numel() * workspace.element_size(), _stream_of(dev)))
     return out
 
 

@@ -25,33 +25,19 @@
 namespace ep {
 namespace {
 
-#ifndef GG_CHUNK
-#define GG_CHUNK 16
-#endif
 constexpr int kRowsM = 128;                     // rows of a tile
 constexpr int kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
 constexpr int kABytes = kRowsM * kBlockK, kBBytes = kTileN * kBlockK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kARows = 32;                      // rows per TMA box of A: rows past the segment's end are not read
-#ifndef GG_WARPS
-#define GG_WARPS 8
-#endif
-#ifndef GG_BUFS
-#define GG_BUFS 2
-#endif
-constexpr int kAddWarps = GG_WARPS;             // warps that scale and add
-constexpr int kBufs = GG_BUFS;
+constexpr int kAddWarps = 8;                    // warps that scale and add
 constexpr int kAddThreads = kAddWarps * 32;
 constexpr int kThreads = 128 + kAddThreads;
-#ifndef GG_IR
-#define GG_IR 72
-#define GG_AR 216
-#endif
-constexpr int kIssueRegs = GG_IR, kAddRegs = GG_AR;
+constexpr int kIssueRegs = 72, kAddRegs = 216;  // 128 * 72 + 256 * 216 = 384 * 168
 constexpr int kShares = kAddWarps / 4;          // column shares of a tile
 constexpr int kCols = kTileN / kShares;         // columns of a share
-constexpr int kChunk = GG_CHUNK;                // columns per TMEM load
+constexpr int kChunk = 16;                      // columns per TMEM load
 constexpr int kAhead = 16;                      // blocks whose scales are brought together
 
 struct Shared {
@@ -64,7 +50,7 @@ struct Shared {
     alignas(8) float2 sw[2][kAhead + 1];
     float sa[2][kAhead + 1][kRowsM + 1];
     int4 tile[2];                     // the tile that each scale buffer belongs to
-    float amax[kShares][kRowsM];      // swiglu: the shares' row maxima
+    float amax[2][kShares][kRowsM];   // swiglu: the shares' row maxima
     int first[EP_MAX_EXPERTS], count[EP_MAX_EXPERTS];
     int tiles[EP_MAX_EXPERTS + 1];    // exclusive scan of the experts' row tiles
 };
@@ -138,7 +124,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
             mbar_init(scale_full + 8 * i, 2);
             mbar_init(scale_empty + 8 * i, kAddWarps);
         }
-        mbar_init(swap, kAddThreads);
+        mbar_init(swap, kAddWarps);
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.gave_up = 0;
@@ -341,14 +327,13 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                     if (work) {
                         tc_fence_after();
                         const uint32_t from = lanes + buf * (kTileN / 8);
-                        uint32_t v[kBufs][kChunk];
-                        if (kBufs == 2) tmem_load(v[0], from);
+                        uint32_t v[2][kChunk];
+                        tmem_load(v[0], from);
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {
-                            if (kBufs == 1) tmem_load(v[0], from + column(c));
                             tmem_wait();
                             if (c + 1 < kChunks) {
-                                if (kBufs == 2) tmem_load(v[(c + 1) % kBufs], from + column(c + 1));
+                                tmem_load(v[(c + 1) & 1], from + column(c + 1));
                             } else {
                                 tc_fence_before();
                                 __syncwarp();
@@ -356,7 +341,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                             }
 #pragma unroll
                             for (int j = 0; j < kChunk / 2; ++j)
-                                fma2(acc[c * kChunk / 2 + j], v[c % kBufs][2 * j], v[c % kBufs][2 * j + 1],
+                                fma2(acc[c * kChunk / 2 + j], v[c & 1][2 * j], v[c & 1][2 * j + 1],
                                      c < kChunks / 2 ? p0 : p1);
                         }
                     } else if (lane == 0) {
@@ -392,16 +377,16 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                     h[2 * c + 1] = swiglu(hi2(acc[c]), hi2(acc[kH / 2 + c]));
                     amax = fmaxf(amax, fmaxf(fabsf(h[2 * c]), fabsf(h[2 * c + 1])));
                 }
-                sh.amax[share][r] = amax;
-                mbar_arrive(swap);
+                // the shares' maxima meet in shared memory, every other tile's in
+                // the other place: who writes there again has passed a barrier
+                // that all reach after reading
+                sh.amax[swaps & 1][share][r] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(swap);
                 if (!mbar_wait(swap, swaps & 1, gave_up)) break;
-                ++swaps;
                 float a = 1e-4f;
 #pragma unroll
-                for (int j = 0; j < kShares; ++j) a = fmaxf(a, sh.amax[j][r]);
-                // all have read the maxima before any writes the next tile's
-                mbar_arrive(swap);
-                if (!mbar_wait(swap, swaps & 1, gave_up)) break;
+                for (int j = 0; j < kShares; ++j) a = fmaxf(a, sh.amax[swaps & 1][j][r]);
                 ++swaps;
                 if (live) {
                     const float inv = __fdiv_rn(448.0f, a);
