@@ -13,3 +13,4 @@ from .binding import (  # noqa: F401
     combine_reduce, RankLayoutOut, EP_FLAG_BAD_EXPERT, EP_FLAG_OVERFLOW, EP_FLAG_BAD_ROW, EP_FLAG_TIMEOUT,
     EP_FLAG_BAD_LOGIT,
 )
+from .expert_layer import ExpertLayer  # noqa: F401

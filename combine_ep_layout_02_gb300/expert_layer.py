@@ -1,0 +1,53 @@
+"""A gated expert layer on one GPU, from the router's logits to the combined
+hidden states, through the calls of ``binding``:
+
+    route -> moe_few                                            up to 64 tokens
+    route -> layout_dispatch (FP8) -> group_gemm_swiglu_fp8
+          -> group_gemm_fp8 -> combine                          above
+
+Both paths cast x and the activated hidden rows to FP8 in the same way; the
+second also rounds every expert's output row to bf16 before the weighted sum.
+"""
+import torch
+
+from . import binding
+
+
+class ExpertLayer:
+    """Experts held as e4m3 codes with one float32 scale per 128 x 128 block:
+    ``w13_q`` [E, 2I, H] (gate rows, then up rows), ``w13_scale`` [E, 2I/128,
+    H/128], ``w2_q`` [E, H, I], ``w2_scale`` [E, H/128, I/128].  ``k`` experts
+    per token; the keyword arguments are ``binding.route``'s."""
+
+    def __init__(self, w13_q, w13_scale, w2_q, w2_scale, k, *, bias=None, groups=1, groups_per_token=None,
+                 scoring="softmax", renormalize=True, scale=1.0):
+        if w13_q.dim() != 3 or w2_q.dim() != 3 or w13_q.shape[1] != 2 * w2_q.shape[2]:
+            raise ValueError("w13_q must be [E, 2I, H] and w2_q [E, H, I]")
+        self.w13_q, self.w13_scale, self.w2_q, self.w2_scale = w13_q, w13_scale, w2_q, w2_scale
+        self.E, self.k = w13_q.shape[0], k
+        self.routing = dict(bias=bias, groups=groups, groups_per_token=groups_per_token, scoring=scoring,
+                            renormalize=renormalize, scale=scale)
+        # the device status word of every call made here (binding.status_read)
+        self.status = torch.zeros(1, dtype=torch.int32, device=w13_q.device)
+
+    def __call__(self, x, logits, out=None):
+        """x [T, H] bf16 and the router's logits [T, E] to out [T, H] bf16, on
+        the current stream."""
+        if logits.shape != (x.shape[0], self.E):
+            raise ValueError("logits must be [T, E]")
+        idx, w = binding.route(logits, self.k, status=self.status, **self.routing)
+        return self.experts(x, idx, w, out)
+
+    def experts(self, x, topk_idx, topk_w, out=None):
+        """The same for a route that is already at hand."""
+        if x.shape[0] <= binding.MOE_FEW_MAX_TOKENS:
+            return binding.moe_few(x, topk_idx, topk_w, self.w13_q, self.w13_scale, self.w2_q, self.w2_scale,
+                                   out=out, status=self.status)
+        # the layout zeroes the word that it is given, so it has one of its own
+        lay, q, s = binding.layout_dispatch(x, topk_idx, self.E, with_rank_counts=False, fp8=True)
+        at = (lay.expert_counts, lay.expert_offsets)
+        h, hs = binding.group_gemm_swiglu_fp8(q, s, self.w13_q, self.w13_scale, *at, status=self.status)
+        y = binding.group_gemm_fp8(h, hs, self.w2_q, self.w2_scale, *at, status=self.status)
+        out = binding.combine(y, topk_w, lay.dst_row, out=out, status=self.status)
+        self.status |= lay.status
+        return out
