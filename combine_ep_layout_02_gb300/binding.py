@@ -455,6 +455,13 @@ def _on_current(device, fn, *args):
         return fn(*args)
 
 
+def _want(name, t, dtype, device):
+    """``_check_dev``, with the checks that cost least first: the smallest calls
+    spend most of their time on the host."""
+    if t.dtype is not dtype or t.get_device() != device.index or not t.is_contiguous():
+        _check_dev(name, t, dtype, device)
+
+
 def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="softmax",
           renormalize=True, scale=1.0, topk_idx=None, topk_w=None, status=None):
     """Top-k experts of ``logits`` [T, E] (float32 or bf16) and their weights
@@ -470,17 +477,17 @@ def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="sof
     T, E = logits.shape
     dev = logits.device
     if bias is not None:
-        _check_dev("bias", bias, torch.float32, dev)
+        _want("bias", bias, torch.float32, dev)
         if tuple(bias.shape) != (E,):
             raise ValueError("bias must be [E]")
     if topk_idx is None:
         topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
     if topk_w is None:
         topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
-    for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32)):
-        _check_dev(name, t, dt, dev)
-        if tuple(t.shape) != (T, k):
-            raise ValueError("%s must be [T, k]" % name)
+    _want("topk_idx", topk_idx, torch.int32, dev)
+    _want("topk_w", topk_w, torch.float32, dev)
+    if topk_idx.shape != (T, k) or topk_w.shape != (T, k):
+        raise ValueError("topk_idx and topk_w must be [T, k]")
     _rc("ep_route", _on_current(
         dev, load().ep_route, logits.data_ptr(), LOGIT_TYPES[logits.dtype],
         None if bias is None else bias.data_ptr(), T, E, k, groups,
@@ -494,12 +501,12 @@ def _check_group_gemm(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets,
     """Types, devices and shapes of an expert product; returns (rows, K, E, weight rows)."""
     _check_dev("a_q", a_q, torch.uint8)
     dev = a_q.device
-    _check_dev("a_scale", a_scale, torch.float32, dev)
-    _check_dev("w_q", w_q, torch.uint8, dev)
-    _check_dev("w_scale", w_scale, torch.float32, dev)
-    _check_dev("expert_counts", expert_counts, torch.int32, dev)
+    _want("a_scale", a_scale, torch.float32, dev)
+    _want("w_q", w_q, torch.uint8, dev)
+    _want("w_scale", w_scale, torch.float32, dev)
+    _want("expert_counts", expert_counts, torch.int32, dev)
     if expert_offsets is not None:
-        _check_dev("expert_offsets", expert_offsets, torch.int32, dev)
+        _want("expert_offsets", expert_offsets, torch.int32, dev)
     if kind not in LAYOUT_KINDS:
         raise ValueError("kind must be one of %s" % ", ".join(sorted(LAYOUT_KINDS)))
     if a_q.dim() != 2 or w_q.dim() != 3:
@@ -528,7 +535,7 @@ def group_gemm_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, ki
     dev = a_q.device
     if out is None:
         out = torch.empty(rows, N, dtype=torch.bfloat16, device=dev)
-    _check_dev("out", out, torch.bfloat16, dev)
+    _want("out", out, torch.bfloat16, dev)
     if tuple(out.shape) != (rows, N):
         raise ValueError("out must be [rows, N]")
     _rc("ep_group_gemm_fp8", _on_current(
@@ -554,8 +561,8 @@ def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offs
         out_q = torch.empty(rows, inner, dtype=torch.uint8, device=dev)
     if out_scale is None:
         out_scale = torch.empty(rows, inner // 128, dtype=torch.float32, device=dev)
-    _check_dev("out_q", out_q, torch.uint8, dev)
-    _check_dev("out_scale", out_scale, torch.float32, dev)
+    _want("out_q", out_q, torch.uint8, dev)
+    _want("out_scale", out_scale, torch.float32, dev)
     if tuple(out_q.shape) != (rows, inner) or tuple(out_scale.shape) != (rows, inner // 128):
         raise ValueError("out_q must be [rows, I] and out_scale [rows, I/128]")
     _rc("ep_group_gemm_swiglu_fp8", _on_current(
@@ -584,7 +591,7 @@ def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, wor
     for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, torch.float32),
                         ("w13_q", w13_q, torch.uint8), ("w13_scale", w13_scale, torch.float32),
                         ("w2_q", w2_q, torch.uint8), ("w2_scale", w2_scale, torch.float32)):
-        _check_dev(name, t, dt, dev)
+        _want(name, t, dt, dev)
     T, H = x.shape
     k = topk_idx.shape[1]
     E, n, inner = w13_q.shape[0], w13_q.shape[1], w2_q.shape[2]
@@ -596,7 +603,7 @@ def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, wor
         raise ValueError("w13_scale must be [E, 2I/128, H/128] and w2_scale [E, H/128, I/128]")
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _check_dev("out", out, torch.bfloat16, dev)
+    _want("out", out, torch.bfloat16, dev)
     if out.shape != x.shape:
         raise ValueError("out must be [T, H]")
     if workspace is None:

@@ -2,6 +2,7 @@
 // Every check that can fail happens before anything is enqueued.
 #include <stdint.h>
 
+#include "ep_experts.cuh"
 #include "ep_internal.cuh"
 
 namespace {

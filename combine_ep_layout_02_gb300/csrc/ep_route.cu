@@ -20,7 +20,7 @@
 // the warp find the choices instead.
 //
 // Bound by the ALU: MEASURED_ROUTE.
-#include "ep_internal.cuh"
+#include "ep_experts.cuh"
 
 namespace ep {
 namespace {

@@ -6,7 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "ep_internal.cuh"
+#include "ep_experts.cuh"
 
 namespace ep {
 

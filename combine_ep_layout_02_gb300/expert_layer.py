@@ -5,8 +5,10 @@ hidden states, through the calls of ``binding``:
     route -> layout_dispatch (FP8) -> group_gemm_swiglu_fp8
           -> group_gemm_fp8 -> combine                          above
 
-Both paths cast x and the activated hidden rows to FP8 in the same way; the
-second also rounds every expert's output row to bf16 before the weighted sum.
+Both paths cast x and the activated hidden rows to FP8, x with quotients that
+differ in the last bit (a code may differ by one where a value lies between
+two); the second also rounds every expert's output row to bf16 before the
+weighted sum.
 """
 import torch
 

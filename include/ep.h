@@ -392,13 +392,15 @@ EP_API int ep_combine_fp8(const uint8_t* y_q, const float* y_scale, const float*
  * in two kernels (the low-latency end of the Decode-like profile, where a
  * token's experts' weights are read for one or a few rows each): no dispatch
  * buffer, no layout.  For token t:
- *     x8     = the FP8 cast of x[t] (ep_dispatch_fp8's)
+ *     x8     = the FP8 cast of x[t]: ep_dispatch_fp8's, with the quotient
+ *              inv = fl32(fl32(1 / a') * 448)
  *     h8_j   = the FP8 cast of SwiGLU of the first product of expert
  *              e = topk_idx[t, j] (ep_group_gemm_swiglu_fp8's)
  *     y_j    = its second product (ep_group_gemm_fp8's) in fp32, not rounded
  *     out[t] = bf16_rne( sum over j with a valid expert of topk_w[t, j] * y_j )
  * which is the chain dispatch_fp8, group_gemm_swiglu_fp8, group_gemm_fp8,
- * combine without the bf16 rounding of each y_j.  All sums are held in fp32
+ * combine without the bf16 rounding of each y_j; codes of x also differ by one
+ * where x * 448 / a' is the midpoint of two (the chain rounds it once).  All sums are held in fp32
  * in a fixed order: the same inputs give the same bits.  An id of -1 is a
  * dropped pair; other ids outside [0, E) are skipped and raise
  * EP_FLAG_BAD_EXPERT.  A token without a valid pair gives +0.

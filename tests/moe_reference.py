@@ -40,16 +40,16 @@ def weights64(q, scale):
     return decode(q) * s[..., : q.shape[-2], :]
 
 
-def quantise_f32(x):
+def quantise_f32(x, reciprocal=False):
     """The FP8 cast of bf16 or float32 rows by its fp32 definition: (the codes'
-    values as float64; scales float32).  Both divisions are of two tensors:
-    with a Python number on either side torch multiplies by a reciprocal,
-    which is not the IEEE quotient."""
+    values as float64; scales float32).  448 / amax is the IEEE quotient of
+    two tensors, or with `reciprocal` 1 / amax times 448, each rounded."""
     f = x.float()
     b = f.view(*f.shape[:-1], -1, 128)
     a = b.abs().amax(-1).clamp_min(1e-4)
     c = torch.full_like(a, 448.0)
-    v = (b * (c / a).unsqueeze(-1)).clamp(-448.0, 448.0)
+    inv = (torch.ones_like(a) / a) * 448.0 if reciprocal else c / a
+    v = (b * inv.unsqueeze(-1)).clamp(-448.0, 448.0)
     return v.to(torch.float8_e4m3fn).double().view(f.shape), a / c
 
 

@@ -29,14 +29,14 @@ def problem(T, H, I, E, k, seed, idx=None):
                 w2_q=random_codes((E, H, I), g), w2_scale=sc(E, H // 128, I // 128) / 100 * I ** -0.5)
 
 
-def expected(p):
-    """(out in 64 bits, bound): the fp32 errors of both products, of SwiGLU and
+def expected(p, reciprocal=True):
+    """(out in 64 bits, bound), x cast as ep_moe_few or as ep_dispatch_fp8 does: the fp32 errors of both products, of SwiGLU and
     of the sum over experts, and what the cast of h can be off where they move
     a value across a midpoint of e4m3 (carried through |w2|)."""
     T, H = p["x"].shape
     I = p["w2_q"].shape[2]
     E = p["w2_q"].shape[0]
-    xq, xs = ref.quantise_f32(p["x"])
+    xq, xs = ref.quantise_f32(p["x"], reciprocal)
     x = xq * xs.double().repeat_interleave(128, dim=1)
     out = torch.zeros(T, H, dtype=torch.float64, device=DEV)
     err, mag = torch.zeros_like(out), torch.zeros_like(out)
@@ -124,13 +124,14 @@ def test_agrees_with_the_chain():
     y = ep.group_gemm_fp8(hq, hs, p["w2_q"], p["w2_scale"], lay.expert_counts, lay.expert_offsets)
     chain = ep.combine(y, p["topk_w"], lay.dst_row)
     got = ep.moe_few(**p)
-    # Both hold `expected`'s bound; the chain also rounds each y to bf16
-    # (2^-8 of it) before the weighted sum.
-    want, err = expected(p)
+    # Both hold `expected`'s bound for their cast of x; the chain also rounds
+    # each y to bf16 (2^-8 of it) before the weighted sum.
+    want, err = expected(p, reciprocal=False)
     ysum = torch.zeros(T, H, dtype=torch.float64, device=DEV)
     for j in range(k):
         ysum += p["topk_w"][:, j:j + 1].double().abs() * y[lay.dst_row[:, j].long()].double().abs()
     assert ((chain.double() - want).abs() <= 2.0 ** -8 * (want.abs() + ysum * 1.01 + err) + err).all()
+    want, err = expected(p)
     assert ((got.double() - want).abs() <= 2.0 ** -8 * (want.abs() + err) + err).all()
 
 
