@@ -17,9 +17,11 @@
 // Both kernels are a ring of TMA stages in shared memory, filled by one warp
 // as far ahead as the ring reaches, across items, and emptied by the others.
 //   up: a stage is one block of K of 128 gate and 128 up rows (32 KB).  Each
-//   of 16 warps owns 8 channels: its tile is their 8 gate and 8 up rows, so
-//   that a lane's accumulators are the gate and up values of the same h, and
-//   the FP8 cast of the 128 channels needs only the warps' maxima.
+//   of 8 warps owns 16 channels as two tiles of 8 gate and the same 8 up rows,
+//   so that a lane's accumulators are the gate and up values of the same h,
+//   and the FP8 cast of the 128 channels needs only the warps' maxima.  Where
+//   the tokens leave room two blocks share an SM, and one streams while the
+//   other casts x or writes h.
 //   down: a block owns 16 output channels for all groups; a stage is eight
 //   blocks of K of one group's 16 weight rows (16 KB) with its tokens' codes
 //   and scales.  The warps take the stages in turn, each adds its weighted
@@ -38,6 +40,13 @@ namespace {
 constexpr int kCols = 8;  // tokens per group: columns of one MMA
 constexpr int kMaxPairs = EP_MOE_FEW_MAX_TOKENS * EP_MAX_TOPK;
 constexpr int kSmemLimit = 227 * 1024;
+constexpr int kSmemHalf = 113 * 1024;  // of two blocks on an SM
+
+// h between the kernels: per pair and eight blocks of 128 channels a record of
+// their codes and their scales, one copy for a stage of the down kernel.
+constexpr int kRecordBlocks = 8;
+constexpr int kRecordScales = kRecordBlocks * 128;            // bytes before the scales
+constexpr int kRecord = kRecordScales + kRecordBlocks * 4;
 
 // The groups of a route, built by every block for itself.
 struct Groups {
@@ -190,11 +199,13 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
 struct Operands {
     uint32_t a[4][4], b[8];
 };
-__device__ __forceinline__ void load_operands(Operands& o, uint32_t a_row, uint32_t b_row) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t r = lane & 7, hi = lane >> 4, quad = lane >> 3;
+__device__ __forceinline__ void load_tokens(Operands& o, uint32_t b_row) {
+    const uint32_t quad = (threadIdx.x & 31) >> 3;
     load_matrices(*reinterpret_cast<uint32_t(*)[4]>(o.b), b_row + quad * 16);
     load_matrices(*reinterpret_cast<uint32_t(*)[4]>(o.b + 4), b_row + 64 + quad * 16);
+}
+__device__ __forceinline__ void load_weights(Operands& o, uint32_t a_row) {
+    const uint32_t lane = threadIdx.x & 31, r = lane & 7, hi = lane >> 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) load_matrices(o.a[j], a_row + (((2 * j + hi) ^ r) << 4));
 }
@@ -273,7 +284,8 @@ __device__ __forceinline__ Fp8Group cast16(const uint4& lo, const uint4& hi) {
     return Fp8Group{make_uint4(q[0], q[1], q[2], q[3]), __fdiv_rn(a, 448.0f)};
 }
 
-constexpr int kUpWarps = 16;
+constexpr int kUpWarps = 8;
+constexpr int kUpTiles = 16 / kUpWarps;  // of 8 channels, per warp
 constexpr int kUpStage = 2 * 128 * 128;  // one block of K of 128 gate and 128 up rows
 constexpr int kUpMaxStages = 6;
 
@@ -281,18 +293,17 @@ struct UpShared {
     uint64_t full[kUpMaxStages], empty[kUpMaxStages], sync;
     int gave_up;
     uint64_t part_full;
-    float amax[2][kUpWarps][kCols];  // [item parity][warp][column]
+    float amax[2][kCols][kUpWarps];  // [item parity][column][warp]
     Groups g;
 };
 
 // C > 1: the C blocks of a cluster share each item's channels of K and the
 // first adds the others' sums in order; every cluster has at most one item.
 template <int C>
-__global__ void __launch_bounds__((kUpWarps + 1) * 32, 1)
+__global__ void __launch_bounds__((kUpWarps + 1) * 32, 2)
 few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restrict__ x, int T,
               int H, int k, const int32_t* __restrict__ topk_idx, const float* __restrict__ s13,
-              int I, int E, int stages, uint8_t* __restrict__ hq, float* __restrict__ hs,
-              int hs_stride, uint32_t* __restrict__ status) {
+              int I, int E, int stages, uint8_t* __restrict__ h8, uint32_t* __restrict__ status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* xq = ring + stages * kUpStage;
@@ -300,7 +311,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     const int held = min(T, kCols);
     UpShared& sh = *reinterpret_cast<UpShared*>(xq + held * stride);  // 16-byte aligned
     float* xs = reinterpret_cast<float*>(&sh + 1);
-    // C > 1: the other blocks' sums [C - 1][warp][lane]
+    // C > 1: the other blocks' sums [C - 1][warp][tile][lane]
     float4* part = reinterpret_cast<float4*>(((uintptr_t)(xs + held * (H / 128)) + 15) & ~(uintptr_t)15);
     const int nk = H / 128, nb = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -349,7 +360,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
         WarpsBarrier barrier{smem_addr(&sh.sync)};
         const int row = lane >> 2, q4 = lane & 3;
         // matrices 0 and 2: this warp's gate rows, 1 and 3: its up rows
-        const uint32_t a_lane = smem_addr(ring) + ((lane >> 3) & 1) * (kUpStage / 2) + (warp * 8 + (lane & 7)) * 128;
+        const uint32_t a_lane = smem_addr(ring) + ((lane >> 3) & 1) * (kUpStage / 2) + (warp * 8 * kUpTiles + (lane & 7)) * 128;
         const uint32_t b_lane = smem_addr(xq) + min(lane & 7, held - 1) * stride;
         const float* x0 = xs + min(2 * q4, held - 1) * nk;  // the scales of this lane's two tokens
         const float* x1 = xs + min(2 * q4 + 1, held - 1) * nk;
@@ -361,13 +372,11 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
             const float* sg = s13 + ((int64_t)sh.g.expert[grp] * 2 * nb + b) * nk;
             const float* su = sg + (int64_t)nb * nk;
             if (grp != have) {
-                if (!(ok = barrier.sync(gave_up))) break;  // the previous group's reads are done
-                // one warp per token and half of its channels
-                const int t = sh.g.pair[first + min(warp >> 1, n - 1)] / k;
-                if ((warp >> 1) < n) {
-                    const uint16_t* src = x + (int64_t)t * H;
-                    uint8_t* to = xq + (warp >> 1) * stride;
-                    for (int c0 = k0 * 128 + (warp & 1) * 1024; c0 < k1 * 128; c0 += 2048) {
+                // the previous group's reads are done: all warps met at the maxima since
+                for (int tok = warp; tok < n; tok += kUpWarps) {
+                    const uint16_t* src = x + (int64_t)(sh.g.pair[first + tok] / k) * H;
+                    uint8_t* to = xq + tok * stride;
+                    for (int c0 = k0 * 128; c0 < k1 * 128; c0 += 1024) {
                         uint4 a[2], q[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
@@ -384,7 +393,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                             const Fp8Group f = cast16(a[u], q[u]);
                             if (c < k1 * 128) {
                                 *reinterpret_cast<uint4*>(to + c) = f.q;
-                                if ((lane & 7) == 0) xs[(warp >> 1) * nk + (c >> 7)] = f.sf;
+                                if ((lane & 7) == 0) xs[tok * nk + (c >> 7)] = f.sf;
                             }
                         }
                     }
@@ -392,7 +401,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 have = grp;
                 if (!(ok = barrier.sync(gave_up))) break;
             }
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float acc[kUpTiles][4] = {};
             float vg = 0.0f, vu = 0.0f;  // the weights' scales, a block per lane
             for (int kb = k0; kb < k1; ++kb) {
                 if ((kb - k0) % 32 == 0) {
@@ -401,10 +410,18 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                     vu = __ldg(su + to);
                 }
                 if (!(ok = mbar_wait(full + 8 * s, phase, gave_up))) break;
-                Operands o;
-                load_operands(o, a_lane + s * kUpStage, b_lane + kb * 128);
-                float p[4];
-                block_product(p, o);
+                Operands o[kUpTiles];
+                float p[kUpTiles][4];
+                load_tokens(o[0], b_lane + kb * 128);
+#pragma unroll
+                for (int j = 0; j < kUpTiles; ++j) {
+                    if (j > 0)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[j].b[i] = o[0].b[i];
+                    load_weights(o[j], a_lane + s * kUpStage + j * 8 * 128);
+                }
+#pragma unroll
+                for (int j = 0; j < kUpTiles; ++j) block_product(p[j], o[j]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + 8 * s);
                 if (++s == (uint32_t)stages) {
@@ -414,18 +431,25 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 const float wg = __shfl_sync(kFullMask, vg, (kb - k0) % 32);
                 const float wu = __shfl_sync(kFullMask, vu, (kb - k0) % 32);
                 const float c0 = x0[kb], c1 = x1[kb];
-                acc[0] = __fmaf_rn(p[0], __fmul_rn(c0, wg), acc[0]);
-                acc[1] = __fmaf_rn(p[1], __fmul_rn(c1, wg), acc[1]);
-                acc[2] = __fmaf_rn(p[2], __fmul_rn(c0, wu), acc[2]);
-                acc[3] = __fmaf_rn(p[3], __fmul_rn(c1, wu), acc[3]);
+#pragma unroll
+                for (int j = 0; j < kUpTiles; ++j) {
+                    acc[j][0] = __fmaf_rn(p[j][0], __fmul_rn(c0, wg), acc[j][0]);
+                    acc[j][1] = __fmaf_rn(p[j][1], __fmul_rn(c1, wg), acc[j][1]);
+                    acc[j][2] = __fmaf_rn(p[j][2], __fmul_rn(c0, wu), acc[j][2]);
+                    acc[j][3] = __fmaf_rn(p[j][3], __fmul_rn(c1, wu), acc[j][3]);
+                }
             }
             if (!ok) break;
             if (C > 1) {
                 if (rank > 0) {  // hand the sums to the cluster's first block: nothing else to do
-                    const uint32_t to = cluster_addr(smem_addr(part + ((rank - 1) * kUpWarps + warp) * 32 + lane), 0);
-                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(acc[0]),
-                                 "f"(acc[1]), "f"(acc[2]), "f"(acc[3])
-                                 : "memory");
+#pragma unroll
+                    for (int j = 0; j < kUpTiles; ++j) {
+                        const uint32_t to = cluster_addr(
+                            smem_addr(part + (((rank - 1) * kUpWarps + warp) * kUpTiles + j) * 32 + lane), 0);
+                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(acc[j][0]),
+                                     "f"(acc[j][1]), "f"(acc[j][2]), "f"(acc[j][3])
+                                     : "memory");
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_addr(&sh.part_full), 0));
                     break;
@@ -433,25 +457,30 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 if (!(ok = mbar_wait_cluster(smem_addr(&sh.part_full), 0, gave_up))) break;
 #pragma unroll
                 for (int r = 0; r < C - 1; ++r) {
-                    const float4 v = part[(r * kUpWarps + warp) * 32 + lane];
-                    acc[0] = __fadd_rn(acc[0], v.x);
-                    acc[1] = __fadd_rn(acc[1], v.y);
-                    acc[2] = __fadd_rn(acc[2], v.z);
-                    acc[3] = __fadd_rn(acc[3], v.w);
+#pragma unroll
+                    for (int j = 0; j < kUpTiles; ++j) {
+                        const float4 v = part[((r * kUpWarps + warp) * kUpTiles + j) * 32 + lane];
+                        acc[j][0] = __fadd_rn(acc[j][0], v.x);
+                        acc[j][1] = __fadd_rn(acc[j][1], v.y);
+                        acc[j][2] = __fadd_rn(acc[j][2], v.z);
+                        acc[j][3] = __fadd_rn(acc[j][3], v.w);
+                    }
                 }
             }
-            float h[2], m[2];
+            float h[kUpTiles][2], m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                h[i] = swiglu(acc[i], acc[2 + i]);
-                m[i] = fabsf(h[i]);
-                m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], 4));
-                m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], 8));
-                m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], 16));
+#pragma unroll
+                for (int j = 0; j < kUpTiles; ++j) {
+                    h[j][i] = swiglu(acc[j][i], acc[j][2 + i]);
+                    m[i] = fmaxf(m[i], fabsf(h[j][i]));
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(kFullMask, m[i], o));
             }
             if (lane < 4) {
-                sh.amax[parity][warp][2 * lane] = m[0];
-                sh.amax[parity][warp][2 * lane + 1] = m[1];
+                sh.amax[parity][2 * lane][warp] = m[0];
+                sh.amax[parity][2 * lane + 1][warp] = m[1];
             }
             if (!(ok = barrier.sync(gave_up))) break;
 #pragma unroll
@@ -459,13 +488,18 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 const int col = 2 * q4 + i;
                 float a = 1e-4f;
 #pragma unroll
-                for (int w = 0; w < kUpWarps; ++w) a = fmaxf(a, sh.amax[parity][w][col]);
+                for (int w = 0; w < kUpWarps; ++w) a = fmaxf(a, sh.amax[parity][col][w]);
                 if (col < n) {
                     const int pair = sh.g.pair[first + col];
                     const float inv = __fdiv_rn(448.0f, a);
-                    hq[(int64_t)pair * I + b * 128 + warp * 8 + row] =
-                        (uint8_t)cvt_e4m3x2_rn_sat(__fmul_rn(h[i], inv), 0.0f);
-                    if (warp == 0 && row == 0) hs[(int64_t)pair * hs_stride + b] = __fdiv_rn(a, 448.0f);
+                    uint8_t* record = h8 + ((int64_t)pair * ((nb + kRecordBlocks - 1) / kRecordBlocks) +
+                                            b / kRecordBlocks) * kRecord;
+                    uint8_t* to = record + b % kRecordBlocks * 128 + warp * 8 * kUpTiles + row;
+#pragma unroll
+                    for (int j = 0; j < kUpTiles; ++j)
+                        to[j * 8] = (uint8_t)cvt_e4m3x2_rn_sat(__fmul_rn(h[j][i], inv), 0.0f);
+                    if (warp == 0 && row == 0)
+                        reinterpret_cast<float*>(record + kRecordScales)[b % kRecordBlocks] = __fdiv_rn(a, 448.0f);
                 }
             }
             parity ^= 1;  // the next item's maxima go to the other buffer
@@ -480,7 +514,7 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
 template <int C>
 cudaError_t launch_up(int blocks, size_t smem, cudaStream_t stream, const CUtensorMap& w_map, const void* x,
                       int T, int H, int k, const int32_t* topk_idx, const float* s13, int I, int E, int stages,
-                      uint8_t* hq, float* hs, int hs_stride, uint32_t* status) {
+                      uint8_t* h8, uint32_t* status) {
     static std::atomic<uint64_t> configured{0};
     const cudaError_t err = raise_smem_limit(few_up_kernel<C>, kSmemLimit, configured);
     if (err != cudaSuccess) return err;
@@ -497,7 +531,7 @@ cudaError_t launch_up(int blocks, size_t smem, cudaStream_t stream, const CUtens
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, few_up_kernel<C>, w_map, static_cast<const uint16_t*>(x), T, H, k,
-                              topk_idx, s13, I, E, stages, hq, hs, hs_stride, status);
+                              topk_idx, s13, I, E, stages, h8, status);
 }
 
 
@@ -506,11 +540,11 @@ cudaError_t launch_up(int blocks, size_t smem, cudaStream_t stream, const CUtens
 constexpr int kDownWarps = 6;
 constexpr int kDownStages = kDownWarps;           // a warp's stages always lie in the same place
 constexpr int kDownRows = 16;                     // output channels of a block
-constexpr int kDownBlocks = 8;                    // blocks of K of a stage
+constexpr int kDownBlocks = kRecordBlocks;        // blocks of K of a stage
 constexpr int kDownW = kDownRows * kDownBlocks * 128;
-constexpr int kTokenRow = kDownBlocks * 128 + 16;  // a token's codes, padded against bank conflicts
-constexpr int kScaleRow = kDownBlocks;            // its scales
-constexpr int kDownStage = (kDownW + kCols * kTokenRow + kCols * kScaleRow * 4 + 1023) / 1024 * 1024;
+constexpr int kTokenRow = kRecord + 16;           // an odd number of 16 bytes: eight rows' chunks meet all banks
+constexpr int kDownStage = (kDownW + kCols * kTokenRow + 1023) / 1024 * 1024;
+static_assert(kTokenRow / 16 % 2 == 1 && kRecord % 16 == 0, "");
 
 struct DownShared {
     uint64_t full[kDownStages], empty[kDownStages], sync;
@@ -526,8 +560,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 __global__ void __launch_bounds__((kDownWarps + 2) * 32, 1)
-few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ hq,
-                const float* __restrict__ hs, int hs_stride, int T, int H, int k,
+few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ h8, int T, int H, int k,
                 const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
                 const float* __restrict__ s2, int I, int E, uint16_t* __restrict__ out,
                 uint32_t* __restrict__ status) {
@@ -569,7 +602,7 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                     if (!(ok = fill.wait(gave_up))) break;
                     if (elect_one()) {
                         const uint32_t bar = full + 8 * fill.s;
-                        mbar_expect_tx(bar, kDownW + tokens * (min(kDownBlocks, nk - b0) * 128 + kScaleRow * 4));
+                        mbar_expect_tx(bar, kDownW + tokens * kRecord);
                         tma_load_3d(smem_addr(ring) + fill.s * kDownStage, &w_map, 0, wrow, b0, bar);
                     }
                     __syncwarp();
@@ -579,31 +612,27 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
         }
         if (!ok) fill.drain();
     } else if (warp == kDownWarps + 1) {
-        // ---- h: a stage's tokens' codes and scales, one lane each
+        // ---- h: a stage's tokens' records, one lane each
         pdl_wait();
         asm volatile("fence.proxy.async.global;" ::: "memory");
         Fill fill{full, empty, (uint32_t)kDownStages};
         bool ok = true;
+        const int records = (nk + kRecordBlocks - 1) / kRecordBlocks;
         const uint32_t to = smem_addr(ring) + kDownW + lane * kTokenRow;
-        const uint32_t to_s = smem_addr(ring) + kDownW + kCols * kTokenRow + lane * kScaleRow * 4;
-        int64_t pair = -1;  // this lane's pair of the group to come
-        auto look = [&](int grp) {
-            pair = grp < groups && lane < sh.g.size[grp] ? sh.g.pair[sh.g.first[grp] + lane] : -1;
+        // this lane's records of a group, if it has any
+        auto look = [&](int grp) -> const uint8_t* {
+            return grp < groups && lane < sh.g.size[grp]
+                       ? h8 + (int64_t)sh.g.pair[sh.g.first[grp] + lane] * records * kRecord
+                       : nullptr;
         };
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            look(0);
+            const uint8_t* next = look(0);
             for (int grp = 0; grp < groups && ok; ++grp) {
-                const bool mine = pair >= 0;
-                const uint8_t* q = hq + pair * I;
-                const float* c = hs + pair * hs_stride;
-                look(grp + 1);
-                for (int b0 = 0; b0 < nk; b0 += kDownBlocks) {
+                const uint8_t* src = next;
+                next = look(grp + 1);
+                for (int i = 0; i < records; ++i) {
                     if (!(ok = fill.wait(gave_up))) break;
-                    if (mine) {
-                        const uint32_t at = fill.s * kDownStage, bar = full + 8 * fill.s;
-                        bulk_load(to + at, q + b0 * 128, min(kDownBlocks, nk - b0) * 128, bar);
-                        bulk_load(to_s + at, c + b0, kScaleRow * 4, bar);
-                    }
+                    if (src) bulk_load(to + fill.s * kDownStage, src + i * kRecord, kRecord, full + 8 * fill.s);
                     __syncwarp();
                     fill.next();
                 }
@@ -618,7 +647,7 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
         const int row = lane >> 2, q4 = lane & 3;
         const uint32_t a_lane = smem_addr(ring) + (lane & 15) * 128;
         const uint32_t b_lane = smem_addr(ring) + kDownW + (lane & 7) * kTokenRow;
-        const uint8_t* c_lane = ring + kDownW + kCols * kTokenRow + 2 * q4 * kScaleRow * 4;  // two tokens' scales
+        const uint8_t* c_lane = ring + kDownW + 2 * q4 * kTokenRow + kRecordScales;  // the first of two tokens' scales
         float* slab = slabs + warp * slab_n;
         const int per_group = (nk + kDownBlocks - 1) / kDownBlocks;  // stages
         const uint32_t per_tile = groups * per_group;
@@ -663,15 +692,20 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const uint32_t a = a_lane + s * kDownStage, t = b_lane + s * kDownStage;
                 const float* c = reinterpret_cast<const float*>(c_lane + s * kDownStage);
+                Operands o[2];  // the next block's operands are read behind this one's MMAs
+                load_tokens(o[0], t);
+                load_weights(o[0], a);
 #pragma unroll
                 for (int j = 0; j < kDownBlocks; ++j) {
                     if (now.b0 + j < nk) {  // warp-uniform
-                        Operands o;
-                        load_operands(o, a + j * kDownRows * 128, t + j * 128);
+                        if (j + 1 < kDownBlocks) {  // past the last block: what lies there, not used
+                            load_tokens(o[(j + 1) & 1], t + (j + 1) * 128);
+                            load_weights(o[(j + 1) & 1], a + (j + 1) * kDownRows * 128);
+                        }
                         float p[4];
-                        block_product(p, o);
+                        block_product(p, o[j & 1]);
                         const float w = __shfl_sync(kFullMask, now.scale, j);
-                        const float c0 = __fmul_rn(c[j], w), c1 = __fmul_rn(c[kScaleRow + j], w);
+                        const float c0 = __fmul_rn(c[j], w), c1 = __fmul_rn(c[kTokenRow / 4 + j], w);
                         acc[0] = __fmaf_rn(p[0], c0, acc[0]);
                         acc[1] = __fmaf_rn(p[1], c1, acc[1]);
                         acc[2] = __fmaf_rn(p[2], c0, acc[2]);
@@ -730,7 +764,7 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
 size_t up_rest(int T, int H, int C) {  // shared memory besides the ring
     const int held = T < kCols ? T : kCols;
     return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4 +
-           (C > 1 ? 16 + (size_t)(C - 1) * kUpWarps * 32 * 16 : 0);
+           (C > 1 ? 16 + (size_t)(C - 1) * kUpWarps * kUpTiles * 32 * 16 : 0);
 }
 size_t down_smem(int T) {
     return 1024 + (size_t)kDownStages * kDownStage + (size_t)kDownWarps * T * kDownRows * 4 + sizeof(DownShared);
@@ -741,13 +775,10 @@ static_assert(1024 + kCols * (EP_MOE_FEW_MAX_WIDTH + 16) + sizeof(UpShared) +
 static_assert(1024 + kDownStages * kDownStage + kDownWarps * EP_MOE_FEW_MAX_TOKENS * kDownRows * 4 +
                       sizeof(DownShared) <= kSmemLimit, "");
 
-int hs_stride_of(int I) { return (I / 128 + 7) / 8 * 8; }  // a stage's scales are copied as whole 32 bytes
-
 }  // namespace
 
-size_t moe_few_h_bytes(int64_t T, int k, int I) { return ((size_t)T * k * I + 255) / 256 * 256; }
 size_t moe_few_bytes(int64_t T, int k, int I) {
-    return moe_few_h_bytes(T, k, I) + ((size_t)T * k * hs_stride_of(I) * 4 + 255) / 256 * 256;
+    return ((size_t)T * k * ((I / 128 + kRecordBlocks - 1) / kRecordBlocks) * kRecord + 255) / 256 * 256;
 }
 
 cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* topk_idx,
@@ -758,9 +789,7 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     static std::atomic<int> sm_cache[64];
     int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
     if (sms <= 0) sms = 1;
-    uint8_t* hq = static_cast<uint8_t*>(workspace);
-    float* hs = reinterpret_cast<float*>(hq + moe_few_h_bytes(T, k, I));
-    const int hs_stride = hs_stride_of(I);
+    uint8_t* h8 = static_cast<uint8_t*>(workspace);
 
     CUtensorMap w13_map, w2_map;
     cudaError_t err = byte_matrix_map(&w13_map, w13, (int64_t)E * 2 * I, H, 128);
@@ -773,12 +802,14 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     // One token, H = 2048, I = 1024, k = 8, 64 items: MEASURED_SPLIT.
     const int C = H > 8192 || H < 1024 ? 1 : items * 4 <= sms ? 4 : items * 2 <= sms ? 2 : 1;
     const size_t rest = up_rest(T, H, C);
-    int stages = (int)((kSmemLimit - rest) / kUpStage);
+    // Two blocks per SM where each has at least two stages and an item.
+    const int per_sm = C == 1 && items > sms && rest + 2 * kUpStage <= kSmemHalf ? 2 : 1;
+    int stages = (int)(((per_sm == 2 ? kSmemHalf : kSmemLimit) - rest) / kUpStage);
     if (stages > kUpMaxStages) stages = kUpMaxStages;
-    const int blocks = C > 1 ? (int)items * C : (int)(items < sms ? items : sms);
+    const int blocks = C > 1 ? (int)items * C : (int)(items < sms * per_sm ? items : sms * per_sm);
     const auto up = C == 4 ? launch_up<4> : C == 2 ? launch_up<2> : launch_up<1>;
     err = up(blocks, rest + (size_t)stages * kUpStage, stream, w13_map, x, T, H, k, topk_idx, s13, I, E, stages,
-             hq, hs, hs_stride, status);
+             h8, status);
     if (err != cudaSuccess) return err;
 
     const int tiles = H / kDownRows;
@@ -788,7 +819,7 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     err = raise_smem_limit(few_down_kernel, kSmemLimit, configured);
     if (err != cudaSuccess) return err;
     return launch_pdl(few_down_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                      dim3((kDownWarps + 2) * 32), down_smem(T), stream, w2_map, hq, hs, hs_stride, T,
+                      dim3((kDownWarps + 2) * 32), down_smem(T), stream, w2_map, h8, T,
                       H, k, topk_idx, topk_w, s2, I, E, static_cast<uint16_t*>(out), status);
 }
 
