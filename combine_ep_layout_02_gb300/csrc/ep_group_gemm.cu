@@ -22,6 +22,18 @@
 // to the other two, which need 128 for the sums alone.
 #include "ep_tcgen05.cuh"
 
+//
+// Few rows per expert: bound by the weights' bytes (64 rows each, 256 experts:
+// 590 us and 1.12 ms, 6.8 TB/s, at the copy rate).  Many rows: the tensor pipe
+// is busy 58 % of the cycles (8,192 rows per 32 experts, K = 7168: 430 us, 2.2
+// PFLOP/s).  What a block's sum needs in turn limits it: 512 cycles of MMAs, 300
+// until the adding warps see them, 450 to read and add, and two sums in flight
+// because two are all that TMEM holds.  Long calls also meet the power limit
+// (1.45 GHz after some milliseconds, 1.7 GHz at first).  Measured and not
+// taken: a pair of SMs per 256 x 256 tile (464 against 444 us; half of the
+// weight traffic, but rows are padded to 256 and each hand-over crosses the
+// SMs), 16 adding warps (476), the two halves of N as separate MMAs (538: A is
+// read twice from shared memory), 32 columns per TMEM load (461).
 namespace ep {
 namespace {
 

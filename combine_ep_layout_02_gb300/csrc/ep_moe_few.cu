@@ -27,6 +27,13 @@
 //   and scales.  The warps take the stages in turn, each adds its weighted
 //   results per token in shared memory of its own, and the block adds the
 //   warps' sums in order: the result never depends on timing.
+// Measured (L2 cold, against the weights' bytes at the copy rate): 8 tokens,
+// H = 7168, I = 2048, 256 experts: 386 us, 6.5 TB/s, bound by DRAM; 45 tokens,
+// H = 2048, I = 1024, 128 experts: 149 us, 5.1 TB/s, bound by the per-item
+// work of the up blocks and by the down stages' latency (shared-memory
+// operands, 6 stages in flight); one token there: 20 us, 2.5 TB/s, bound by the
+// two kernels' start-up and hand-over (about 10 us) beside 7.5 us of weights.
+//
 // An SM can draw more than twice its share of the memory's bandwidth, so that
 // neither kernel needs its items to divide evenly over the SMs.  Only where
 // there are fewer items than half the SMs do clusters of blocks share one.
@@ -618,23 +625,30 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
         Fill fill{full, empty, (uint32_t)kDownStages};
         bool ok = true;
         const int records = (nk + kRecordBlocks - 1) / kRecordBlocks;
-        const uint32_t to = smem_addr(ring) + kDownW + lane * kTokenRow;
-        // this lane's records of a group, if it has any
+        // four groups at a look: lane 8 g + c has the records of column c of group g
+        const uint32_t to = smem_addr(ring) + kDownW + (lane & 7) * kTokenRow;
         auto look = [&](int grp) -> const uint8_t* {
-            return grp < groups && lane < sh.g.size[grp]
-                       ? h8 + (int64_t)sh.g.pair[sh.g.first[grp] + lane] * records * kRecord
+            grp += lane >> 3;
+            return grp < groups && (lane & 7) < sh.g.size[grp]
+                       ? h8 + (int64_t)sh.g.pair[sh.g.first[grp] + (lane & 7)] * records * kRecord
                        : nullptr;
         };
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             const uint8_t* next = look(0);
-            for (int grp = 0; grp < groups && ok; ++grp) {
+            for (int grp0 = 0; grp0 < groups && ok; grp0 += 4) {
                 const uint8_t* src = next;
-                next = look(grp + 1);
-                for (int i = 0; i < records; ++i) {
+                next = look(grp0 + 4);
+                const int n = min(4, groups - grp0) * records;
+                for (int i = 0, g = 0, r = 0; i < n; ++i) {
                     if (!(ok = fill.wait(gave_up))) break;
-                    if (src) bulk_load(to + fill.s * kDownStage, src + i * kRecord, kRecord, full + 8 * fill.s);
+                    if (src && (lane >> 3) == g)
+                        bulk_load(to + fill.s * kDownStage, src + r * kRecord, kRecord, full + 8 * fill.s);
                     __syncwarp();
                     fill.next();
+                    if (++r == records) {
+                        r = 0;
+                        ++g;
+                    }
                 }
             }
         }
@@ -692,24 +706,36 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const uint32_t a = a_lane + s * kDownStage, t = b_lane + s * kDownStage;
                 const float* c = reinterpret_cast<const float*>(c_lane + s * kDownStage);
-                Operands o[2];  // the next block's operands are read behind this one's MMAs
-                load_tokens(o[0], t);
-                load_weights(o[0], a);
+                // two blocks at a time, the next two's operands read behind their
+                // MMAs; what lies past the last block is read, not used
+                Operands o[4];
+                auto operands = [&](int j) {
+                    load_tokens(o[j & 3], t + j * 128);
+                    load_weights(o[j & 3], a + j * kDownRows * 128);
+                };
+                operands(0);
+                operands(1);
 #pragma unroll
-                for (int j = 0; j < kDownBlocks; ++j) {
+                for (int j = 0; j < kDownBlocks; j += 2) {
                     if (now.b0 + j < nk) {  // warp-uniform
-                        if (j + 1 < kDownBlocks) {  // past the last block: what lies there, not used
-                            load_tokens(o[(j + 1) & 1], t + (j + 1) * 128);
-                            load_weights(o[(j + 1) & 1], a + (j + 1) * kDownRows * 128);
+                        if (j + 2 < kDownBlocks) {
+                            operands(j + 2);
+                            operands(j + 3);
                         }
-                        float p[4];
-                        block_product(p, o[j & 1]);
-                        const float w = __shfl_sync(kFullMask, now.scale, j);
-                        const float c0 = __fmul_rn(c[j], w), c1 = __fmul_rn(c[kTokenRow / 4 + j], w);
-                        acc[0] = __fmaf_rn(p[0], c0, acc[0]);
-                        acc[1] = __fmaf_rn(p[1], c1, acc[1]);
-                        acc[2] = __fmaf_rn(p[2], c0, acc[2]);
-                        acc[3] = __fmaf_rn(p[3], c1, acc[3]);
+                        float p[2][4];
+                        block_product(p[0], o[j & 3]);
+                        block_product(p[1], o[(j + 1) & 3]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (now.b0 + j + i < nk) {
+                                const float w = __shfl_sync(kFullMask, now.scale, j + i);
+                                const float c0 = __fmul_rn(c[j + i], w), c1 = __fmul_rn(c[kTokenRow / 4 + j + i], w);
+                                acc[0] = __fmaf_rn(p[i][0], c0, acc[0]);
+                                acc[1] = __fmaf_rn(p[i][1], c1, acc[1]);
+                                acc[2] = __fmaf_rn(p[i][2], c0, acc[2]);
+                                acc[3] = __fmaf_rn(p[i][3], c1, acc[3]);
+                            }
+                        }
                     }
                 }
                 __syncwarp();
@@ -799,10 +825,13 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     const int64_t items = (int64_t)T * k * (I / 128);
     // Few items leave SMs without one: then several blocks share an item's K
     // (not at widths where the tokens would leave the ring too few stages).
-    // One token, H = 2048, I = 1024, k = 8, 64 items: MEASURED_SPLIT.
+    // One token, unshared against shared: 8 items at H = 7168 37.5 -> 19.9 us
+    // (C = 4), 64 items at 7168 49.5 -> 42.6 us (C = 2), 16 items at 2048 15.9
+    // -> 13.2 us (C = 4), 64 items at 2048 the same (19.7 and 20.0 us).
     const int C = H > 8192 || H < 1024 ? 1 : items * 4 <= sms ? 4 : items * 2 <= sms ? 2 : 1;
     const size_t rest = up_rest(T, H, C);
-    // Two blocks per SM where each has at least two stages and an item.
+    // Two blocks per SM where each has at least two stages and an item (45
+    // tokens, H = 2048: 152 us against 159 us with one).
     const int per_sm = C == 1 && items > sms && rest + 2 * kUpStage <= kSmemHalf ? 2 : 1;
     int stages = (int)(((per_sm == 2 ? kSmemHalf : kSmemLimit) - rest) / kUpStage);
     if (stages > kUpMaxStages) stages = kUpMaxStages;

@@ -19,7 +19,10 @@
 // than 32 reach it (many equal keys, or k near 32) k rounds of a maximum over
 // the warp find the choices instead.
 //
-// Bound by the ALU: MEASURED_ROUTE.
+// Bound by the instructions of one token (about 600 per warp; 88 % of the
+// issue slots): 65,536 x 256 logits, 8 groups of which 4, k = 8: 38-40 us, 1.8
+// TB/s; k rounds over all registers instead of the candidates took 103 us, and
+// one expert per register and 32 lanes instead of vectors per lane takes 80 us.
 #include "ep_experts.cuh"
 
 namespace ep {

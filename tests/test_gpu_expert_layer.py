@@ -35,7 +35,7 @@ def test_both_paths_match_the_definition(T):
     layer = layer_of(p, k, groups=4, groups_per_token=2)
     out = layer(p["x"], logits)
     idx, w = ref.route(logits, k, groups=4, groups_per_token=2)
-    few = T <= ep.MOE_FEW_MAX_TOKENS  # the two paths cast x with another quotient
+    few = layer.few(T)  # the two paths cast x with another quotient
     want, err = expected({**p, "topk_idx": idx.to(DEV), "topk_w": w.to(DEV)}, few)
     # the longer path rounds each expert's output to bf16 (2^-8 of it), at most
     # the sum of the magnitudes of its terms; the weights are good to 2^-16
@@ -46,6 +46,15 @@ def test_both_paths_match_the_definition(T):
     bound = 2.0 ** -8 * (want.abs() + 1.01 * terms + err) + err + 2.0 ** -16 * terms
     assert ((out.double() - want).abs() <= bound).all()
     assert ep.status_read(layer.status) == 0
+
+
+def test_choice_of_the_path():
+    p = problem(1, 256, 128, 8, 2, 3)
+    small = layer_of(p, 2)
+    assert small.few(1) and small.few(64) and not small.few(65)
+    big = layer_of({**p, "w13_q": p["w13_q"].expand(8, 256, 256)}, 2)
+    big.w13_q = torch.empty(8, 4096, 2048, dtype=torch.uint8, device=DEV)  # 64 MB of weights
+    assert big.few(8) and not big.few(9)
 
 
 def test_flags_of_every_call_reach_the_status_word():
