@@ -175,6 +175,8 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
     const uint32_t total = (uint32_t)sh.tiles[E] * ntiles;  // at most an output row's tiles each
     const int wrows = SWIGLU ? 2 * N : N;     // weight rows per expert
     const int wblocks = (wrows + 127) / 128;  // and blocks of 128 of them
+    // rows of output that allow 32-byte stores
+    const bool wide = SWIGLU ? (uintptr_t)out_q % 32 == 0 : (uintptr_t)out % 32 == 0 && N % 16 == 0;
     const uint32_t step = gridDim.x;
 
     if (warp < 4) {
@@ -369,15 +371,21 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
             if (!SWIGLU) {
                 if (work && live) {
                     uint16_t* o = out + row * N + t.n0 + share * kCols;
-                    const int left = N - t.n0 - share * kCols;  // a multiple of 8
+                    const int cols = N - t.n0 - share * kCols;  // a multiple of 8
+                    auto pack8 = [&](int c) {
+                        uint32_t q[4];
 #pragma unroll
-                    for (int c = 0; c < kCols / 8; ++c) {
-                        if (c * 8 < left) {
-                            uint32_t q[4];
+                        for (int j = 0; j < 4; ++j) q[j] = pack_bf16x2_rn(lo2(acc[4 * c + j]), hi2(acc[4 * c + j]));
+                        return make_uint4(q[0], q[1], q[2], q[3]);
+                    };
+                    if (wide) {  // whole sectors
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) q[j] = pack_bf16x2_rn(lo2(acc[4 * c + j]), hi2(acc[4 * c + j]));
-                            st_v4(o + c * 8, make_uint4(q[0], q[1], q[2], q[3]));
-                        }
+                        for (int c = 0; c < kCols / 8; c += 2)
+                            if (c * 8 < cols) st_v8(o + c * 8, Vec32{pack8(c), pack8(c + 1)});
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kCols / 8; ++c)
+                            if (c * 8 < cols) st_v4(o + c * 8, pack8(c));
                     }
                 }
             } else {
@@ -403,8 +411,7 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                 if (live) {
                     const float inv = __fdiv_rn(448.0f, a);
                     uint8_t* o = out_q + row * N + t.n0 + share * kH;
-#pragma unroll
-                    for (int c = 0; c < kH / 16; ++c) {
+                    auto codes16 = [&](int c) {
                         uint32_t q[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -412,7 +419,14 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
                             q[j] = cvt_e4m3x2_rn_sat(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
                                    (cvt_e4m3x2_rn_sat(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
                         }
-                        st_v4(o + c * 16, make_uint4(q[0], q[1], q[2], q[3]));
+                        return make_uint4(q[0], q[1], q[2], q[3]);
+                    };
+                    if (wide) {
+#pragma unroll
+                        for (int c = 0; c < kH / 16; c += 2) st_v8(o + c * 16, Vec32{codes16(c), codes16(c + 1)});
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kH / 16; ++c) st_v4(o + c * 16, codes16(c));
                     }
                     if (share == 0) out_scale[row * (N / 128) + t.n0 / 128] = __fdiv_rn(a, 448.0f);
                 }

@@ -183,6 +183,18 @@ def test_outputs_stay_inside_their_buffers():
     assert (rawo[:2048] == -7).all() and (rawo[-2048:] == -7).all()
 
 
+def test_outputs_on_16_but_not_32_bytes():
+    p, rows = problem([37, 100], "contiguous", 256, 512, 16, exact=True)
+    raw = torch.zeros(rows * 512 + 64, dtype=torch.bfloat16, device=DEV)
+    off = raw[8:8 + rows * 512].view(rows, 512)
+    assert off.data_ptr() % 32 == 16
+    assert torch.equal(ep.group_gemm_fp8(**p, out=off), ep.group_gemm_fp8(**p))
+    want, scale = ep.group_gemm_swiglu_fp8(**p)
+    rawq = torch.zeros(rows * 256 + 64, dtype=torch.uint8, device=DEV)
+    q, s = ep.group_gemm_swiglu_fp8(**p, out_q=rawq[16:16 + rows * 256].view(rows, 256))
+    assert torch.equal(q, want) and torch.equal(s, scale)
+
+
 def test_nan_codes_stay_in_their_row():
     p, rows = problem([130, 20], "contiguous", 256, 264, 10, exact=True)
     p["a_q"][5, 200] = 0x7F
