@@ -1,7 +1,9 @@
 /*
  * ep.h -- C ABI of the GB300 (sm_103a) MoE expert-parallel hot path:
  * routing layout, dispatch (BF16 or FP8 e4m3 with per-128-channel scales)
- * and weighted top-k combine, all on one GPU.
+ * and weighted top-k combine, and what stands around them in an expert
+ * layer: the router's choice, the experts' FP8 products, and the whole layer
+ * for a few tokens; all on one GPU.
  *
  * The operations are the local steps of DeepEP-style dispatch/combine as the
  * pages state the problem ("Replace EP backend comparison with Decode-like
@@ -30,7 +32,7 @@
  *  - Conditions found on the device never trap: they are OR-ed as EP_FLAG_*
  *    bits into the optional `status` word (a device uint32), which the caller
  *    reads with ep_status_read().  ep_layout() zeroes the word first;
- *    ep_dispatch*() and ep_combine() only OR into it.
+ *    every other call only ORs into it.
  *  - Kernels are launched with programmatic stream serialisation: each one
  *    waits for the preceding work in the stream before touching memory, and
  *    lets the next kernel launch early.  A caller's own kernel launched right
@@ -83,9 +85,11 @@ enum {
     EP_FLAG_BAD_EXPERT = 1u, /* an expert id outside [-1, E): the pair was skipped */
     EP_FLAG_OVERFLOW = 2u,   /* masked layout: slot >= capacity, the pair was dropped */
     EP_FLAG_BAD_ROW = 4u,    /* dispatch/combine: dst_row outside [-1, rows): skipped */
-    EP_FLAG_TIMEOUT = 8u     /* layout: a block of the one-launch cluster layout waited
-                                over a second for the others' totals and gave up; the
-                                outputs are incomplete (not expected on a working GPU) */,
+    EP_FLAG_TIMEOUT = 8u,    /* a wait inside a kernel lasted over a second and was given
+                                up: in the one-launch cluster layout for the other blocks'
+                                totals, in the expert products and the few-token layer for
+                                a copy, a product or another warp.  The outputs are
+                                incomplete (not expected on a working GPU) */
     EP_FLAG_BAD_LOGIT = 16u  /* ep_route: a logit (or logit + bias) is NaN: that expert
                                 was passed over */
 };
