@@ -25,7 +25,7 @@
 //
 // Few rows per expert: bound by the weights' bytes (64 rows each, 256 experts:
 // 590 us and 1.12 ms, 6.8 TB/s, at the copy rate).  Many rows: the tensor pipe
-// is busy 58 % of the cycles (8,192 rows per 32 experts, K = 7168: 430 us, 2.2
+// is busy 58 % of the cycles (16,384 rows, 32 experts, K = 7168: 430 us, 2.2
 // PFLOP/s).  What a block's sum needs in turn limits it: 512 cycles of MMAs, 300
 // until the adding warps see them, 450 to read and add, and two sums in flight
 // because two are all that TMEM holds.  Long calls also meet the power limit
