@@ -544,8 +544,10 @@ cudaError_t launch_up(int blocks, size_t smem, cudaStream_t stream, const CUtens
 
 // ---- down -----------------------------------------------------------------
 
-constexpr int kDownWarps = 6;
-constexpr int kDownStages = kDownWarps;           // a warp's stages always lie in the same place
+// Multiplying warps, and as many stages: a warp's stages always lie in the same
+// place.  Eight where the tokens' sums leave room for them, else six (8 tokens
+// at H = 7168: 383 us against 395 us with six; one at 2048: 19.5 against 20.2).
+constexpr int kDownMaxWarps = 8, kDownMinWarps = 6;
 constexpr int kDownRows = 16;                     // output channels of a block
 constexpr int kDownBlocks = kRecordBlocks;        // blocks of K of a stage
 constexpr int kDownW = kDownRows * kDownBlocks * 128;
@@ -554,7 +556,7 @@ constexpr int kDownStage = (kDownW + kCols * kTokenRow + 1023) / 1024 * 1024;
 static_assert(kTokenRow / 16 % 2 == 1 && kRecord % 16 == 0, "");
 
 struct DownShared {
-    uint64_t full[kDownStages], empty[kDownStages], sync;
+    uint64_t full[kDownMaxWarps], empty[kDownMaxWarps], sync;
     int gave_up;
     Groups g;
 };
@@ -566,11 +568,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+template <int kDownWarps>
 __global__ void __launch_bounds__((kDownWarps + 2) * 32, 1)
 few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ h8, int T, int H, int k,
                 const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
                 const float* __restrict__ s2, int I, int E, uint16_t* __restrict__ out,
                 uint32_t* __restrict__ status) {
+    constexpr int kDownStages = kDownWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     float* slabs = reinterpret_cast<float*>(ring + kDownStages * kDownStage);  // [warp][token][16 channels]
@@ -695,7 +699,7 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
         bool ok = barrier.sync(gave_up);
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, base += per_tile) {
             const float* ws = s2 + (int64_t)(tile * kDownRows / 128) * nk;  // of expert 0
-            // this warp's stages: every sixth of the block's sequence; the next
+            // this warp's stages: every kDownWarps-th of the block's sequence; the next
             // one's scalars are read behind the wait for this one
             Next next = look(at - base, ws);
             for (; at < base + per_tile; at += kDownWarps) {
@@ -792,14 +796,13 @@ size_t up_rest(int T, int H, int C) {  // shared memory besides the ring
     return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4 +
            (C > 1 ? 16 + (size_t)(C - 1) * kUpWarps * kUpTiles * 32 * 16 : 0);
 }
-size_t down_smem(int T) {
-    return 1024 + (size_t)kDownStages * kDownStage + (size_t)kDownWarps * T * kDownRows * 4 + sizeof(DownShared);
+constexpr size_t down_smem(int warps, int T) {
+    return 1024 + (size_t)warps * kDownStage + (size_t)warps * T * kDownRows * 4 + sizeof(DownShared);
 }
 static_assert(1024 + kCols * (EP_MOE_FEW_MAX_WIDTH + 16) + sizeof(UpShared) +
                       kCols * (EP_MOE_FEW_MAX_WIDTH / 128) * 4 + 2 * kUpStage <= kSmemLimit,
               "at least two stages at the widest");
-static_assert(1024 + kDownStages * kDownStage + kDownWarps * EP_MOE_FEW_MAX_TOKENS * kDownRows * 4 +
-                      sizeof(DownShared) <= kSmemLimit, "");
+static_assert(down_smem(kDownMinWarps, EP_MOE_FEW_MAX_TOKENS) <= kSmemLimit, "");
 
 }  // namespace
 
@@ -844,12 +847,15 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     const int tiles = H / kDownRows;
     err = byte_blocks_map(&w2_map, w2, (int64_t)E * H, I, kDownRows, kDownBlocks);
     if (err != cudaSuccess) return err;
-    static std::atomic<uint64_t> configured{0};
-    err = raise_smem_limit(few_down_kernel, kSmemLimit, configured);
+    static std::atomic<uint64_t> configured[2];
+    const bool most = down_smem(kDownMaxWarps, T) <= kSmemLimit;
+    const int warps = most ? kDownMaxWarps : kDownMinWarps;
+    const auto down = most ? few_down_kernel<kDownMaxWarps> : few_down_kernel<kDownMinWarps>;
+    err = raise_smem_limit(down, kSmemLimit, configured[most]);
     if (err != cudaSuccess) return err;
-    return launch_pdl(few_down_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                      dim3((kDownWarps + 2) * 32), down_smem(T), stream, w2_map, h8, T,
-                      H, k, topk_idx, topk_w, s2, I, E, static_cast<uint16_t*>(out), status);
+    return launch_pdl(down, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3((warps + 2) * 32),
+                      down_smem(warps, T), stream, w2_map, h8, T, H, k, topk_idx, topk_w, s2, I, E,
+                      static_cast<uint16_t*>(out), status);
 }
 
 }  // namespace ep

@@ -109,10 +109,17 @@ __device__ __forceinline__ float sigmoid(float l) {
     return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
 }
 
+// The choice of groups, with its divisions made on the host.
+struct GroupChoice {
+    int groups, chosen;
+    uint32_t inverse;  // group_of()'s
+    int span_log2;     // whole vectors per lane: lanes of a group, if a power of two (else -1)
+};
+
 template <int NV, bool FULL, typename L>
 __global__ void __launch_bounds__(kWarps * 32)
 route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64_t T, int E, int k,
-             int groups, int groups_per_token, int scoring, int renormalize, float scale,
+             GroupChoice gc, int scoring, int renormalize, float scale,
              int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
              uint32_t* __restrict__ status) {
     // candidates as (word, ~id), in the order of the choice; the groups' best keys before that
@@ -158,43 +165,41 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
     }
 
     bool in = true;  // FULL: whether the lane's experts are in a chosen group
-    if (groups_per_token < groups) {
-        const int per = E / groups;
-        const uint32_t inverse = ((1u << 20) + per - 1) / per;
-        const int span = per / NV;  // lanes of a group
-        const bool lanes = FULL && span * NV == per && (span & (span - 1)) == 0;
-        uint32_t best;  // lane g: the best key of group g
-        if (lanes) {
-            best = top;
+    if (gc.chosen < gc.groups) {
+        // A group's rank is how many are better, or as good and earlier.
+        if (FULL && gc.span_log2 >= 0) {  // the groups are equal runs of lanes
+            const int span = 1 << gc.span_log2, mine_g = lane >> gc.span_log2;
+            uint32_t best = top;
             for (int o = 1; o < span; o <<= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
-            best = __shfl_sync(kFullMask, best, (lane * span) & 31);
+            int rank = 0;
+#pragma unroll 4
+            for (int x = 1; x < gc.groups; ++x) {
+                const uint32_t other = __shfl_xor_sync(kFullMask, best, x << gc.span_log2);
+                rank += other > best || (other == best && (mine_g ^ x) < mine_g);
+            }
+            in = rank < gc.chosen;
+            if (!in) top = 0u;
         } else {
             uint32_t* bests = reinterpret_cast<uint32_t*>(mine);
             bests[lane] = 0u;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (key[i]) atomicMax(bests + group_of(id(i), inverse), key[i]);
+                if (key[i]) atomicMax(bests + group_of(id(i), gc.inverse), key[i]);
             __syncwarp();
-            best = bests[lane];
+            const uint32_t best = bests[lane];  // of group `lane`
             __syncwarp();
-        }
-        // a group's rank: how many are better, or as good and earlier
-        int rank = 0;
+            int rank = 0;
 #pragma unroll 4
-        for (int g = 0; g < groups; ++g) {
-            const uint32_t other = __shfl_sync(kFullMask, best, g);
-            rank += other > best || (other == best && g < lane);
-        }
-        const unsigned chosen = __ballot_sync(kFullMask, rank < groups_per_token);
-        if (lanes) {
-            in = (chosen >> (lane / span)) & 1u;
-            if (!in) top = 0u;
-        } else {
+            for (int g = 0; g < gc.groups; ++g) {
+                const uint32_t other = __shfl_sync(kFullMask, best, g);
+                rank += other > best || (other == best && g < lane);
+            }
+            const unsigned chosen = __ballot_sync(kFullMask, rank < gc.chosen);
             top = 0u;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (!((chosen >> (group_of(id(i), inverse) & 31)) & 1u)) key[i] = 0u;
+                if (!((chosen >> (group_of(id(i), gc.inverse) & 31)) & 1u)) key[i] = 0u;
                 top = max(top, key[i]);
             }
         }
@@ -306,9 +311,13 @@ cudaError_t launch(const L* logits, const float* bias, int64_t T, int E, int k, 
                    int groups_per_token, int scoring, int renormalize, float scale,
                    int32_t* topk_idx, float* topk_w, uint32_t* status, cudaStream_t stream) {
     const dim3 grid((unsigned)((T + kWarps - 1) / kWarps)), block(kWarps * 32);
+    const int per = E / groups;
+    GroupChoice gc{groups, groups_per_token, ((1u << 20) + per - 1) / per, -1};
+    if ((groups & (groups - 1)) == 0 && E % 32 == 0)  // 32 / groups lanes each
+        for (gc.span_log2 = 0; (groups << gc.span_log2) < 32;) ++gc.span_log2;
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, block, 0, stream, logits, bias, T, E, k, groups,
-                          groups_per_token, scoring, renormalize, scale, topk_idx, topk_w, status);
+        return launch_pdl(kernel, grid, block, 0, stream, logits, bias, T, E, k, gc, scoring,
+                          renormalize, scale, topk_idx, topk_w, status);
     };
     // whole vectors per lane where a row is 32 lanes of them and lies on 16 bytes
     const bool vectors = ((uintptr_t)logits | (uintptr_t)bias) % 16 == 0;
