@@ -127,9 +127,9 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
-    if (t >= T) return;  // warp-uniform
-    const L* row = logits + t * E;
+    const uint32_t t = blockIdx.x * kWarps + warp;  // T * k < 2^31
+    if (t >= (uint32_t)T) return;  // warp-uniform
+    const L* row = logits + (uint64_t)t * (uint32_t)E;
     uint64_t* mine = list[warp];
 
     auto id = [lane](int i) { return FULL ? lane * NV + i : i * 32 + lane; };
@@ -166,18 +166,19 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
 
     bool in = true;  // FULL: whether the lane's experts are in a chosen group
     if (gc.chosen < gc.groups) {
-        // A group's rank is how many are better, or as good and earlier.
         if (FULL && gc.span_log2 >= 0) {  // the groups are equal runs of lanes
-            const int span = 1 << gc.span_log2, mine_g = lane >> gc.span_log2;
-            uint32_t best = top;
+            const int span = 1 << gc.span_log2, group = lane >> gc.span_log2;
+            uint32_t best = top;  // of this lane's group, 0 once it is chosen
             for (int o = 1; o < span; o <<= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
-            int rank = 0;
-#pragma unroll 4
-            for (int x = 1; x < gc.groups; ++x) {
-                const uint32_t other = __shfl_xor_sync(kFullMask, best, x << gc.span_log2);
-                rank += other > best || (other == best && (mine_g ^ x) < mine_g);
+            in = false;
+            for (int r = 0; r < gc.chosen; ++r) {
+                const uint32_t m = __reduce_max_sync(kFullMask, best);
+                const int first = __ffs(__ballot_sync(kFullMask, best == m)) - 1;
+                if (group == first >> gc.span_log2) {
+                    in = true;
+                    best = 0u;
+                }
             }
-            in = rank < gc.chosen;
             if (!in) top = 0u;
         } else {
             uint32_t* bests = reinterpret_cast<uint32_t*>(mine);
@@ -189,7 +190,7 @@ route_kernel(const L* __restrict__ logits, const float* __restrict__ bias, int64
             __syncwarp();
             const uint32_t best = bests[lane];  // of group `lane`
             __syncwarp();
-            int rank = 0;
+            int rank = 0;  // how many groups are better, or as good and earlier
 #pragma unroll 4
             for (int g = 0; g < gc.groups; ++g) {
                 const uint32_t other = __shfl_sync(kFullMask, best, g);
