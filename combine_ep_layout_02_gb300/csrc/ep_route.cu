@@ -19,10 +19,11 @@
 // than 32 reach it (many equal keys, or k near 32) k rounds of a maximum over
 // the warp find the choices instead.
 //
-// Bound by the instructions of one token (about 600 per warp; 88 % of the
-// issue slots): 65,536 x 256 logits, 8 groups of which 4, k = 8: 38-40 us, 1.8
-// TB/s; k rounds over all registers instead of the candidates took 103 us, and
-// one expert per register and 32 lanes instead of vectors per lane takes 80 us.
+// Bound by the instructions of one token (about 510 per warp; 85 % of the
+// issue slots): 65,536 x 256 logits, 4 of 8 groups, k = 8: 33 us, 2.1 TB/s.  k
+// rounds over all registers instead of the candidates took 103 us.  Of the 510
+// the keys take 110, the groups 45, the threshold 50, collecting the candidates
+// 110, ranking them 100, weights and output 90.
 #include "ep_experts.cuh"
 
 namespace ep {
@@ -320,11 +321,14 @@ cudaError_t launch(const L* logits, const float* bias, int64_t T, int E, int k, 
         return launch_pdl(kernel, grid, block, 0, stream, logits, bias, T, E, k, gc, scoring,
                           renormalize, scale, topk_idx, topk_w, status);
     };
-    // whole vectors per lane where a row is 32 lanes of them and lies on 16 bytes
+    // whole vectors per lane where a row is 32 lanes of a register count that
+    // is instantiated, and lies on 16 bytes (65,536 x 256: 33 against 80 us)
     const bool vectors = ((uintptr_t)logits | (uintptr_t)bias) % 16 == 0;
+    if (vectors && E == 64) return go(route_kernel<2, true, L>);
     if (vectors && E == 128) return go(route_kernel<4, true, L>);
     if (vectors && E == 256) return go(route_kernel<8, true, L>);
     if (vectors && E == 512) return go(route_kernel<16, true, L>);
+    if (vectors && E == 1024) return go(route_kernel<32, true, L>);
     if (E <= 32) return go(route_kernel<1, false, L>);
     if (E <= 64) return go(route_kernel<2, false, L>);
     if (E <= 128) return go(route_kernel<4, false, L>);

@@ -83,3 +83,34 @@ def test_example_runs():
                         "--inner", "256", "--experts", "16", "--topk", "2"], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout[-1000:] + r.stderr[-2000:]
     assert r.stdout.count("us per layer") == 3
+
+
+CAPTURE = r'''
+import sys, torch
+sys.path.insert(0, ROOT_DIR)
+import combine_ep_layout_02_gb300 as ep
+dev = torch.device("cuda:0")
+E, H, I, k = 8, 256, 128, 2
+g = torch.Generator(device=dev).manual_seed(1)
+codes = lambda *s: torch.randint(0, 127, s, generator=g, device=dev, dtype=torch.int32).to(torch.uint8)
+layer = ep.ExpertLayer(codes(E, 2 * I, H), torch.full((E, 2, 2), 1e-4, device=dev), codes(E, H, I),
+                       torch.full((E, 2, 1), 1e-4, device=dev), k)
+for T in (5, 100):
+    x = torch.randn(T, H, generator=g, device=dev).to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device=dev)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        out = layer(x, logits)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, layer(x, logits)) and ep.status_read(layer.status) == 0
+print("CAPTURE-FIRST OK")
+'''
+
+
+def test_first_calls_inside_graph_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE.replace("ROOT_DIR", repr(root))], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "CAPTURE-FIRST OK" in r.stdout, r.stdout[-1000:] + r.stderr[-3000:]
