@@ -9,31 +9,33 @@
 //           e4m3 cast of ep_dispatch_fp8 per row and 128 channels of h.
 //
 // A tile is 128 rows of one expert by 256 weight rows (swiglu: 128 gate rows
-// and the 128 up rows of the same channels).  The scales are fp32 and differ per row and block of 128, so that the tensor
-// core cannot apply them: it makes each block's sum (four tcgen05.mma of
-// K = 32 into one of two TMEM buffers), and eight warps read that sum back,
-// scale it and add it into fp32 registers while the next block's MMAs run.
-// A TMEM lane is a row, so the row's scale is one value per thread.
+// and the 128 up rows of the same channels).  The scales are fp32 and differ
+// per row and block of 128, so that the tensor core cannot apply them: it makes
+// each block's sum (four tcgen05.mma of K = 32 into one of two TMEM buffers),
+// and eight warps read that sum back, scale it and add it into fp32 registers
+// while the next block's MMAs run.  A TMEM lane is a row, so the row's scale is
+// one value per thread.
 //
 // One persistent block per SM: warp 0 issues the TMA loads (128-byte swizzle,
 // four stages), warp 1 the MMAs, warps 2 and 3 bring the scales into shared
 // memory, and warps 4-11 scale, add and write the output.  The block is
 // launched with 168 registers a thread; the first warpgroup leaves 80 of them
 // to the other two, which need 128 for the sums alone.
-#include "ep_tcgen05.cuh"
-
 //
 // Few rows per expert: bound by the weights' bytes (64 rows each, 256 experts:
 // 590 us and 1.12 ms, 6.8 TB/s, at the copy rate).  Many rows: the tensor pipe
 // is busy 58 % of the cycles (16,384 rows, 32 experts, K = 7168: 430 us, 2.2
-// PFLOP/s).  What a block's sum needs in turn limits it: 512 cycles of MMAs, 300
-// until the adding warps see them, 450 to read and add, and two sums in flight
-// because two are all that TMEM holds.  Long calls also meet the power limit
+// PFLOP/s).  The adding warps' chain sets the pace, about 880 cycles per block of
+// K: some 150 to learn that a sum is there, 450 to read and add it, the rest the
+// scales, the loop and the share of the tile's epilogue; 512 cycles of MMAs and
+// the loads run beside it.  Long calls also meet the power limit
 // (1.45 GHz after some milliseconds, 1.7 GHz at first).  Measured and not
 // taken: a pair of SMs per 256 x 256 tile (464 against 444 us; half of the
 // weight traffic, but rows are padded to 256 and each hand-over crosses the
 // SMs), 16 adding warps (476), the two halves of N as separate MMAs (538: A is
 // read twice from shared memory), 32 columns per TMEM load (461).
+#include "ep_tcgen05.cuh"
+
 namespace ep {
 namespace {
 

@@ -139,6 +139,15 @@ def test_route_feeds_the_layout_and_replays_in_a_graph():
     assert torch.equal(lay.expert_counts.cpu().long(), torch.bincount(idx.cpu().long().view(-1), minlength=128))
 
 
+def test_route_beyond_32_bit_offsets():
+    T, E = (1 << 23) + 5, 512                     # 2^32 logits and some
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    at = torch.arange(T, device=DEV) % E
+    l.scatter_(1, at[:, None], 3.0)
+    idx, w = ep.route(l, 1)
+    assert torch.equal(idx[:, 0].long(), at) and (w == 1.0).all()
+
+
 def test_route_of_no_tokens():
     idx, w = ep.route(torch.empty(0, 64, device=DEV), 8)
     assert idx.shape == (0, 8) and w.shape == (0, 8)

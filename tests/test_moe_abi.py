@@ -1,6 +1,8 @@
 """Host-side argument checks of the router and the expert products (no GPU
 needed: every call below is refused before anything is enqueued)."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -17,6 +19,15 @@ def lib():
     cuda_build.build()
     from combine_ep_layout_02_gb300 import binding
     return binding.load()
+
+
+def test_limits_match_the_header():
+    from combine_ep_layout_02_gb300 import binding
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ep.h")) as f:
+        text = f.read()
+    assert int(re.search(r"#define EP_MOE_FEW_MAX_TOKENS (\d+)", text).group(1)) == binding.MOE_FEW_MAX_TOKENS
+    assert int(re.search(r"EP_TYPE_BF16 = (\d)", text).group(1)) == 1
+    assert int(re.search(r"EP_SCORE_SIGMOID = (\d)", text).group(1)) == binding.SCORES["sigmoid"]
 
 
 def test_route_argument_validation(lib):
