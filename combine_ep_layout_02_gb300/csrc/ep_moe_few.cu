@@ -378,30 +378,34 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
             const int grp = item / nb, b = item % nb, n = sh.g.size[grp], first = sh.g.first[grp];
             const float* sg = s13 + ((int64_t)sh.g.expert[grp] * 2 * nb + b) * nk;
             const float* su = sg + (int64_t)nb * nk;
+            // the weights' scales, a block per lane: the first 32, read behind the cast
+            float vg = __ldg(sg + min(k0 + lane, nk - 1)), vu = __ldg(su + min(k0 + lane, nk - 1));
             if (grp != have) {
-                // the previous group's reads are done: all warps met at the maxima since
-                for (int tok = warp; tok < n; tok += kUpWarps) {
-                    const uint16_t* src = x + (int64_t)(sh.g.pair[first + tok] / k) * H;
-                    uint8_t* to = xq + tok * stride;
-                    for (int c0 = k0 * 128; c0 < k1 * 128; c0 += 1024) {
-                        uint4 a[2], q[2];
+                // The previous group's reads are done: all warps met at the maxima
+                // since.  Pieces of 512 channels, two per warp at a time.
+                const int per = (k1 - k0 + 3) / 4, pieces = n * per;
+                for (int p0 = warp; p0 < pieces; p0 += 2 * kUpWarps) {
+                    uint4 a[2], q[2];
+                    int tok[2], c[2];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int c = c0 + u * 512 + lane * 16;
-                            a[u] = q[u] = make_uint4(0, 0, 0, 0);
-                            if (c < k1 * 128) {
-                                a[u] = __ldg(reinterpret_cast<const uint4*>(src + c));
-                                q[u] = __ldg(reinterpret_cast<const uint4*>(src + c + 8));
-                            }
+                    for (int u = 0; u < 2; ++u) {
+                        const int piece = p0 + u * kUpWarps;
+                        tok[u] = piece / per;
+                        c[u] = k0 * 128 + (piece - tok[u] * per) * 512 + lane * 16;
+                        if (piece >= pieces) c[u] = k1 * 128;  // no such piece
+                        a[u] = q[u] = make_uint4(0, 0, 0, 0);
+                        if (c[u] < k1 * 128) {
+                            const uint16_t* src = x + (int64_t)(sh.g.pair[first + tok[u]] / k) * H + c[u];
+                            a[u] = __ldg(reinterpret_cast<const uint4*>(src));
+                            q[u] = __ldg(reinterpret_cast<const uint4*>(src + 8));
                         }
+                    }
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int c = c0 + u * 512 + lane * 16;
-                            const Fp8Group f = cast16(a[u], q[u]);
-                            if (c < k1 * 128) {
-                                *reinterpret_cast<uint4*>(to + c) = f.q;
-                                if ((lane & 7) == 0) xs[tok * nk + (c >> 7)] = f.sf;
-                            }
+                    for (int u = 0; u < 2; ++u) {
+                        const Fp8Group f = cast16(a[u], q[u]);
+                        if (c[u] < k1 * 128) {
+                            *reinterpret_cast<uint4*>(xq + tok[u] * stride + c[u]) = f.q;
+                            if ((lane & 7) == 0) xs[tok[u] * nk + (c[u] >> 7)] = f.sf;
                         }
                     }
                 }
@@ -409,9 +413,8 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
                 if (!(ok = barrier.sync(gave_up))) break;
             }
             float acc[kUpTiles][4] = {};
-            float vg = 0.0f, vu = 0.0f;  // the weights' scales, a block per lane
             for (int kb = k0; kb < k1; ++kb) {
-                if ((kb - k0) % 32 == 0) {
+                if (kb > k0 && (kb - k0) % 32 == 0) {
                     const int to = min(kb + lane, nk - 1);
                     vg = __ldg(sg + to);
                     vu = __ldg(su + to);
