@@ -27,12 +27,12 @@
 //   and scales.  The warps take the stages in turn, each adds its weighted
 //   results per token in shared memory of its own, and the block adds the
 //   warps' sums in order: the result never depends on timing.
-// Measured (L2 cold, against the weights' bytes at the copy rate): 8 tokens,
-// H = 7168, I = 2048, 256 experts: 386 us, 6.5 TB/s, bound by DRAM; 45 tokens,
-// H = 2048, I = 1024, 128 experts: 149 us, 5.1 TB/s, bound by the per-item
-// work of the up blocks and by the down stages' latency (shared-memory
-// operands, 6 stages in flight); one token there: 20 us, 2.5 TB/s, bound by the
-// two kernels' start-up and hand-over (about 10 us) beside 7.5 us of weights.
+// Measured (L2 cold; the rate is the weights' bytes over the time): 8 tokens,
+// H = 7168, I = 2048, 256 experts: 366 us, 6.9 TB/s, bound by DRAM; 45 tokens,
+// H = 2048, I = 1024, 128 experts: 149 us, 5.1 TB/s, bound by the last round of
+// up items and by the down warps' 1,930 cycles per stage; one token there: 19
+// us, 2.7 TB/s, bound by the two kernels' start-up and hand-over (about 10 us)
+// beside 7.5 us of weights.
 //
 // An SM can draw more than twice its share of the memory's bandwidth, so that
 // neither kernel needs its items to divide evenly over the SMs.  Only where
