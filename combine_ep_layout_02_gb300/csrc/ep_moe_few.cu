@@ -6,9 +6,9 @@
 // each, so that the time is that of streaming the weights once.
 //
 // Mathematics: a tile of 16 weight rows is the A operand of an e4m3
-// mma.m16n8k32 and up to 8 of the expert's tokens are its 8 columns (a "group":
-// an expert with more tokens is several groups, whose later readings of the
-// weights come from L2).  Four MMAs make the sum of one block of 128 channels,
+// mma.m16n8k32 and up to 8 of the expert's (token, place) pairs are its 8
+// columns (a "group", of no more pairs than the call has tokens: an expert with
+// more is several groups, whose later readings of the weights come from L2).  Four MMAs make the sum of one block of 128 channels,
 // which is then scaled by a_scale * w_scale and added in fp32.  Tensor cores
 // of the fifth generation would need 128 rows by at least 8 columns per
 // instruction and a trip through TMEM per block; the work here is 2 % of what
@@ -39,12 +39,12 @@
 // there are fewer items than half the SMs do clusters of blocks share one.
 #include <stddef.h>
 
+#include "ep_few_plan.h"
 #include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kCols = 8;  // tokens per group: columns of one MMA
 constexpr int kMaxPairs = EP_MOE_FEW_MAX_TOKENS * EP_MAX_TOPK;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSmemHalf = 113 * 1024;  // of two blocks on an SM
@@ -69,7 +69,7 @@ struct Groups {
 
 // Up to 32 pairs: one per lane, ranked by (expert, pair).
 __device__ void build_groups_warp(Groups& g, const int32_t* __restrict__ topk_idx, int P, int E,
-                                  uint32_t* status, bool report) {
+                                  int limit, uint32_t* status, bool report) {
     const int lane = threadIdx.x & 31;
     const int e = lane < P ? __ldg(topk_idx + lane) : -1;
     const bool live = e >= 0 && e < E;
@@ -89,13 +89,13 @@ __device__ void build_groups_warp(Groups& g, const int32_t* __restrict__ topk_id
     const int se = lane < n ? g.seen[lane] : -1;  // the lane-th pair in that order
     const unsigned peers = __match_any_sync(kFullMask, se);
     const int in = __popc(peers & lanemask_lt());
-    const bool head = lane < n && in % kCols == 0;
+    const bool head = lane < n && in % limit == 0;
     const unsigned heads = __ballot_sync(kFullMask, head);
     if (head) {
         const int grp = __popc(heads & lanemask_lt());
         g.expert[grp] = (uint16_t)se;
         g.first[grp] = (uint16_t)lane;
-        g.size[grp] = (uint8_t)min(kCols, __popc(peers) - in);
+        g.size[grp] = (uint8_t)group_size(__popc(peers), in / limit, limit);
     }
     if (lane == 0) g.count = __popc(heads);
 }
@@ -114,9 +114,10 @@ __device__ void mark_twice(Groups& g, int k) {
 // work: at most 2,048 ids, 32 at a time.
 __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, int P, int k, int E,
                              uint32_t* status, bool report) {
+    const int limit = group_limit(P / k);
     if (P <= 32) {
         if (threadIdx.x < 32) {
-            build_groups_warp(g, topk_idx, P, E, status, report);
+            build_groups_warp(g, topk_idx, P, E, limit, status, report);
             __syncwarp();
             mark_twice(g, k);
         }
@@ -141,7 +142,7 @@ __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, in
         for (int e0 = 0; e0 < E; e0 += 32) {  // scans over the experts
             const int e = e0 + lane;
             const int n = e < E ? g.start[e] : 0;
-            const int m = (n + kCols - 1) / kCols;
+            const int m = group_count(n, limit);
             int ps = n, gs = m;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -155,8 +156,8 @@ __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, in
             for (int i = 0; i < m; ++i) {
                 const int at = groups + gs - m + i;
                 g.expert[at] = (uint16_t)e;
-                g.first[at] = (uint16_t)(first + i * kCols);
-                g.size[at] = (uint8_t)min(kCols, n - i * kCols);
+                g.first[at] = (uint16_t)(first + i * limit);
+                g.size[at] = (uint8_t)group_size(n, i, limit);
             }
             if (e < E) g.start[e] = (uint16_t)first;
             pairs += __shfl_sync(kFullMask, ps, 31);
@@ -291,8 +292,6 @@ __device__ __forceinline__ Fp8Group cast16(const uint4& lo, const uint4& hi) {
     return Fp8Group{make_uint4(q[0], q[1], q[2], q[3]), __fdiv_rn(a, 448.0f)};
 }
 
-constexpr int kUpWarps = 8;
-constexpr int kUpTiles = 16 / kUpWarps;  // of 8 channels, per warp
 constexpr int kUpStage = 2 * 128 * 128;  // one block of K of 128 gate and 128 up rows
 constexpr int kUpMaxStages = 6;
 
@@ -314,12 +313,11 @@ few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restr
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* xq = ring + stages * kUpStage;
-    const int stride = H + 16;  // 16 bytes of padding: eight tokens' chunks meet all banks
-    const int held = min(T, kCols);
-    UpShared& sh = *reinterpret_cast<UpShared*>(xq + held * stride);  // 16-byte aligned
-    float* xs = reinterpret_cast<float*>(&sh + 1);
-    // C > 1: the other blocks' sums [C - 1][warp][tile][lane]
-    float4* part = reinterpret_cast<float4*>(((uintptr_t)(xs + held * (H / 128)) + 15) & ~(uintptr_t)15);
+    const UpPlan plan = up_plan(T, H, C, sizeof(UpShared));
+    const int stride = plan.stride, held = plan.rows;
+    UpShared& sh = *reinterpret_cast<UpShared*>(xq + plan.shared);
+    float* xs = reinterpret_cast<float*>(xq + plan.scales);
+    float4* part = reinterpret_cast<float4*>(xq + plan.part);  // C > 1
     const int nk = H / 128, nb = I / 128;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
@@ -794,16 +792,13 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
     if (threadIdx.x == 0 && sh.gave_up && status) atomicOr(status, EP_FLAG_TIMEOUT);
 }
 
-size_t up_rest(int T, int H, int C) {  // shared memory besides the ring
-    const int held = T < kCols ? T : kCols;
-    return 1024 + (size_t)held * (H + 16) + sizeof(UpShared) + (size_t)held * (H / 128) * 4 +
-           (C > 1 ? 16 + (size_t)(C - 1) * kUpWarps * kUpTiles * 32 * 16 : 0);
+constexpr size_t up_rest(int T, int H, int C) {  // shared memory besides the ring
+    return 1024 + up_plan(T, H, C, sizeof(UpShared)).bytes;
 }
 constexpr size_t down_smem(int warps, int T) {
     return 1024 + (size_t)warps * kDownStage + (size_t)warps * T * kDownRows * 4 + sizeof(DownShared);
 }
-static_assert(1024 + kCols * (EP_MOE_FEW_MAX_WIDTH + 16) + sizeof(UpShared) +
-                      kCols * (EP_MOE_FEW_MAX_WIDTH / 128) * 4 + 2 * kUpStage <= kSmemLimit,
+static_assert(up_rest(EP_MOE_FEW_MAX_TOKENS, EP_MOE_FEW_MAX_WIDTH, 1) + 2 * kUpStage <= kSmemLimit,
               "at least two stages at the widest");
 static_assert(down_smem(kDownMinWarps, EP_MOE_FEW_MAX_TOKENS) <= kSmemLimit, "");
 
@@ -826,8 +821,7 @@ cudaError_t launch_moe_few(const void* x, int T, int H, int k, const int32_t* to
     CUtensorMap w13_map, w2_map;
     cudaError_t err = byte_matrix_map(&w13_map, w13, (int64_t)E * 2 * I, H, 128);
     if (err != cudaSuccess) return err;
-    // at most one group per pair and 128 channels (an expert with more than 8
-    // tokens has as many groups as its pairs need)
+    // at most one group per pair and 128 channels
     const int64_t items = (int64_t)T * k * (I / 128);
     // Few items leave SMs without one: then several blocks share an item's K
     // (not at widths where the tokens would leave the ring too few stages).

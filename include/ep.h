@@ -407,7 +407,8 @@ EP_API int ep_combine_fp8(const uint8_t* y_q, const float* y_scale, const float*
  * where x * 448 / a' is the midpoint of two (the chain rounds it once).  All sums are held in fp32
  * in a fixed order: the same inputs give the same bits.  An id of -1 is a
  * dropped pair; other ids outside [0, E) are skipped and raise
- * EP_FLAG_BAD_EXPERT.  A token without a valid pair gives +0.
+ * EP_FLAG_BAD_EXPERT.  A token without a valid pair gives +0.  A token may name
+ * an expert several times: each place counts with its own weight.
  *
  *  x          [T, H] bf16, 16-byte aligned;  topk_idx [T, k] int32;  topk_w [T, k] float32.
  *  w13_q      [E, 2*I, H] e4m3 codes (gate rows, then up rows), 32-byte aligned;
