@@ -574,6 +574,7 @@ def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offs
 
 
 MOE_FEW_MAX_TOKENS = 64
+MOE_FEW_MAX_WIDTH = 16384  # of H and of I
 
 
 def moe_few_workspace_bytes(T, k, inner):

@@ -41,14 +41,18 @@ class ExpertLayer:
         return self.experts(x, idx, w, out)
 
     def few(self, T):
-        """Whether T tokens go through ``moe_few``: it saves the five launches of
+        """Whether T tokens go through ``moe_few``.  It takes widths up to
+        ``MOE_FEW_MAX_WIDTH`` and weights on 32 bytes, the longer path any
+        width and weights on 16.  Where both take the call: ``moe_few`` saves the five launches of
         the longer path about 10 us, but reads an expert's weights at the full
         rate only for one or two tokens each.  Measured, few against long, in
         us: H 2048, I 1024, E 128, k 8: 16 / 28 (1 token), 103 / 104 (16), 154 /
         140 (48); H 7168, I 2048, E 64, k 8: 69 / 77 (1), 429 / 410 (16), 584 /
         436 (64); H 1024, I 512, E 8, k 2, whose weights are 13 MB: 10 / 21 (1),
         21 / 23 (64)."""
-        if T > binding.MOE_FEW_MAX_TOKENS:
+        if T > binding.MOE_FEW_MAX_TOKENS or max(self.w13_q.shape[2], self.w2_q.shape[2]) > binding.MOE_FEW_MAX_WIDTH:
+            return False
+        if self.w13_q.data_ptr() % 32 or self.w2_q.data_ptr() % 32:
             return False
         return T * self.k <= 2 * self.E or self.w13_q.numel() + self.w2_q.numel() <= 32 << 20
 
