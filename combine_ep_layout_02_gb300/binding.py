@@ -462,6 +462,16 @@ def _want(name, t, dtype, device):
         _check_dev(name, t, dtype, device)
 
 
+def _status_addr(status, device):
+    """Address of the optional status word, which kernels write to."""
+    if status is None:
+        return None
+    _want("status", status, torch.uint32 if status.dtype is torch.uint32 else torch.int32, device)
+    if status.numel() < 1:
+        raise ValueError("status must hold a word")
+    return status.data_ptr()
+
+
 def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="softmax",
           renormalize=True, scale=1.0, topk_idx=None, topk_w=None, status=None):
     """Top-k experts of ``logits`` [T, E] (float32 or bf16) and their weights
@@ -493,7 +503,7 @@ def route(logits, k, *, bias=None, groups=1, groups_per_token=None, scoring="sof
         None if bias is None else bias.data_ptr(), T, E, k, groups,
         groups if groups_per_token is None else groups_per_token, SCORES[scoring],
         1 if renormalize else 0, scale, topk_idx.data_ptr(), topk_w.data_ptr(),
-        None if status is None else status.data_ptr(), _stream_of(dev)))
+        _status_addr(status, dev), _stream_of(dev)))
     return topk_idx, topk_w
 
 
@@ -541,7 +551,7 @@ def group_gemm_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offsets, ki
     _rc("ep_group_gemm_fp8", _on_current(
         dev, load().ep_group_gemm_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K, w_q.data_ptr(),
         w_scale.data_ptr(), N, E, expert_counts.data_ptr(), _addr(expert_offsets),
-        LAYOUT_KINDS[kind], capacity, out.data_ptr(), _addr(status),
+        LAYOUT_KINDS[kind], capacity, out.data_ptr(), _status_addr(status, dev),
         _stream_of(dev)))
     return out
 
@@ -569,7 +579,7 @@ def group_gemm_swiglu_fp8(a_q, a_scale, w_q, w_scale, expert_counts, expert_offs
         dev, load().ep_group_gemm_swiglu_fp8, a_q.data_ptr(), a_scale.data_ptr(), rows, K,
         w_q.data_ptr(), w_scale.data_ptr(), inner, E, expert_counts.data_ptr(),
         _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, out_q.data_ptr(), out_scale.data_ptr(),
-        _addr(status), _stream_of(dev)))
+        _status_addr(status, dev), _stream_of(dev)))
     return out_q, out_scale
 
 
@@ -609,10 +619,11 @@ def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, wor
         raise ValueError("out must be [T, H]")
     if workspace is None:
         workspace = torch.empty(moe_few_workspace_bytes(T, k, inner), dtype=torch.uint8, device=dev)
+    _want("workspace", workspace, workspace.dtype, dev)
     _rc("ep_moe_few", _on_current(
         dev, load().ep_moe_few, x.data_ptr(), T, H, k, topk_idx.data_ptr(), topk_w.data_ptr(),
         w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_scale.data_ptr(), inner, E,
-        out.data_ptr(), _addr(status), workspace.data_ptr(),
+        out.data_ptr(), _status_addr(status, dev), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(dev)))
     return out
 
