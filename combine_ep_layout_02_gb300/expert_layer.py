@@ -23,7 +23,8 @@ class ExpertLayer:
 
     def __init__(self, w13_q, w13_scale, w2_q, w2_scale, k, *, bias=None, groups=1, groups_per_token=None,
                  scoring="softmax", renormalize=True, scale=1.0):
-        if w13_q.dim() != 3 or w2_q.dim() != 3 or w13_q.shape[1] != 2 * w2_q.shape[2]:
+        if (w13_q.dim() != 3 or w2_q.dim() != 3 or w13_q.shape[1] != 2 * w2_q.shape[2]
+                or tuple(w2_q.shape[:2]) != (w13_q.shape[0], w13_q.shape[2])):
             raise ValueError("w13_q must be [E, 2I, H] and w2_q [E, H, I]")
         self.w13_q, self.w13_scale, self.w2_q, self.w2_scale = w13_q, w13_scale, w2_q, w2_scale
         self.E, self.k = w13_q.shape[0], k
@@ -58,6 +59,12 @@ class ExpertLayer:
 
     def experts(self, x, topk_idx, topk_w, out=None):
         """The same for a route that is already at hand."""
+        if x.dim() != 2 or x.shape[1] != self.w13_q.shape[2]:
+            raise ValueError("x must be [T, H]")
+        if topk_idx.dim() != 2 or topk_idx.shape[0] != x.shape[0] or topk_w.shape != topk_idx.shape:
+            raise ValueError("topk_idx and topk_w must be [T, k]")
+        if out is not None and out.shape != x.shape:
+            raise ValueError("out must be [T, H]")
         if self.few(x.shape[0]):
             return binding.moe_few(x, topk_idx, topk_w, self.w13_q, self.w13_scale, self.w2_q, self.w2_scale,
                                    out=out, status=self.status)

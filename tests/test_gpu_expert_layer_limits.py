@@ -65,3 +65,26 @@ def test_weights_on_16_but_not_32_bytes(built, T, name):
 def test_widest_layer_of_the_few_token_call(built):
     p = problem(1, 128, ep.MOE_FEW_MAX_WIDTH, 2, 1, 11)
     assert layer_of(p, 1).few(1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 100])     # one for each path
+def test_shapes_are_refused_on_both_paths(built, T):
+    p = problem(T, 256, 128, 8, 2, 13)
+    layer = layer_of(p, 2)
+    assert layer.few(T) == (T == 4)
+    x, idx, w = p["x"], p["topk_idx"], p["topk_w"]
+    for args in ((x, idx[:, :1].contiguous(), w), (x, idx, w[:, :1].contiguous()), (x, idx[1:], w[1:]),
+                 (x[1:], idx, w), (x, idx, w[1:]), (x[:, :128].contiguous(), idx, w), (x, idx.view(-1), w.view(-1)),
+                 (x, idx, w, torch.empty(T - 1, 256, dtype=torch.bfloat16, device=DEV)),
+                 (x, idx, w, torch.empty(T, 128, dtype=torch.bfloat16, device=DEV))):
+        with pytest.raises(ValueError):
+            layer.experts(*args)
+
+
+@pytest.mark.gpu
+def test_weights_that_do_not_fit_each_other_are_refused(built):
+    p = problem(1, 256, 128, 4, 2, 17)
+    for w2 in (p["w2_q"][:3], p["w2_q"][:, :128].contiguous(), p["w2_q"][:, :, :64].contiguous()):
+        with pytest.raises(ValueError):
+            ep.ExpertLayer(p["w13_q"], p["w13_scale"], w2, p["w2_scale"], 2)
