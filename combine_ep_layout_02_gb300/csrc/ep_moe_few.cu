@@ -60,18 +60,28 @@ struct Groups {
     int count;
     uint16_t expert[kMaxPairs];  // per group
     uint16_t first[kMaxPairs];   // its first entry of `pair`, and their number
-    uint8_t size[kMaxPairs];
-    uint8_t twice[kMaxPairs];    // whether two of its pairs belong to one token
     uint16_t pair[kMaxPairs];    // pairs t * k + j ordered by expert, then by pair
+    union {
+        struct {
+            uint8_t size[kMaxPairs];
+            uint8_t twice[kMaxPairs];  // whether two of its pairs belong to one token
+        };
+        uint16_t id[kMaxPairs];  // until the pairs are in order: each one's expert
+    };
     uint16_t start[EP_MAX_EXPERTS];
     uint16_t seen[EP_MAX_EXPERTS];
 };
 
+// An id of the route.  The down kernel reads them before it waits for the up
+// kernel, when only that one's own wait has seen the route complete: the load
+// takes the value from L2, past any line that this SM holds from a call before.
+__device__ __forceinline__ int route_id(const int32_t* p) { return __ldcg(p); }
+
 // Up to 32 pairs: one per lane, ranked by (expert, pair).
-__device__ void build_groups_warp(Groups& g, const int32_t* __restrict__ topk_idx, int P, int E,
+__device__ void build_groups_warp(Groups& g, const int32_t* topk_idx, int P, int E,
                                   int limit, uint32_t* status, bool report) {
     const int lane = threadIdx.x & 31;
-    const int e = lane < P ? __ldg(topk_idx + lane) : -1;
+    const int e = lane < P ? route_id(topk_idx + lane) : -1;
     const bool live = e >= 0 && e < E;
     if (report) warp_flag(status, !live && e != -1, EP_FLAG_BAD_EXPERT);
     const int key = live ? e : EP_MAX_EXPERTS;
@@ -110,9 +120,9 @@ __device__ void mark_twice(Groups& g, int k) {
     }
 }
 
-// Fills `g` (shared); all threads of the block call it.  One warp does the
-// work: at most 2,048 ids, 32 at a time.
-__device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, int P, int k, int E,
+// Fills `g` (shared); all threads of the block call it.  All read the ids, at
+// most 2,048; one warp orders them, 32 at a time.
+__device__ void build_groups(Groups& g, const int32_t* topk_idx, int P, int k, int E,
                              uint32_t* status, bool report) {
     const int limit = group_limit(P / k);
     if (P <= 32) {
@@ -124,61 +134,67 @@ __device__ void build_groups(Groups& g, const int32_t* __restrict__ topk_idx, in
         __syncthreads();
         return;
     }
+    constexpr int kNone = 0xffff;
     for (int e = threadIdx.x; e < E; e += blockDim.x) g.start[e] = g.seen[e] = 0;
+    bool bad = false;
+    for (int p = threadIdx.x; p < P; p += blockDim.x) {
+        const int e = route_id(topk_idx + p);
+        const bool live = e >= 0 && e < E;
+        bad |= !live && e != -1;
+        g.id[p] = (uint16_t)(live ? e : kNone);
+    }
+    if (report) warp_flag(status, bad, EP_FLAG_BAD_EXPERT);
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        bool bad = false;
-        for (int p0 = 0; p0 < P; p0 += 32) {  // pairs per expert
-            const int e = p0 + lane < P ? __ldg(topk_idx + p0 + lane) : -1;
-            const bool live = e >= 0 && e < E;
-            bad |= !live && e != -1;
-            const unsigned peers = __match_any_sync(kFullMask, live ? e : -1);
-            if (live && (peers & lanemask_lt()) == 0) g.start[e] += (uint16_t)__popc(peers);
-            __syncwarp();
-        }
-        if (report) warp_flag(status, bad, EP_FLAG_BAD_EXPERT);
-        int pairs = 0, groups = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {  // scans over the experts
-            const int e = e0 + lane;
-            const int n = e < E ? g.start[e] : 0;
-            const int m = group_count(n, limit);
-            int ps = n, gs = m;
+        auto inclusive = [lane](int v) {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(kFullMask, ps, o), b = __shfl_up_sync(kFullMask, gs, o);
-                if (lane >= o) {
-                    ps += a;
-                    gs += b;
-                }
+                const int a = __shfl_up_sync(kFullMask, v, o);
+                if (lane >= o) v += a;
             }
-            const int first = pairs + ps - n;
-            for (int i = 0; i < m; ++i) {
-                const int at = groups + gs - m + i;
-                g.expert[at] = (uint16_t)e;
-                g.first[at] = (uint16_t)(first + i * limit);
-                g.size[at] = (uint8_t)group_size(n, i, limit);
-            }
-            if (e < E) g.start[e] = (uint16_t)first;
-            pairs += __shfl_sync(kFullMask, ps, 31);
-            groups += __shfl_sync(kFullMask, gs, 31);
+            return v;
+        };
+        for (int p0 = 0; p0 < P; p0 += 32) {  // pairs per expert
+            const int e = p0 + lane < P ? g.id[p0 + lane] : kNone;
+            const unsigned peers = __match_any_sync(kFullMask, e);
+            if (e != kNone && (peers & lanemask_lt()) == 0) g.start[e] += (uint16_t)__popc(peers);
+            __syncwarp();
         }
-        if (lane == 0) g.count = groups;
+        int pairs = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {  // their exclusive scan
+            const int e = e0 + lane, n = e < E ? g.start[e] : 0, sum = inclusive(n);
+            if (e < E) g.start[e] = (uint16_t)(pairs + sum - n);
+            pairs += __shfl_sync(kFullMask, sum, 31);
+        }
         __syncwarp();
         for (int p0 = 0; p0 < P; p0 += 32) {  // the pairs in expert order
-            const int e = p0 + lane < P ? __ldg(topk_idx + p0 + lane) : -1;
-            const bool live = e >= 0 && e < E;
-            const unsigned peers = __match_any_sync(kFullMask, live ? e : -1);
+            const int e = p0 + lane < P ? g.id[p0 + lane] : kNone;
+            const unsigned peers = __match_any_sync(kFullMask, e);
             const int before = __popc(peers & lanemask_lt());
             int at = 0;
-            if (live) at = g.start[e] + g.seen[e] + before;
+            if (e != kNone) at = g.start[e] + g.seen[e] + before;
             __syncwarp();
-            if (live) {
+            if (e != kNone) {
                 g.pair[at] = (uint16_t)(p0 + lane);
                 if (before == 0) g.seen[e] += (uint16_t)__popc(peers);
             }
             __syncwarp();
         }
+        int groups = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {  // the groups; `id` is no longer needed
+            const int e = e0 + lane, n = e < E ? g.seen[e] : 0;
+            const int m = group_count(n, limit), sum = inclusive(m);
+            for (int i = 0; i < m; ++i) {
+                const int at = groups + sum - m + i;
+                g.expert[at] = (uint16_t)e;
+                g.first[at] = (uint16_t)(g.start[e] + i * limit);
+                g.size[at] = (uint8_t)group_size(n, i, limit);
+            }
+            groups += __shfl_sync(kFullMask, sum, 31);
+        }
+        if (lane == 0) g.count = groups;
+        __syncwarp();
         mark_twice(g, k);
     }
     __syncthreads();
@@ -308,7 +324,7 @@ struct UpShared {
 template <int C>
 __global__ void __launch_bounds__((kUpWarps + 1) * 32, 2)
 few_up_kernel(const __grid_constant__ CUtensorMap w_map, const uint16_t* __restrict__ x, int T,
-              int H, int k, const int32_t* __restrict__ topk_idx, const float* __restrict__ s13,
+              int H, int k, const int32_t* topk_idx, const float* __restrict__ s13,
               int I, int E, int stages, uint8_t* __restrict__ h8, uint32_t* __restrict__ status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -572,7 +588,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 template <int kDownWarps>
 __global__ void __launch_bounds__((kDownWarps + 2) * 32, 1)
 few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __restrict__ h8, int T, int H, int k,
-                const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
+                const int32_t* topk_idx, const float* __restrict__ topk_w,
                 const float* __restrict__ s2, int I, int E, uint16_t* __restrict__ out,
                 uint32_t* __restrict__ status) {
     constexpr int kDownStages = kDownWarps;
