@@ -9,7 +9,7 @@ from .binding import (  # noqa: F401
     EpError, LayoutOut, Pipeline, combine, combine_fp8, dispatch, dispatch_fp8, layout, layout_dispatch,
     layout_workspace_bytes, load,
     layout_static_ws, route, group_gemm_fp8, group_gemm_swiglu_fp8, moe_few,
-    moe_few_workspace_bytes, MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_WIDTH, status_read, rank_layout, rank_rows_bound, expand, expand_fp8, combine_partial,
+    moe_few_workspace_bytes, MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_WIDTH, status_read, status_merge, rank_layout, rank_rows_bound, expand, expand_fp8, combine_partial,
     combine_reduce, RankLayoutOut, EP_FLAG_BAD_EXPERT, EP_FLAG_OVERFLOW, EP_FLAG_BAD_ROW, EP_FLAG_TIMEOUT,
     EP_FLAG_BAD_LOGIT,
 )

@@ -80,6 +80,7 @@ def load():
         "ep_moe_few_workspace_bytes": ([i64, i32, i32], sz),
         "ep_moe_few": ([P, i64, i32, i32, P, P, P, P, P, P, i32, i32, P, P, P, sz, P], i32),
         "ep_status_read": ([P, P, P], i32),
+        "ep_status_merge": ([P, P, P], i32),
         "ep_pipeline_create": ([i32, ctypes.POINTER(ctypes.c_void_p)], i32),
         "ep_pipeline_destroy": ([P], i32),
         "ep_roundtrip_host": ([P, P, P, P, P, P, i64, i64, i32, i32, i32, i32, i32, i64, P, P, P,
@@ -635,6 +636,14 @@ def status_read(status):
         code = load().ep_status_read(_ptr(status), _stream(status.device), ctypes.byref(flags))
     _rc("ep_status_read", code)
     return int(flags.value)
+
+
+def status_merge(src, into):
+    """OR the status word ``src`` into ``into`` on the current stream, atomically
+    (see ``ep_status_merge``)."""
+    dev = into.device
+    _rc("ep_status_merge", _on_current(dev, load().ep_status_merge, _status_addr(src, dev),
+                                       _status_addr(into, dev), _stream_of(dev)))
 
 
 class Pipeline:

@@ -19,6 +19,13 @@ inline int cuda_status(cudaError_t e) {
 
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+__global__ void status_merge_kernel(const uint32_t* from, uint32_t* into) {
+    ep::pdl_wait();
+    ep::pdl_trigger();
+    const uint32_t bits = *from;
+    if (bits) atomicOr(into, bits);
+}
+
 // Common checks of (T, H, k, rows) for dispatch and combine.
 int check_rows_args(int64_t T, int64_t H, int k, int64_t rows) {
     if (T < 0 || H <= 0 || k < 1 || k > EP_MAX_TOPK || rows < 0) return EP_ERR_INVALID_ARG;
@@ -496,6 +503,13 @@ int ep_status_read(const uint32_t* status, void* stream, uint32_t* host_flags) {
                                     as_stream(stream));
     if (e == cudaSuccess) e = cudaStreamSynchronize(as_stream(stream));
     return cuda_status(e);
+}
+
+int ep_status_merge(const uint32_t* from, uint32_t* into, void* stream) {
+    if (!from || !into) return EP_ERR_INVALID_ARG;
+    if (!aligned(from, 4) || !aligned(into, 4)) return EP_ERR_ALIGNMENT;
+    return cuda_status(ep::launch_pdl(status_merge_kernel, dim3(1), dim3(1), 0, as_stream(stream),
+                                      from, into));
 }
 
 }  // extern "C"

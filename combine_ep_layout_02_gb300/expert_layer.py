@@ -74,5 +74,5 @@ class ExpertLayer:
         h, hs = binding.group_gemm_swiglu_fp8(q, s, self.w13_q, self.w13_scale, *at, status=self.status)
         y = binding.group_gemm_fp8(h, hs, self.w2_q, self.w2_scale, *at, status=self.status)
         out = binding.combine(y, topk_w, lay.dst_row, out=out, status=self.status)
-        self.status |= lay.status
+        binding.status_merge(lay.status, self.status)
         return out

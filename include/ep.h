@@ -554,6 +554,12 @@ EP_API int ep_roundtrip_host(void* handle, void* stream, const void* x_host,
  * synchronising `stream`. */
 EP_API int ep_status_read(const uint32_t* status, void* stream, uint32_t* host_flags);
 
+/* OR the device status word `from` into `into`, on the device: one atomic, so
+ * that calls on other streams may raise flags in `into` at the same time.  For
+ * callers who keep one word over several calls of which a layout, which zeroes
+ * the word that it is given, is one. */
+EP_API int ep_status_merge(const uint32_t* from, uint32_t* into, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
