@@ -19,14 +19,14 @@
 // One persistent block per SM: warp 0 issues the TMA loads (128-byte swizzle,
 // four stages), warp 1 the MMAs, warps 2 and 3 bring the scales into shared
 // memory, and warps 4-11 scale, add and write the output.  The block is
-// launched with 168 registers a thread; the first warpgroup leaves 80 of them
-// to the other two, which need 128 for the sums alone.
+// launched with 168 registers a thread; the first warpgroup keeps 72 and leaves
+// the rest to the other two, 216 each, which need 128 for the sums alone.
 //
 // Few rows per expert: bound by the weights' bytes (64 rows each, 256 experts:
-// 590 us and 1.12 ms, 6.8 TB/s, at the copy rate).  Many rows: the tensor pipe
-// is busy 58 % of the cycles (16,384 rows, 32 experts, K = 7168: 430 us, 2.2
-// PFLOP/s).  The adding warps' chain sets the pace, about 880 cycles per block of
-// K: some 150 to learn that a sum is there, 450 to read and add it, the rest the
+// 575 us and 1.09 ms, 7.0 TB/s; a plain copy, half of it writes, makes 6.7).
+// Many rows: the tensor pipe is busy 58 % of the cycles (16,384 rows, 32 experts,
+// K = 7168: 430 us, 2.2 PFLOP/s).  The adding warps' chain sets the pace, about
+// 880 cycles per block of K: some 150 to learn that a sum is there, 450 to read and add it, the rest the
 // scales, the loop and the share of the tile's epilogue; 512 cycles of MMAs and
 // the loads run beside it.  Long calls also meet the power limit
 // (1.45 GHz after some milliseconds, 1.7 GHz at first).  Measured and not
@@ -44,7 +44,7 @@ constexpr int kTileN = 256, kBlockK = 128;
 constexpr int kStages = 4;
 constexpr int kABytes = kRowsM * kBlockK, kBBytes = kTileN * kBlockK;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kARows = 32;                      // rows per TMA box of A: rows past the segment's end are not read
+constexpr int kARows = 32;                      // rows per TMA box of A: at most 31 past the segment's end are read
 constexpr int kAddWarps = 8;                    // warps that scale and add
 constexpr int kAddThreads = kAddWarps * 32;
 constexpr int kThreads = 128 + kAddThreads;

@@ -27,12 +27,14 @@
 //   and scales.  The warps take the stages in turn, each adds its weighted
 //   results per token in shared memory of its own, and the block adds the
 //   warps' sums in order: the result never depends on timing.
-// Measured (L2 cold; the rate is the weights' bytes over the time): 8 tokens,
-// H = 7168, I = 2048, 256 experts: 366 us, 6.9 TB/s, bound by DRAM; 45 tokens,
-// H = 2048, I = 1024, 128 experts: 149 us, 5.1 TB/s, bound by the last round of
-// up items and by the down warps' 1,930 cycles per stage; one token there: 19
-// us, 2.7 TB/s, bound by the two kernels' start-up and hand-over (about 10 us)
-// beside 7.5 us of weights.
+// Measured (three sets of weights in turn; the rate is the weights' bytes over
+// the time): 8 tokens, H = 7168, I = 2048, 256 experts: 380-390 us, 6.5-6.7 TB/s,
+// bound by DRAM; 45 tokens, H = 2048, I = 1024, 128 experts: 140-146 us, 5.3 TB/s,
+// bound by the last round of up items and by the down warps' 1,930 cycles per
+// stage; one token there: 17-20 us, 2.7 TB/s, bound by the two kernels' start-up
+// and hand-over (about 10 us) beside 7.5 us of weights: an up block and a down
+// block ask for more shared memory than one SM has, so that the down blocks of
+// the SMs with an up block begin to read when that one ends.
 //
 // An SM can draw more than twice its share of the memory's bandwidth, so that
 // neither kernel needs its items to divide evenly over the SMs.  Only where
@@ -617,7 +619,8 @@ few_down_kernel(const __grid_constant__ CUtensorMap w_map, const uint8_t* __rest
     const int groups = sh.g.count;
 
     if (warp == kDownWarps) {
-        // ---- weights, from before the up kernel has finished
+        // ---- weights, from before the up kernel has finished on the SMs that
+        // its blocks have left
         Fill fill{full, empty, (uint32_t)kDownStages};
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {

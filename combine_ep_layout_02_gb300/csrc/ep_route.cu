@@ -321,8 +321,12 @@ cudaError_t launch(const L* logits, const float* bias, int64_t T, int E, int k, 
         return launch_pdl(kernel, grid, block, 0, stream, logits, bias, T, E, k, gc, scoring,
                           renormalize, scale, topk_idx, topk_w, status);
     };
-    // whole vectors per lane where a row is 32 lanes of a register count that
-    // is instantiated, and lies on 16 bytes (65,536 x 256: 33 against 80 us)
+    // Whole vectors per lane where a row is 32 lanes of a power of two of
+    // registers and lies on 16 bytes.  Other rows take single loads, and the
+    // groups' maxima by atomics in shared memory, in the next power of two of
+    // registers: 65,536 tokens, fp32, k = 8, without groups and with 4 of 8, in us:
+    // 96 experts 22 and 31 (128: 22 and 28), 160 experts 27 and 45 (256: 26 and
+    // 32), 384 experts 37 and 100 (512: 35 and 40).
     const bool vectors = ((uintptr_t)logits | (uintptr_t)bias) % 16 == 0;
     if (vectors && E == 64) return go(route_kernel<2, true, L>);
     if (vectors && E == 128) return go(route_kernel<4, true, L>);

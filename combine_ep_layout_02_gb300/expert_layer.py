@@ -30,7 +30,8 @@ class ExpertLayer:
         self.E, self.k = w13_q.shape[0], k
         self.routing = dict(bias=bias, groups=groups, groups_per_token=groups_per_token, scoring=scoring,
                             renormalize=renormalize, scale=scale)
-        # the device status word of every call made here (binding.status_read)
+        # the device status word of every call made here, on whatever streams
+        # (binding.status_read)
         self.status = torch.zeros(1, dtype=torch.int32, device=w13_q.device)
 
     def __call__(self, x, logits, out=None):

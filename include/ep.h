@@ -32,7 +32,8 @@
  *  - Conditions found on the device never trap: they are OR-ed as EP_FLAG_*
  *    bits into the optional `status` word (a device uint32), which the caller
  *    reads with ep_status_read().  ep_layout() zeroes the word first;
- *    every other call only ORs into it.
+ *    every other call only ORs into it.  A call without the word (NULL) does
+ *    the same and reports nothing, an EP_FLAG_TIMEOUT included.
  *  - Kernels are launched with programmatic stream serialisation: each one
  *    waits for the preceding work in the stream before touching memory, and
  *    lets the next kernel launch early.  A caller's own kernel launched right
@@ -133,7 +134,12 @@ EP_API size_t ep_layout_workspace_bytes(int64_t T, int k, int E, int R, int with
  *                              sum is 0)
  *       SIGMOID:               sigmoid(l_j)
  *     times `scale`; computed in fp32, with the largest logit subtracted
- *     first in a softmax (several logits of +inf share it equally).
+ *     first in a softmax (several logits of +inf share it equally).  In fp32
+ *     the sigmoid of a logit below about -88.7 is 0.
+ *   - The bias is added to the logit under either scoring, and a group counts
+ *     by its best key.  A router whose bias is added to the score itself
+ *     (sigmoid(l) + b), or whose groups count by the sum of their best scores,
+ *     makes another choice, which this call does not offer.
  *
  *  logits    [T, E] float32 or bf16 (logits_type), row-major, aligned to the type.
  *  bias      [E] float32 or NULL.
@@ -325,7 +331,9 @@ EP_API int ep_layout_dispatch_fp8(const int32_t* topk_idx, int64_t T, int k, int
  *            first min(expert_counts[e], capacity) rows from e*capacity
  *            (expert_offsets may be NULL; rows >= E*capacity).
  *            A contiguous segment outside [0, rows) is cut to it and raises
- *            EP_FLAG_BAD_ROW.  Rows of no segment are neither read nor written.
+ *            EP_FLAG_BAD_ROW.  Rows of no segment are never written and change no
+ *            result, whatever they hold; up to 31 rows that follow a segment in
+ *            the buffer may be read.
  *  out       [rows, N] bf16, 16-byte aligned.
  * Limits: K % 128 == 0; N % 8 == 0; rows < 2^31; E * N < 2^31.
  */
