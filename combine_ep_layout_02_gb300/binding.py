@@ -29,6 +29,8 @@ EP_FLAG_BAD_LOGIT = 16
 LAYOUT_KINDS = {"contiguous": 0, "masked": 1}
 LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 SCORES = {"softmax": 0, "sigmoid": 1}
+TYPES = {torch.float32: 0, torch.bfloat16: 1}  # of outputs, biases and gradients that may be either
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 _lib = None
 
@@ -79,6 +81,15 @@ def load():
         "ep_group_gemm_swiglu_fp8": ([P, P, i64, i64, P, P, i64, i32, P, P, i32, i32, P, P, P, P], i32),
         "ep_moe_few_workspace_bytes": ([i64, i32, i32], sz),
         "ep_moe_few": ([P, i64, i32, i32, P, P, P, P, P, P, i32, i32, P, P, P, sz, P], i32),
+        "ep_group_gemm": ([P, i64, i64, P, i64, i32, P, P, i32, i32, P, P, P], i32),
+        "ep_group_gemm_swiglu": ([P, i64, i64, P, i64, i32, P, P, i32, i32, P, P, P, P], i32),
+        "ep_group_gemm_dgrad": ([P, i64, i64, P, i64, i32, P, P, i32, i32, P, P, P], i32),
+        "ep_group_gemm_swiglu_dgrad": ([P, i64, i64, P, i64, i32, P, P, P, i32, i32, P, P, P], i32),
+        "ep_group_gemm_wgrad": ([P, P, i64, i64, i64, i32, P, P, i32, i32, P, P, i32, P, P], i32),
+        "ep_linear_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "ep_linear": ([P, i64, i64, P, i64, P, i32, i32, P, P, i32, P, P, P, sz, P], i32),
+        "ep_linear_backward": ([P, P, P, P, i64, i64, i64, i32, P, P, P, P, i32, P, P, P], i32),
+        "ep_combine_backward": ([P, P, P, P, i64, i64, i32, i64, P, P, P, P], i32),
         "ep_status_read": ([P, P, P], i32),
         "ep_status_merge": ([P, P, P], i32),
         "ep_pipeline_create": ([i32, ctypes.POINTER(ctypes.c_void_p)], i32),
@@ -627,6 +638,250 @@ def moe_few(x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, wor
         out.data_ptr(), _status_addr(status, dev), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream_of(dev)))
     return out
+
+
+def _check_segments(expert_counts, expert_offsets, kind, E, device):
+    _want("expert_counts", expert_counts, torch.int32, device)
+    if expert_offsets is not None:
+        _want("expert_offsets", expert_offsets, torch.int32, device)
+    if kind not in LAYOUT_KINDS:
+        raise ValueError("kind must be one of %s" % ", ".join(sorted(LAYOUT_KINDS)))
+    if expert_counts.numel() < E or (expert_offsets is not None and expert_offsets.numel() < E):
+        raise ValueError("expert_counts and expert_offsets need an entry per expert")
+
+
+def _check_rows(name, a, weights, w, channel):
+    """Types, devices and shapes of a buffer of rows and the experts' weights,
+    whose dimension `channel` the rows have; returns the device."""
+    _check_dev(name, a, torch.bfloat16)
+    _want(weights, w, torch.bfloat16, a.device)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("%s must be [rows, width] and %s hold an expert per entry" % (name, weights))
+    if a.shape[1] != w.shape[channel]:
+        raise ValueError("%s has %d channels, %s %d" % (name, a.shape[1], weights, w.shape[channel]))
+    return a.device
+
+
+def _result(name, t, shape, dtype, device):
+    """`t`, checked, or a new tensor in its place."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(name, t, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return t
+
+
+def _result_of_types(name, t, shape, dtype, device):
+    """The same where the result may be float32 or bf16."""
+    dtype = dtype if t is None else t.dtype
+    if dtype not in TYPES:
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, dtype))
+    return _result(name, t, shape, dtype, device)
+
+
+def group_gemm(x, w, expert_counts, expert_offsets, kind="contiguous", capacity=0, out=None, status=None):
+    """Product of every expert's rows of the dispatched BF16 buffer ``x`` [rows, K]
+    with its weight ``w`` [E, N, K] into ``out`` [rows, N] bf16 (see
+    ``ep_group_gemm``).  Counts and offsets are the layout's; rows that belong
+    to no expert keep what ``out`` held."""
+    dev = _check_rows("x", x, "w", w, 2)
+    E, N, K = w.shape
+    _check_segments(expert_counts, expert_offsets, kind, E, dev)
+    out = _result("out", out, (x.shape[0], N), torch.bfloat16, dev)
+    _rc("ep_group_gemm", _on_current(
+        dev, load().ep_group_gemm, x.data_ptr(), x.shape[0], K, w.data_ptr(), N, E,
+        expert_counts.data_ptr(), _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, out.data_ptr(),
+        _status_addr(status, dev), _stream_of(dev)))
+    return out
+
+
+def group_gemm_swiglu(x, w13, expert_counts, expert_offsets, kind="contiguous", capacity=0, out=None,
+                      z=None, status=None):
+    """First product of gated experts with SwiGLU in its epilogue: ``w13``
+    [E, 2I, K] holds the gate rows, then the up rows; ``out`` [rows, I].  ``z``
+    [rows, 2I] bf16, where given, gets the pre-activations, which
+    ``group_gemm_swiglu_dgrad`` takes."""
+    dev = _check_rows("x", x, "w13", w13, 2)
+    E, n, K = w13.shape
+    if n % 2 != 0:
+        raise ValueError("w13 must hold as many gate as up rows")
+    _check_segments(expert_counts, expert_offsets, kind, E, dev)
+    out = _result("out", out, (x.shape[0], n // 2), torch.bfloat16, dev)
+    if z is not None:
+        _result("z", z, (x.shape[0], n), torch.bfloat16, dev)
+    _rc("ep_group_gemm_swiglu", _on_current(
+        dev, load().ep_group_gemm_swiglu, x.data_ptr(), x.shape[0], K, w13.data_ptr(), n // 2, E,
+        expert_counts.data_ptr(), _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, out.data_ptr(),
+        _addr(z), _status_addr(status, dev), _stream_of(dev)))
+    return out
+
+
+def group_gemm_dgrad(dy, w, expert_counts, expert_offsets, kind="contiguous", capacity=0, dx=None, status=None):
+    """Gradient of ``group_gemm``'s input: ``dy`` [rows, N], ``w`` [E, N, K] to
+    ``dx`` [rows, K] bf16 (see ``ep_group_gemm_dgrad``)."""
+    dev = _check_rows("dy", dy, "w", w, 1)
+    E, N, K = w.shape
+    _check_segments(expert_counts, expert_offsets, kind, E, dev)
+    dx = _result("dx", dx, (dy.shape[0], K), torch.bfloat16, dev)
+    _rc("ep_group_gemm_dgrad", _on_current(
+        dev, load().ep_group_gemm_dgrad, dy.data_ptr(), dy.shape[0], N, w.data_ptr(), K, E,
+        expert_counts.data_ptr(), _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, dx.data_ptr(),
+        _status_addr(status, dev), _stream_of(dev)))
+    return dx
+
+
+def group_gemm_swiglu_dgrad(dy, w2, z, expert_counts, expert_offsets, kind="contiguous", capacity=0, dz=None,
+                            status=None):
+    """Gradient through the second product and SwiGLU: ``dy`` [rows, H] of the
+    second product's output, ``w2`` [E, H, I] and the pre-activations ``z``
+    [rows, 2I] to ``dz`` [rows, 2I] bf16 (see ``ep_group_gemm_swiglu_dgrad``)."""
+    dev = _check_rows("dy", dy, "w2", w2, 1)
+    E, H, inner = w2.shape
+    _check_segments(expert_counts, expert_offsets, kind, E, dev)
+    shape = (dy.shape[0], 2 * inner)
+    _result("z", z, shape, torch.bfloat16, dev)
+    dz = _result("dz", dz, shape, torch.bfloat16, dev)
+    _rc("ep_group_gemm_swiglu_dgrad", _on_current(
+        dev, load().ep_group_gemm_swiglu_dgrad, dy.data_ptr(), dy.shape[0], H, w2.data_ptr(), inner, E,
+        z.data_ptr(), expert_counts.data_ptr(), _addr(expert_offsets), LAYOUT_KINDS[kind], capacity,
+        dz.data_ptr(), _status_addr(status, dev), _stream_of(dev)))
+    return dz
+
+
+def group_gemm_wgrad(dy, x, expert_counts, expert_offsets, kind="contiguous", capacity=0, dw=None, add=None,
+                     dtype=torch.float32, status=None):
+    """Gradient of the experts' weights: ``dy`` [rows, N], ``x`` [rows, K] to
+    ``dw`` [E, N, K], float32 or bf16 (``dtype`` where ``dw`` is not given), of
+    as many experts as ``dw`` or ``expert_counts`` has.  ``add``, of ``dw``'s
+    shape and type, is added; it may be ``dw`` itself (see ``ep_group_gemm_wgrad``)."""
+    _check_dev("dy", dy, torch.bfloat16)
+    dev = dy.device
+    _want("x", x, torch.bfloat16, dev)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [rows, N] and x [rows, K]")
+    E = expert_counts.numel() if dw is None else dw.shape[0]
+    _check_segments(expert_counts, expert_offsets, kind, E, dev)
+    dw = _result_of_types("dw", dw, (E, dy.shape[1], x.shape[1]), dtype, dev)
+    if add is not None:
+        _result("add", add, dw.shape, dw.dtype, dev)
+    _rc("ep_group_gemm_wgrad", _on_current(
+        dev, load().ep_group_gemm_wgrad, dy.data_ptr(), x.data_ptr(), dy.shape[0], dy.shape[1], x.shape[1], E,
+        expert_counts.data_ptr(), _addr(expert_offsets), LAYOUT_KINDS[kind], capacity, _addr(add),
+        dw.data_ptr(), TYPES[dw.dtype], _status_addr(status, dev), _stream_of(dev)))
+    return dw
+
+
+def linear_workspace_bytes(M, K, N, activation="none"):
+    return int(load().ep_linear_workspace_bytes(M, K, N, ACTIVATIONS[activation]))
+
+
+def _check_linear(x, w, activation):
+    """Types, devices and shapes of a dense product; returns (device, M, K, N)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
+    _check_dev("x", x, torch.bfloat16)
+    _want("w", w, torch.bfloat16, x.device)
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x must be [M, K] and w [N, K]")
+    n = w.shape[0]
+    if activation == "swiglu":
+        if n % 2 != 0:
+            raise ValueError("w must hold as many gate as up rows")
+        n //= 2
+    return x.device, x.shape[0], x.shape[1], n
+
+
+def linear(x, w, bias=None, activation="none", residual=None, out=None, dtype=torch.bfloat16, z=None,
+           workspace=None, status=None):
+    """``act(x w^T + bias) + residual``: ``x`` [M, K] bf16, ``w`` [N, K] bf16
+    (swiglu: [2N, K], gate rows, then up rows), ``bias`` float32 or bf16, one
+    per row of ``w``; ``out`` [M, N] and ``residual`` float32 or bf16 (``dtype``
+    where ``out`` is not given; swiglu: bf16).  ``z``, of one column per row of
+    ``w``, where given, gets the pre-activations in bf16, which
+    ``linear_backward`` takes (see ``ep_linear``)."""
+    dev, M, K, N = _check_linear(x, w, activation)
+    out = _result_of_types("out", out, (M, N), dtype, dev)
+    if activation == "swiglu" and out.dtype is not torch.bfloat16:
+        raise ValueError("swiglu gives bfloat16")
+    if bias is not None:
+        _result_of_types("bias", bias, (w.shape[0],), None, dev)
+    if residual is not None:
+        _result("residual", residual, (M, N), out.dtype, dev)
+    if z is not None:
+        _result("z", z, (M, w.shape[0]), torch.bfloat16, dev)
+    lib = load()
+    act = ACTIVATIONS[activation]
+    need = lib.ep_linear_workspace_bytes(M, K, N, act)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _want("workspace", workspace, workspace.dtype, dev)
+    _rc("ep_linear", _on_current(
+        dev, lib.ep_linear, x.data_ptr(), M, K, w.data_ptr(), N, _addr(bias),
+        TYPES[torch.float32 if bias is None else bias.dtype], act, _addr(residual), out.data_ptr(),
+        TYPES[out.dtype], _addr(z), _status_addr(status, dev), _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_of(dev)))
+    return out
+
+
+LinearGrads = namedtuple("LinearGrads", "dx dw dbias dz")
+
+
+def linear_backward(dy, x, w, z=None, activation="none", dz=None, dx=None, dw=None, dbias=None, add=None,
+                    dtype=torch.float32, with_dx=True, with_dw=True, with_dbias=True, status=None):
+    """Gradients of ``linear`` from ``dy`` [M, N] bf16 and the pre-activations
+    ``z`` that it kept (none for activation "none"): dx [M, K] bf16, dw of w's
+    shape (float32 or bf16, ``dtype`` where ``dw`` is not given) with ``add``,
+    which may be ``dw`` itself, added to it, dbias float32, and dz bf16, the
+    gradient of the pre-activations.  The residual's gradient is ``dy``.  Those
+    not wanted are None (see ``ep_linear_backward``)."""
+    dev, M, K, N = _check_linear(x, w, activation)
+    _want("dy", dy, torch.bfloat16, dev)
+    if tuple(dy.shape) != (M, N):
+        raise ValueError("dy must be [M, N]")
+    if (z is None) != (activation == "none"):
+        raise ValueError("z must be what linear kept, and None without an activation")
+    if z is not None:
+        _result("z", z, (M, w.shape[0]), torch.bfloat16, dev)
+        dz = _result("dz", dz, z.shape, torch.bfloat16, dev)
+    elif dz is not None:
+        raise ValueError("there is no dz without an activation")
+    dx = _result("dx", dx, (M, K), torch.bfloat16, dev) if with_dx else None
+    dw = _result_of_types("dw", dw, w.shape, dtype, dev) if with_dw else None
+    if add is not None:
+        if dw is None:
+            raise ValueError("there is nothing to add to without dw")
+        _result("add", add, dw.shape, dw.dtype, dev)
+    dbias = _result("dbias", dbias, (w.shape[0],), torch.float32, dev) if with_dbias else None
+    _rc("ep_linear_backward", _on_current(
+        dev, load().ep_linear_backward, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _addr(z), M, K, N,
+        ACTIVATIONS[activation], _addr(dz), _addr(dx), _addr(add), _addr(dw),
+        0 if dw is None else TYPES[dw.dtype], _addr(dbias), _status_addr(status, dev), _stream_of(dev)))
+    return LinearGrads(dx, dw, dbias, dz)
+
+
+def combine_backward(dout, y, topk_w, dst_row, dy=None, dw=None, status=None):
+    """Gradients of ``combine``: ``dout`` [T, H] bf16 to (dy [rows, H] bf16, the
+    gradient of the experts' outputs ``y``, and dw [T, k] float32, that of
+    ``topk_w``).  Rows that no pair maps to keep what ``dy`` held (see
+    ``ep_combine_backward``)."""
+    _check_dev("dout", dout, torch.bfloat16)
+    dev = dout.device
+    for name, t, dt in (("y", y, torch.bfloat16), ("topk_w", topk_w, torch.float32), ("dst_row", dst_row, torch.int32)):
+        _want(name, t, dt, dev)
+    if dout.dim() != 2 or y.dim() != 2 or y.shape[1] != dout.shape[1]:
+        raise ValueError("dout must be [T, H] and y [rows, H]")
+    T, H = dout.shape
+    if dst_row.dim() != 2 or dst_row.shape[0] != T or topk_w.shape != dst_row.shape:
+        raise ValueError("topk_w and dst_row must be [T, k]")
+    dy = _result("dy", dy, y.shape, torch.bfloat16, dev)
+    dw = _result("dw", dw, topk_w.shape, torch.float32, dev)
+    _rc("ep_combine_backward", _on_current(
+        dev, load().ep_combine_backward, dout.data_ptr(), y.data_ptr(), topk_w.data_ptr(), dst_row.data_ptr(),
+        T, H, dst_row.shape[1], y.shape[0], dy.data_ptr(), dw.data_ptr(), _status_addr(status, dev),
+        _stream_of(dev)))
+    return dy, dw
 
 
 def status_read(status):

@@ -1,0 +1,101 @@
+// ep_products.cuh -- what the BF16 products of an expert layer share: their
+// arguments, the activations and their derivatives, and the launchers.
+#pragma once
+
+#include "ep_experts.cuh"
+
+namespace ep {
+
+// The three products of rows [rows, K] or [rows, N] with weights [E, N, K]:
+//   kForward  out[r, n] = sum_k x[r, k] w[e, n, k]
+//   kInput    dx[r, k]  = sum_n dy[r, n] w[e, n, k]
+//   kWeight   dw[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
+enum ProductKind { kForward = 0, kInput = 1, kWeight = 2 };
+
+struct ProductArgs {
+    // operands: kForward x, w; kInput dy, w; kWeight dy, x
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t rows;  // of the buffers
+    int64_t N, K;  // rows and width of an expert's weights; with SwiGLU N counts gate and up rows
+    int E;
+    // segments; counts == nullptr: one expert with all rows
+    const int32_t* counts;
+    const int32_t* offsets;
+    int kind, capacity;
+    // epilogue
+    int activation;       // kForward: EP_ACT_*; kInput: EP_ACT_SWIGLU gives dz from z
+    const void* bias;     // [N] or nullptr
+    int bias_type;
+    const void* residual; // of out_type, or nullptr
+    const void* add;      // kWeight: of out_type, or nullptr
+    void* out;
+    int out_type;
+    uint16_t* z;          // kForward: pre-activations out or nullptr; kInput with SwiGLU: in
+    uint32_t* status;
+};
+
+// Rows of expert e (of the whole buffer where there are no experts).
+__device__ __forceinline__ Segment product_segment(const ProductArgs& p, int e) {
+    if (p.counts == nullptr) return Segment{0, p.rows, false};
+    return expert_segment(e, p.counts, p.offsets, p.kind, p.capacity, p.rows);
+}
+
+// 1 / (1 + exp(-v)), the exponential and the quotient each good to 2 ulp; far
+// below zero the divisor reaches 2^126, for which the quotient is 0, the limit.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, __fadd_rn(1.0f, expf(-v))); }
+
+__device__ __forceinline__ float activate(float v, int act) {
+    switch (act) {
+        case EP_ACT_RELU: return v < 0.0f ? 0.0f : v;  // keeps NaN
+        case EP_ACT_SILU: return v * sigmoid(v);
+        case EP_ACT_GELU: return v * normcdff(v);  // 1 + erf would cancel far below zero
+        default: return v;
+    }
+}
+
+// d act / d v, times dy.  The tails are those of the functions: both factors of
+// GELU's second term vanish far from zero.
+__device__ __forceinline__ float activate_back(float v, float dy, int act) {
+    switch (act) {
+        case EP_ACT_RELU: return v > 0.0f ? dy : v == v ? 0.0f : v;
+        case EP_ACT_SILU: {
+            const float s = sigmoid(v);
+            return dy * s * fmaf(v, 1.0f - s, 1.0f);
+        }
+        case EP_ACT_GELU: {
+            return dy * fmaf(v * 0.39894228040143268f, expf(-0.5f * v * v), normcdff(v));
+        }
+        default: return dy;
+    }
+}
+
+// Gradients of gate and up of h = silu(g) u.
+__device__ __forceinline__ void swiglu_back(float g, float u, float dh, float& dg, float& du) {
+    const float s = sigmoid(g);
+    const float ds = dh * s;
+    dg = ds * u * fmaf(g, 1.0f - s, 1.0f);
+    du = ds * g;
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)pack_bf16x2_rn(v, 0.0f); }
+__device__ __forceinline__ float load_typed(const void* p, int type, int64_t i) {
+    return type == EP_TYPE_F32 ? __ldg(static_cast<const float*>(p) + i)
+                               : bf16_value(__ldg(static_cast<const uint16_t*>(p) + i));
+}
+
+// ---- launchers (host) ------------------------------------------------------
+
+cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream);
+
+// dz (unless nullptr) and column sums of the unrounded dz (unless nullptr)
+cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M, int64_t N,
+                                int activation, uint16_t* dz, float* dbias, cudaStream_t stream);
+
+cudaError_t launch_combine_backward(const void* dout, const void* y, const float* topk_w,
+                                    const int32_t* dst_row, int64_t T, int64_t H, int k,
+                                    int64_t rows, void* dy, float* dw, uint32_t* status,
+                                    cudaStream_t stream);
+
+}  // namespace ep

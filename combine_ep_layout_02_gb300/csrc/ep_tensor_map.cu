@@ -27,12 +27,13 @@ cudaError_t encoder(Encode* out) {
 }
 
 cudaError_t encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                   const cuuint64_t* strides, const cuuint32_t* box) {
+                   const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8) {
     Encode fn;
     const cudaError_t err = encoder(&fn);
     if (err != cudaSuccess) return err;
-    const cuuint32_t steps[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base),
+    const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(base),
                           dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -55,6 +56,18 @@ cudaError_t byte_blocks_map(CUtensorMap* map, const void* base, int64_t rows, in
     const cuuint64_t strides[2] = {(cuuint64_t)width, 128};
     const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)blocks};
     return encode(map, base, 3, dims, strides, box);
+}
+
+cudaError_t bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box) {
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0) s[i - 1] = strides[i - 1];
+    }
+    return encode(map, base, rank, d, s, b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 }  // namespace ep

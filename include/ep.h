@@ -2,8 +2,9 @@
  * ep.h -- C ABI of the GB300 (sm_103a) MoE expert-parallel hot path:
  * routing layout, dispatch (BF16 or FP8 e4m3 with per-128-channel scales)
  * and weighted top-k combine, and what stands around them in an expert
- * layer: the router's choice, the experts' FP8 products, and the whole layer
- * for a few tokens; all on one GPU.
+ * layer: the router's choice, the experts' FP8 products, the whole layer for a
+ * few tokens, the experts' BF16 products and the dense product beside them
+ * with their gradients; all on one GPU.
  *
  * The operations are the local steps of DeepEP-style dispatch/combine as the
  * pages state the problem ("Replace EP backend comparison with Decode-like
@@ -96,7 +97,15 @@ enum {
 };
 
 typedef enum { EP_LAYOUT_CONTIGUOUS = 0, EP_LAYOUT_MASKED = 1 } ep_layout_kind_t;
-typedef enum { EP_TYPE_F32 = 0, EP_TYPE_BF16 = 1 } ep_type_t;           /* of ep_route's logits */
+typedef enum { EP_TYPE_F32 = 0, EP_TYPE_BF16 = 1 } ep_type_t; /* of ep_route's logits, of outputs
+                                                                 and biases where a call says so */
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,  /* max(v, 0) */
+    EP_ACT_SILU = 2,  /* v / (1 + exp(-v)) */
+    EP_ACT_GELU = 3,  /* v * (1 + erf(v / sqrt(2))) / 2 */
+    EP_ACT_SWIGLU = 4 /* silu(gate) * up: two rows of weights per output channel */
+} ep_activation_t;
 typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t; /* of ep_route's weights */
 
 /* Library version, (major << 16) | minor. */
@@ -434,6 +443,125 @@ EP_API int ep_moe_few(const void* x, int64_t T, int H, int k, const int32_t* top
                       const float* topk_w, const uint8_t* w13_q, const float* w13_scale,
                       const uint8_t* w2_q, const float* w2_scale, int I, int E, void* out,
                       uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' products over a dispatched BF16 buffer, and their gradients:
+ * what ep_dispatch wrote goes in, what ep_combine reads (or, backward, the
+ * gradient of the dispatched rows, for ep_combine with weights of 1) comes out.
+ * For row r of expert e:
+ *   ep_group_gemm            out[r, n] = bf16_rne( sum over k of a[r, k] * w[e, n, k] )
+ *   ep_group_gemm_swiglu     y as above in fp32 for the 2*I rows of w13 (gate rows, then
+ *                            up rows); out[r, i] = bf16_rne( y[r, i] / (1 + exp(-y[r, i]))
+ *                            * y[r, I + i] ), and, where z is not NULL, z = bf16_rne(y),
+ *                            which the backward pass needs
+ *   ep_group_gemm_dgrad      dx[r, k] = bf16_rne( sum over n of dy[r, n] * w[e, n, k] )
+ *   ep_group_gemm_swiglu_dgrad
+ *                            dh[r, i] = sum over h of dy[r, h] * w2[e, h, i] in fp32, and
+ *                            from it the gradient of the pre-activations z = (g, u), with
+ *                            s = 1 / (1 + exp(-g)):
+ *                              dz[r, i]     = bf16_rne( dh * u * s * (1 + g * (1 - s)) )
+ *                              dz[r, I + i] = bf16_rne( dh * g * s )
+ *   ep_group_gemm_wgrad      dw[e, n, k] = add[e, n, k] + sum over the expert's rows r of
+ *                            dy[r, n] * x[r, k], in dw_type; without `add` (NULL) from 0,
+ *                            so that an expert without rows gets zeros
+ * Sums of exact products of bf16 values are held in fp32, in a fixed order: the
+ * same inputs give the same bits.
+ *
+ *  a, dy, x   [rows, width] bf16 buffers in the dispatch layout, 16-byte aligned.
+ *  w, w13, w2 [E, N, K], [E, 2*I, K] and [E, H, I] bf16, 16-byte aligned.
+ *  z, dz      [rows, 2*I] bf16, 16-byte aligned.
+ *  dw, add    [E, N, K] of dw_type, 16-byte aligned; add may be dw itself.
+ *  expert_counts, expert_offsets, kind, capacity: as for ep_group_gemm_fp8.
+ *             Rows of no segment are never written and change no result,
+ *             whatever they hold; up to 255 rows that follow a segment in the
+ *             buffer may be read.
+ * Outputs overlap no input (but dw may be add).
+ * Limits: all widths multiples of 8, I a multiple of 16; rows < 2^31; E <=
+ * EP_MAX_EXPERTS; E * (rows of weights per expert) < 2^31.
+ */
+EP_API int ep_group_gemm(const void* a, int64_t rows, int64_t K, const void* w, int64_t N, int E,
+                         const int32_t* expert_counts, const int32_t* expert_offsets, int kind,
+                         int capacity, void* out, uint32_t* status, void* stream);
+EP_API int ep_group_gemm_swiglu(const void* a, int64_t rows, int64_t K, const void* w13,
+                                int64_t I, int E, const int32_t* expert_counts,
+                                const int32_t* expert_offsets, int kind, int capacity, void* out,
+                                void* z, uint32_t* status, void* stream);
+EP_API int ep_group_gemm_dgrad(const void* dy, int64_t rows, int64_t N, const void* w, int64_t K,
+                               int E, const int32_t* expert_counts,
+                               const int32_t* expert_offsets, int kind, int capacity, void* dx,
+                               uint32_t* status, void* stream);
+EP_API int ep_group_gemm_swiglu_dgrad(const void* dy, int64_t rows, int64_t H, const void* w2,
+                                      int64_t I, int E, const void* z,
+                                      const int32_t* expert_counts,
+                                      const int32_t* expert_offsets, int kind, int capacity,
+                                      void* dz, uint32_t* status, void* stream);
+EP_API int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int64_t N, int64_t K,
+                               int E, const int32_t* expert_counts,
+                               const int32_t* expert_offsets, int kind, int capacity,
+                               const void* add, void* dw, int dw_type, uint32_t* status,
+                               void* stream);
+
+/*
+ * ep_linear -- the dense product beside the experts (the router's logits, a
+ * shared expert, the layer's residual):
+ *     y[m, n]   = sum over k of x[m, k] * w[n, k], + bias[n]              (fp32)
+ *     out[m, n] = act(y[m, n]) + residual[m, n], rounded once to out_type
+ * With EP_ACT_SWIGLU w is [2*N, K] and bias [2*N] (gate rows, then up rows) and
+ * act is silu(y[m, n]) * y[m, N + n].  Where z is not NULL it gets bf16_rne(y),
+ * which ep_linear_backward() needs.
+ *
+ *  x         [M, K] bf16;  w [N or 2*N, K] bf16, both 16-byte aligned.
+ *  bias      float32 or bf16 (bias_type), or NULL.
+ *  residual  [M, N] of out_type, 16-byte aligned, or NULL; may be out itself.
+ *  out       [M, N] float32 or bf16 (out_type), 16-byte aligned.
+ *  z         [M, N or 2*N] bf16, 16-byte aligned, or NULL.
+ *  workspace ep_linear_workspace_bytes(M, K, N, activation) bytes, 16-byte
+ *            aligned, no initialisation needed; may be NULL where that is 0.
+ * Limits: K and N multiples of 8; with EP_ACT_SWIGLU N a multiple of 16 and
+ * out_type EP_TYPE_BF16; M < 2^31, rows of w < 2^31.  M == 0 is valid.
+ */
+EP_API size_t ep_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation);
+EP_API int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N,
+                     const void* bias, int bias_type, int activation, const void* residual,
+                     void* out, int out_type, void* z, uint32_t* status, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * ep_linear_backward -- gradients of ep_linear (the residual's is dy itself):
+ *     dz    = dy * act'(z) in fp32, kept as bf16_rne (EP_ACT_NONE: dy, no dz)
+ *     dbias = sum over m of dz[m, :], of the unrounded dz, in fp32
+ *     dx    = bf16_rne( dz w )            dw = add + dz^T x in dw_type
+ * dx and dw are the products of the rounded dz.  relu'(0) = 0.
+ *
+ *  dy        [M, N] bf16, 16-byte aligned;  x, w as for ep_linear.
+ *  z         [M, N or 2*N] bf16 as ep_linear wrote it; NULL for EP_ACT_NONE.
+ *  dz        of z's shape, out; required where z is, else NULL.
+ *  dx        [M, K] bf16 out or NULL;  dw [N or 2*N, K] of dw_type out or NULL
+ *            (x may be NULL without dw, w without dx);  dbias [N or 2*N] float32
+ *            out or NULL;  add as for ep_group_gemm_wgrad.
+ *  Alignment and limits as above.  M == 0 gives dw = add (or 0) and dbias = 0.
+ */
+EP_API int ep_linear_backward(const void* dy, const void* x, const void* w, const void* z,
+                              int64_t M, int64_t K, int64_t N, int activation, void* dz, void* dx,
+                              const void* add, void* dw, int dw_type, float* dbias,
+                              uint32_t* status, void* stream);
+
+/*
+ * ep_combine_backward -- gradients of ep_combine: for every pair with
+ * dst_row[t, j] = r >= 0
+ *     dy[r, h]    = bf16_rne( topk_w[t, j] * dout[t, h] )
+ *     dw[t, j]    = sum over h of dout[t, h] * y[r, h]                  (fp32)
+ * and dw[t, j] = 0 for the others.  Rows of dy that no pair maps to are not
+ * touched.  The order of each sum is fixed.
+ *
+ *  dout [T, H], y [rows, H], dy [rows, H] bf16, 16-byte aligned;  topk_w, dw
+ *  [T, k] float32;  dst_row [T, k] int32 as for ep_combine, a dst_row outside
+ *  [-1, rows) being skipped and raising EP_FLAG_BAD_ROW.  dy overlaps no input.
+ *  dw NULL: dy alone is computed and y may be NULL.
+ */
+EP_API int ep_combine_backward(const void* dout, const void* y, const float* topk_w,
+                               const int32_t* dst_row, int64_t T, int64_t H, int k, int64_t rows,
+                               void* dy, float* dw, uint32_t* status, void* stream);
 
 /*
  * Two-stage (rank, then expert) form of dispatch and combine -- the shape of
