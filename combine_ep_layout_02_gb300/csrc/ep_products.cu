@@ -1,134 +1,727 @@
-// ep_products.cu -- BF16 products grouped by expert, with their gradients.
+// ep_products.cu -- BF16 products grouped by expert, and their gradients, on
+// tcgen05.  For rows r of expert e:
+//   forward  out[r, n] = sum_k x[r, k] w[e, n, k]       (dense: one expert)
+//   input    dx[r, k]  = sum_n dy[r, n] w[e, n, k]
+//   weight   dw[e, n, k] = sum_r dy[r, n] x[r, k]
+// bf16 operands, fp32 sums, and an epilogue on the sums: bias, activation or
+// SwiGLU and residual (forward), SwiGLU's derivative (input), an addend
+// (weight).
 //
-// One block per 64 x 64 outputs of an expert, 4 x 4 per thread, fp32 FMAs from
-// shared memory: right for every case, and bound by those FMAs.
+// A tile is the product of a pair of SMs: 256 x up to 256 sums, 128 of the rows
+// in each block's TMEM, both blocks' halves of the other operand shared.  The
+// 256 rows are the weights' output channels (weight: the channels of dy); the
+// columns are the expert's tokens (weight: the channels of x).  Tokens are the
+// ragged side, and the column count of an MMA goes in steps of 32, so that an
+// expert's tokens are split evenly and rounded up to 32, where rows would be
+// rounded up to 256 (16,384 rows over 32 experts: 6 % instead of 25 % wasted).
+// What a kernel reads as rows or columns may have its summed index or its rows
+// contiguous in memory; tcgen05 takes either through the descriptors, so that no
+// operand is transposed.
+//
+// Forward and input: an expert's last columns may hold rows of the next
+// segment, which only reach columns that are not written.  Weight: the tokens
+// are the summed index, and rows behind the segment may hold anything, so that
+// the last block's rows are overwritten with zeros in shared memory before the
+// MMAs read them.
+//
+// One persistent block per SM: warp 0 issues the TMA loads (128-byte swizzle,
+// six stages of 64 values of the summed index), warp 1 of the even block the
+// MMAs, warp 2 clears the tails, warps 4-7 write the output while the next
+// tile's MMAs run into the other half of the TMEM.  TMEM lanes are channels;
+// the output's rows are tokens.  Sums are read in an mma accumulator's layout
+// and turned by stmatrix, so that the stores run along the channels.
 #include "ep_products.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kTileM = 256, kTileN = 256, kBlockK = 64;  // per pair
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * kBlockK * 2, kBBytes = 128 * kBlockK * 2;  // per block and stage
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kThreads = 256;
+constexpr int kEpiWarps = 4;
+constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels
+constexpr int kSlots = 2;        // per warp
+constexpr int kBand = 16;        // channel tiles that share the tokens while they are in L2
+
+struct Shared {
+    alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int gave_up;
+    int first[EP_MAX_EXPERTS], count[EP_MAX_EXPERTS];
+    int tiles[EP_MAX_EXPERTS + 1];  // exclusive scan of the experts' token tiles
+};
+
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kSlots * kSlot + sizeof(Shared);
+static_assert(kSmem <= 227 * 1024, "");
+
+struct Maps {
+    CUtensorMap a;    // the 256-row side: weights; dy
+    CUtensorMap b64;  // the other: boxes of 64 tokens (weight: of 64 tokens x 64 channels of x)
+    CUtensorMap b16;  // boxes of 16 tokens
+};
+
+struct Tile {
+    int e;
+    int m0;       // first channel of the pair's 256 (SwiGLU forward: of 128)
+    int row;      // first token; weight: the segment's first
+    int n;        // valid columns
+    int width;    // columns of the MMA
+    int n0;       // weight: first channel of x
+    int blocks;   // of the summed index
+    int tail;     // weight: rows of the last block that count, 0: all
+};
+
+// Sizes of a call that every role derives its tiles from.
+struct Grid {
+    int channels;     // output channels on the 256-row side
+    int per;          // of them in a tile
+    int mtiles;       // tiles of them
+    int ntiles;       // weight: tiles of x's channels
+    int most;         // columns of a tile at most
+    int blocks;       // of the summed index (not weight)
+    uint64_t total;   // tiles
+};
+
+template <ProductKind KIND>
+struct Walk {
+    int e = 0;
+    // Tile i, as a whole warp walks them in increasing order.
+    __device__ __forceinline__ Tile tile(const Shared& sh, const Grid& g, int E, uint64_t i) {
+        Tile t;
+        if (KIND == kWeight) {
+            const uint32_t per = (uint32_t)g.mtiles * g.ntiles;
+            t.e = (int)(i / per);
+            const uint32_t r = (uint32_t)(i - (uint64_t)t.e * per);
+            t.m0 = (int)(r / g.ntiles) * kTileM;
+            t.n0 = (int)(r % g.ntiles) * g.most;
+            t.row = sh.first[t.e];
+            const int count = sh.count[t.e];
+            t.blocks = (count + kBlockK - 1) / kBlockK;
+            t.tail = count % kBlockK;
+            t.width = g.most;
+            t.n = g.most;
+            return t;
+        }
+        const int lane = threadIdx.x & 31;
+        const uint64_t at = i / (uint32_t)g.mtiles;  // the expert's share: mtiles for each of its token tiles
+        unsigned past;
+        while ((past = __ballot_sync(kFullMask, (uint64_t)sh.tiles[min(e + 1 + lane, E)] > at)) == 0) e += 32;
+        e += __ffs(past) - 1;
+        const uint32_t tokens = (uint32_t)(sh.tiles[e + 1] - sh.tiles[e]);
+        const uint64_t r = i - (uint64_t)sh.tiles[e] * (uint32_t)g.mtiles;
+        // bands of channel tiles; within a band all channels of a token tile, then the next token tile
+        const uint64_t band_size = (uint64_t)tokens * kBand;
+        const uint32_t band = (uint32_t)(r / band_size);
+        const uint32_t in = (uint32_t)(r - band * band_size);
+        const uint32_t wide = min((uint32_t)kBand, (uint32_t)g.mtiles - band * kBand);
+        const uint32_t tt = in / wide;
+        const int count = sh.count[e];
+        t.e = e;
+        t.m0 = (int)(band * kBand + in % wide) * g.per;
+        t.width = (int)(((uint32_t)(count + tokens - 1) / tokens + 31) / 32 * 32);
+        t.row = sh.first[e] + (int)tt * t.width;
+        t.n = min(t.width, count - (int)tt * t.width);  // more than (tokens - 1) * most >= (tokens - 1) * width
+        t.n0 = 0;
+        t.blocks = g.blocks;
+        t.tail = 0;
+        return t;
+    }
+};
+
+// ---- the epilogue's pieces ---------------------------------------------------
+
+// A warp's 32 tokens x 32 channels (SwiGLU forward: 16) of bf16 in shared
+// memory, 16-byte pieces exchanged so that neither the fragments' nor the rows'
+// accesses share a bank.
+template <int PIECES>  // 16-byte pieces per token: 4 or 2
+__device__ __forceinline__ uint32_t slot_at(uint32_t slot, int token, int piece) {
+    return slot + token * (PIECES * 16) + ((piece ^ ((token >> (PIECES == 4 ? 1 : 2)) & (PIECES - 1))) << 4);
+}
+
+// A lane's address for half `h` (channels 16h..) and token groups c, c + 1.
+template <int PIECES>
+__device__ __forceinline__ uint32_t fragment_at(uint32_t slot, int h, int c) {
+    const int lane = threadIdx.x & 31, j = lane >> 3;
+    return slot_at<PIECES>(slot, 8 * (c + (j >> 1)) + (lane & 7), 2 * h + (j & 1));
+}
+
+template <int PIECES>
+__device__ __forceinline__ void put_fragments(uint32_t slot, int h, const float (&v)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = pack_bf16x2_rn(v[4 * c + 2 * j], v[4 * c + 2 * j + 1]);
+        stmatrix_trans(fragment_at<PIECES>(slot, h, c), q);
+    }
+}
+template <int PIECES>
+__device__ __forceinline__ void get_fragments(uint32_t slot, int h, float (&v)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        uint32_t q[4];
+        ldmatrix_trans(q, fragment_at<PIECES>(slot, h, c));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[4 * c + 2 * j] = bf16lo_to_f32(q[j]);
+            v[4 * c + 2 * j + 1] = bf16hi_to_f32(q[j]);
+        }
+    }
+}
+
+// Rows of the slot to memory (or back): `tokens` of 32, the first `channels`
+// (a multiple of 8) of a token's channels, ld apart.
+template <int PIECES, bool LOAD>
+__device__ __forceinline__ void move_rows(uint32_t slot, uint16_t* at, int64_t ld, int tokens, int channels) {
+    const int lane = threadIdx.x & 31, piece = lane % PIECES;
+#pragma unroll
+    for (int t0 = 0; t0 < 32; t0 += 32 / PIECES) {
+        const int t = t0 + lane / PIECES;
+        const uint32_t s = slot_at<PIECES>(slot, t, piece);
+        if (t < tokens && piece * 8 < channels) {
+            uint16_t* p = at + t * ld + piece * 8;
+            uint4 v;
+            if (LOAD) {
+                v = ld_stream_v4(p);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(s), "r"(v.x), "r"(v.y), "r"(v.z),
+                             "r"(v.w)
+                             : "memory");
+            } else {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(s)
+                             : "memory");
+                st_v4(p, v);
+            }
+        }
+    }
+}
+
+template <int PIECES>
+__device__ __forceinline__ void write_rows(uint32_t slot, uint16_t* at, int64_t ld, int tokens, int channels) {
+    __syncwarp();
+    move_rows<PIECES, false>(slot, at, ld, tokens, channels);
+    __syncwarp();
+}
+template <int PIECES>
+__device__ __forceinline__ void read_rows(uint32_t slot, const uint16_t* at, int64_t ld, int tokens, int channels) {
+    move_rows<PIECES, true>(slot, const_cast<uint16_t*>(at), ld, tokens, channels);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void as_floats(const uint32_t (&v)[16], float (&f)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+}
+
+__device__ __forceinline__ void activate16(float (&f)[16], int act) {
+    if (act == EP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = activate(f[i], EP_ACT_RELU);
+    } else if (act == EP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = activate(f[i], EP_ACT_SILU);
+    } else if (act == EP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = activate(f[i], EP_ACT_GELU);
+    }
+}
 
 template <ProductKind KIND, bool SWIGLU>
-__global__ void __launch_bounds__(kThreads) product_kernel(const __grid_constant__ ProductArgs p) {
-    // m: rows of the buffer (kWeight: of the weights); n: output channels; c: the summed index
-    constexpr bool pair = SWIGLU && KIND == kForward;
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1], su[pair ? kStep : 1][kTile + 1];
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p, int most) {
+    constexpr bool kGated = SWIGLU && KIND == kForward;  // two rows of weights per output channel
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* slots = stages + kStages * kStageBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(slots + kEpiWarps * kSlots * kSlot);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), tail = smem_addr(sh.tail);
+    const uint32_t acc_full = smem_addr(sh.acc_full), acc_empty = smem_addr(sh.acc_empty);
+    const uint32_t drain = smem_addr(&sh.drain);
+    volatile int* gave_up = &sh.gave_up;
+
+    if (warp == 0) tmem_alloc_pair(smem_addr(&sh.tmem), 512);
+    if (tid == 32) {
+        tma_prefetch_map(&maps.a);
+        tma_prefetch_map(&maps.b64);
+        if (KIND != kWeight) tma_prefetch_map(&maps.b16);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, KIND == kWeight ? 2 : 1);
+            mbar_init(empty + 8 * i, 1);
+            mbar_init(tail + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.gave_up = 0;
+    }
     pdl_wait();
     pdl_trigger();
-    const int e = blockIdx.z;
-    const Segment s = product_segment(p, e);
-    if (s.bad && p.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        atomicOr(p.status, EP_FLAG_BAD_ROW);
-    const int64_t half = pair ? p.N / 2 : 0;
-    const int64_t nn = KIND == kForward ? (pair ? half : p.N) : p.K;  // output channels
-    const int64_t mm = KIND == kWeight ? p.N : s.count;
-    const int64_t cc = KIND == kForward ? p.K : KIND == kInput ? p.N : s.count;
-    const uint16_t* w = p.b + (int64_t)e * p.N * p.K;
-    const int64_t n0 = (int64_t)blockIdx.x * kTile;
-    const int tm = (threadIdx.x / 16) * 4, tn = (threadIdx.x % 16) * 4;
-    for (int64_t m0 = (int64_t)blockIdx.y * kTile; m0 < mm; m0 += (int64_t)gridDim.y * kTile) {
-        float acc[4][4] = {}, accu[4][4] = {};
-        for (int64_t c0 = 0; c0 < cc; c0 += kStep) {
-            for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-                // the index that is contiguous in memory varies fastest over the threads
-                const int mc = KIND == kWeight ? i / kTile : i % kStep, mx = KIND == kWeight ? i % kTile : i / kStep;
-                const int64_t m = m0 + mx, c = c0 + mc;
-                float v = 0.0f;
-                if (m < mm && c < cc)
-                    v = KIND == kWeight ? bf16_value(p.a[(s.first + c) * p.N + m])
-                                        : bf16_value(p.a[(s.first + m) * cc + c]);
-                sa[mc][mx] = v;
-            }
-            for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-                const int nc = KIND == kForward ? i % kStep : i / kTile, nx = KIND == kForward ? i / kStep : i % kTile;
-                const int64_t n = n0 + nx, c = c0 + nc;
-                float v = 0.0f, u = 0.0f;
-                if (n < nn && c < cc) {
-                    if (KIND == kForward) {
-                        v = bf16_value(w[n * p.K + c]);
-                        if (pair) u = bf16_value(w[(half + n) * p.K + c]);
-                    } else if (KIND == kInput) {
-                        v = bf16_value(w[c * p.K + n]);
-                    } else {
-                        v = bf16_value(p.b[(s.first + c) * p.K + n]);
-                    }
-                }
-                sb[nc][nx] = v;
-                if (pair) su[nc][nx] = u;
-            }
-            __syncthreads();
-            for (int c = 0; c < kStep; ++c)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][j] = fmaf(sa[c][tm + i], sb[c][tn + j], acc[i][j]);
-                        if (pair) accu[i][j] = fmaf(sa[c][tm + i], su[c][tn + j], accu[i][j]);
-                    }
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + tm + i, n = n0 + tn + j;
-                if (m >= mm || n >= nn) continue;
-                const int64_t row = s.first + m;
-                float v = acc[i][j];
-                if (KIND == kWeight) {
-                    const int64_t at = ((int64_t)e * p.N + m) * p.K + n;
-                    if (p.add)
-                        v += p.out_type == EP_TYPE_F32 ? static_cast<const float*>(p.add)[at]
-                                                       : bf16_value(static_cast<const uint16_t*>(p.add)[at]);
-                    if (p.out_type == EP_TYPE_F32) static_cast<float*>(p.out)[at] = v;
-                    else static_cast<uint16_t*>(p.out)[at] = bf16_bits(v);
-                    continue;
-                }
-                if (KIND == kInput) {
-                    uint16_t* out = static_cast<uint16_t*>(p.out);
-                    if (!SWIGLU) {
-                        out[row * nn + n] = bf16_bits(v);
-                    } else {
-                        const int64_t at = row * 2 * nn + n;
-                        float dg, du;
-                        swiglu_back(bf16_value(p.z[at]), bf16_value(p.z[at + nn]), v, dg, du);
-                        out[at] = bf16_bits(dg);
-                        out[at + nn] = bf16_bits(du);
-                    }
-                    continue;
-                }
-                if (p.bias) v += load_typed(p.bias, p.bias_type, n);
-                if (pair) {
-                    float u = accu[i][j];
-                    if (p.bias) u += load_typed(p.bias, p.bias_type, nn + n);
-                    if (p.z) {
-                        p.z[row * 2 * nn + n] = bf16_bits(v);
-                        p.z[row * 2 * nn + nn + n] = bf16_bits(u);
-                    }
-                    v = swiglu(v, u);
-                } else {
-                    if (p.z) p.z[row * nn + n] = bf16_bits(v);
-                    v = activate(v, p.activation);
-                }
-                const int64_t at = row * nn + n;
-                if (p.residual)
-                    v += p.out_type == EP_TYPE_F32 ? static_cast<const float*>(p.residual)[at]
-                                                   : bf16_value(static_cast<const uint16_t*>(p.residual)[at]);
-                if (p.out_type == EP_TYPE_F32) static_cast<float*>(p.out)[at] = v;
-                else static_cast<uint16_t*>(p.out)[at] = bf16_bits(v);
-            }
+    for (int e = tid; e < p.E; e += kThreads) {
+        const Segment s = product_segment(p, e);
+        if (s.bad && blockIdx.x == 0 && p.status) atomicOr(p.status, EP_FLAG_BAD_ROW);
+        sh.first[e] = (int)s.first;
+        sh.count[e] = (int)s.count;
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (KIND != kWeight && warp == 0) {
+        int base = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int n = e0 + lane < p.E ? (int)(((int64_t)sh.count[e0 + lane] + most - 1) / most) : 0;
+            int s = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kFullMask, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e0 + lane < p.E) sh.tiles[e0 + lane] = base + s - n;
+            base += __shfl_sync(kFullMask, s, 31);
+        }
+        if (lane == 0) sh.tiles[p.E] = base;
+    }
+    __syncwarp();
+    cluster_sync();  // both blocks' barriers are set up
+
+    const uint32_t tmem = sh.tmem;
+    const int N = (int)p.N, K = (int)p.K;
+    Grid g;
+    g.channels = KIND == kForward ? (kGated ? N / 2 : N) : KIND == kInput ? K : N;
+    g.per = kGated ? kTileM / 2 : kTileM;
+    g.mtiles = (g.channels + g.per - 1) / g.per;
+    g.most = most;
+    g.ntiles = KIND == kWeight ? (K + most - 1) / most : 1;
+    g.blocks = ((KIND == kInput ? N : K) + kBlockK - 1) / kBlockK;
+    g.total = KIND == kWeight ? (uint64_t)p.E * g.mtiles * g.ntiles : (uint64_t)sh.tiles[p.E] * g.mtiles;
+    const uint32_t pair = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ---- loads: this block's 128 rows of A and its half of B's columns
+        const uint32_t bar0 = cluster_addr(full, 0);
+        uint32_t it = 0;
+        bool ok = true;
+        Walk<KIND> walk;
+        for (uint64_t i = pair; i < g.total && ok; i += step) {
+            const Tile t = walk.tile(sh, g, p.E, i);
+            const int half = t.width / 2;
+            const uint32_t bytes = kABytes + half * kBlockK * 2;
+            const int m = t.m0 + rank * (g.per / 2);          // this block's first channel
+            const int brow = t.row + rank * half;             // and token
+            for (int kb = 0; kb < t.blocks; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                if (!mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
+                const bool last = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1;
+                uint32_t bar = bar0 + 8 * s;
+                if (elect_one()) {
+                    if (KIND == kWeight) {
+                        if (last) {  // counted here, and passed on by warp 2
+                            bar = cluster_addr(tail, rank) + 8 * s;
+                            mbar_expect_tx(tail + 8 * s, bytes);
+                        } else {
+                            mbar_expect_tx_pair(bar, bytes);
+                        }
+                    } else if (rank == 0) {
+                        mbar_expect_tx(full + 8 * s, 2 * bytes);
+                    }
+                    const int k0 = kb * kBlockK;
+                    if (KIND == kWeight) {
+                        const int r0 = t.row + k0;
+                        tma_pair_2d(a, &maps.a, m, r0, bar);
+                        tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
+                        const int n = t.n0 + rank * half;
+                        for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b64, n + j, r0, bar);
+                    } else {
+                        if (kGated) {
+                            tma_pair_5d(a, &maps.a, k0, 0, 0, m / 16, t.e, bar);
+                        } else if (KIND == kForward) {
+                            tma_pair_3d(a, &maps.a, k0, m, t.e, bar);
+                        } else {
+                            tma_pair_3d(a, &maps.a, m, k0, t.e, bar);
+                            tma_pair_3d(a + kABytes / 2, &maps.a, m + 64, k0, t.e, bar);
+                        }
+                        int j = 0;
+                        for (; j + 64 <= half; j += 64) tma_pair_2d(b + j * 128, &maps.b64, k0, brow + j, bar);
+                        for (; j < half; j += 16) tma_pair_2d(b + j * 128, &maps.b16, k0, brow + j, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && rank == 0) {  // given up: the copies in flight end before the block does
+            const uint64_t start = global_ns();
+            for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
+                while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) &&
+                       global_ns() - start < 1000000000ull) {
+                }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMAs of the pair
+        uint32_t it = 0, done = 0;
+        bool ok = true;
+        Walk<KIND> walk;
+        for (uint64_t i = pair; i < g.total && ok; i += step) {
+            const Tile t = walk.tile(sh, g, p.E, i);
+            if (t.blocks == 0) continue;
+            const uint32_t buf = done & 1;
+            if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, gave_up)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * kTileN;
+            const uint32_t instr = bf16_instr_desc(kTileM, t.width, KIND != kForward, KIND == kWeight);
+            for (int kb = 0; kb < t.blocks; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                if (!mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                if (KIND == kWeight) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                tc_fence_after();
+                const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
+                // 16 values of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
+                const uint64_t da = KIND == kForward ? operand_desc(a) : operand_desc_mn(a, kABytes / 2);
+                const uint64_t db = KIND != kWeight ? operand_desc(b) : operand_desc_mn(b, 64 * 128);
+                constexpr uint64_t sa = (KIND == kForward ? 32 : 16 * 128) >> 4;
+                constexpr uint64_t sb = (KIND != kWeight ? 32 : 16 * 128) >> 4;
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < kBlockK / 16; ++j)
+                        mma_pair_bf16(d, da + j * sa, db + j * sb, instr, kb > 0 || j > 0);
+                    mma_commit_pair(empty + 8 * s);
+                    if (kb == t.blocks - 1) mma_commit_pair(acc_full + 8 * buf);
+                }
+                __syncwarp();
+            }
+            ++done;
+        }
+        if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
+            if (elect_one()) mma_commit_pair(drain);
+            __syncwarp();
+            const uint64_t start = global_ns();
+            while (!mbar_try_wait(drain, 0) && global_ns() - start < 1000000000ull) {
+            }
+        }
+    } else if (warp == 2 && KIND == kWeight) {
+        // ---- tails: zeros in the rows behind the segment
+        const uint32_t bar0 = cluster_addr(full, 0);
+        uint32_t it = 0, phases = 0;  // a stage's bit: the parity of its tail barrier
+        Walk<KIND> walk;
+        for (uint64_t i = pair; i < g.total; i += step) {
+            const Tile t = walk.tile(sh, g, p.E, i);
+            it += t.blocks;
+            if (t.blocks == 0 || t.tail == 0) continue;
+            const uint32_t s = (it - 1) % kStages;
+            if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up)) break;
+            phases ^= 1u << s;
+            uint8_t* a = stages + s * kStageBytes;
+            const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
+            for (int q = t.tail * 8 + lane; q < 64 * 8; q += 32)
+                for (int j = 0; j < boxes; ++j)
+                    reinterpret_cast<uint4*>(a + j * 8192)[q] = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(bar0 + 8 * s);
+        }
+    } else if (warp >= 4) {
+        // ---- output
+        const int quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t slot = smem_addr(slots) + quarter * kSlots * kSlot;
+        const uint32_t bar0 = cluster_addr(acc_empty, 0);
+        uint32_t done = 0;
+        Walk<KIND> walk;
+        for (uint64_t i = pair; i < g.total; i += step) {
+            const Tile t = walk.tile(sh, g, p.E, i);
+            const uint32_t buf = done & 1;
+            const uint32_t src = lanes + buf * kTileN;
+            if (t.blocks > 0) {
+                if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) break;
+                tc_fence_after();
+            }
+            auto release = [&]() {  // the buffer's last sums are in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+            };
+            if (KIND == kWeight) {
+                // a lane is a row of dw
+                const int64_t n = t.m0 + (int64_t)rank * 128 + quarter * 32 + lane;
+                const int64_t at = ((int64_t)t.e * N + n) * K + t.n0;
+                const int cols = min(t.width, K - t.n0);  // a multiple of 8
+                for (int c = 0; c < t.width; c += 32) {
+                    uint32_t v[2][16];
+                    __syncwarp();
+                    if (t.blocks > 0) {
+                        tmem_load(v[0], src + c);
+                        tmem_load(v[1], src + c + 16);
+                        tmem_wait_for(v[0]);
+                        tmem_wait_for(v[1]);
+                        if (c + 32 >= t.width) release();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0;
+                    }
+                    if (n >= N) continue;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {  // 8 columns at a time
+                        if (c + 8 * j >= cols) continue;
+                        float f[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(v[j >> 1][(j & 1) * 8 + x]);
+                        const int64_t o = at + c + 8 * j;
+                        if (p.out_type == EP_TYPE_F32) {
+                            if (p.add) {
+                                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + o);
+                                const float4 lo = q[0], hi = q[1];
+                                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+                                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+                            }
+                            uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
+                            st_v4(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                                __float_as_uint(f[3])));
+                            st_v4(q + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                                    __float_as_uint(f[6]), __float_as_uint(f[7])));
+                        } else {
+                            if (p.add) {
+                                const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.add) + o);
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    f[2 * x] += bf16lo_to_f32(w[x]);
+                                    f[2 * x + 1] += bf16hi_to_f32(w[x]);
+                                }
+                            }
+                            st_v4(static_cast<uint16_t*>(p.out) + o,
+                                  make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]),
+                                             pack_bf16x2_rn(f[4], f[5]), pack_bf16x2_rn(f[6], f[7])));
+                        }
+                    }
+                }
+                if (t.blocks > 0) ++done;
+                continue;
+            }
+            // lanes are channels, columns tokens
+            const int span = kGated ? 16 : 32;  // output channels of this warp
+            const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
+            const int chans = min(span, g.channels - ch);
+            if (chans <= 0) {
+                release();
+                ++done;
+                continue;
+            }
+            if (KIND == kForward && !SWIGLU && p.out_type == EP_TYPE_F32) {
+                // a lane's channel for one token after the other: whole lines of fp32
+                const int n = ch + lane;
+                const bool live = n < g.channels;
+                const float b = p.bias && live ? load_typed(p.bias, p.bias_type, n) : 0.0f;
+                for (int c = 0; c < t.n; c += 16) {
+                    uint32_t v[16];
+                    __syncwarp();
+                    tmem_load(v, src + c);
+                    tmem_wait_for(v);
+                    if (c + 16 >= t.n) release();
+                    float f[16];
+                    as_floats(v, f);
+                    const int64_t at = (int64_t)(t.row + c) * g.channels + n;
+                    const int tokens = min(16, t.n - c);
+                    if (p.bias) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] += b;
+                    }
+                    if (p.z && live) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j < tokens) p.z[at + (int64_t)j * g.channels] = bf16_bits(f[j]);
+                    }
+                    activate16(f, p.activation);
+                    if (live) {
+                        const float* res = static_cast<const float*>(p.residual);
+                        if (res) {
+                            float r[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[j] = j < tokens ? res[at + (int64_t)j * g.channels] : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) f[j] += r[j];
+                        }
+                        float* out = static_cast<float*>(p.out);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (j < tokens) out[at + (int64_t)j * g.channels] = f[j];
+                    }
+                }
+                ++done;
+                continue;
+            }
+            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // biases of this lane's channels
+            if (KIND == kForward && p.bias) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = 8 * j + lane / 4;  // TMEM lane of the warp
+                    const int n = kGated ? ch + k % 16 + (j >= 2 ? g.channels : 0) : ch + k;
+                    if (kGated || n < g.channels) b[j] = load_typed(p.bias, p.bias_type, n);
+                }
+            }
+            for (int c = 0; c < t.n; c += 32) {
+                const int tokens = min(32, t.n - c);
+                const int64_t row = t.row + c;
+                uint32_t v[2][16];
+                tmem_load_16x256(v[0], src + c);
+                tmem_load_16x256(v[1], src + c + (16u << 16));
+                tmem_wait_for(v[0]);
+                tmem_wait_for(v[1]);
+                if (c + 32 >= t.n) release();
+                float f[2][16];
+                as_floats(v[0], f[0]);
+                as_floats(v[1], f[1]);
+                if (KIND == kForward && p.bias) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        f[0][j] += b[(j >> 1) & 1];
+                        f[1][j] += b[2 + ((j >> 1) & 1)];
+                    }
+                }
+                uint16_t* out = static_cast<uint16_t*>(p.out);
+                if (kGated) {
+                    if (p.z) {
+                        uint16_t* z = p.z + row * N + ch;
+                        put_fragments<2>(slot, 0, f[0]);
+                        put_fragments<2>(slot + kSlot / 2, 0, f[1]);
+                        write_rows<2>(slot, z, N, tokens, 16);
+                        write_rows<2>(slot + kSlot / 2, z + g.channels, N, tokens, 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[0][j] = swiglu(f[0][j], f[1][j]);
+                    if (p.residual) {
+                        const uint16_t* res = static_cast<const uint16_t*>(p.residual) + row * g.channels + ch;
+                        read_rows<2>(slot + 3 * kSlot / 2, res, g.channels, tokens, 16);
+                        get_fragments<2>(slot + 3 * kSlot / 2, 0, f[1]);
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[0][j] += f[1][j];
+                    }
+                    put_fragments<2>(slot + kSlot, 0, f[0]);
+                    write_rows<2>(slot + kSlot, out + row * g.channels + ch, g.channels, tokens, 16);
+                } else if (KIND == kInput && SWIGLU) {
+                    const uint16_t* z = p.z + row * 2 * K + ch;
+                    read_rows<4>(slot, z, 2 * K, tokens, chans);
+                    read_rows<4>(slot + kSlot, z + K, 2 * K, tokens, chans);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float gate[16], up[16];
+                        get_fragments<4>(slot, h, gate);
+                        get_fragments<4>(slot + kSlot, h, up);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) swiglu_back(gate[j], up[j], f[h][j], gate[j], up[j]);
+                        // a lane's fragments of one half are its own to overwrite once all lanes have read theirs
+                        __syncwarp();
+                        put_fragments<4>(slot, h, gate);
+                        put_fragments<4>(slot + kSlot, h, up);
+                    }
+                    uint16_t* dz = out + row * 2 * K + ch;
+                    write_rows<4>(slot, dz, 2 * K, tokens, chans);
+                    write_rows<4>(slot + kSlot, dz + K, 2 * K, tokens, chans);
+                } else {
+                    const int64_t at = row * g.channels + ch;
+                    if (KIND == kForward) {
+                        if (p.z) {
+                            put_fragments<4>(slot, 0, f[0]);
+                            put_fragments<4>(slot, 1, f[1]);
+                            write_rows<4>(slot, p.z + at, g.channels, tokens, chans);
+                        }
+                        activate16(f[0], p.activation);
+                        activate16(f[1], p.activation);
+                        if (p.residual) {
+                            read_rows<4>(slot + kSlot, static_cast<const uint16_t*>(p.residual) + at, g.channels,
+                                         tokens, chans);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float r[16];
+                                get_fragments<4>(slot + kSlot, h, r);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) f[h][j] += r[j];
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    put_fragments<4>(slot, 0, f[0]);
+                    put_fragments<4>(slot, 1, f[1]);
+                    write_rows<4>(slot, out + at, g.channels, tokens, chans);
+                }
+            }
+            ++done;
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (tid == 0 && sh.gave_up && p.status) atomicOr(p.status, EP_FLAG_TIMEOUT);
+    __syncwarp();
+    cluster_sync();  // no copy, arrival or MMA of the other block reaches this one any more
+    if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream) {
     const bool swiglu = p.activation == EP_ACT_SWIGLU;
-    const int64_t nn = kind == kForward ? (swiglu ? p.N / 2 : p.N) : p.K;
-    const int64_t mm = kind == kWeight ? p.N : p.rows;
-    const int64_t tiles = (mm + kTile - 1) / kTile;
-    const dim3 grid((unsigned)((nn + kTile - 1) / kTile), (unsigned)(tiles < 64 ? tiles : 64), (unsigned)p.E);
-    auto kernel = kind == kForward ? (swiglu ? product_kernel<kForward, true> : product_kernel<kForward, false>)
-                  : kind == kInput ? (swiglu ? product_kernel<kInput, true> : product_kernel<kInput, false>)
-                                   : product_kernel<kWeight, false>;
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, p);
+    const int most = kind == kWeight && p.K <= 128 ? 128 : kTileN;
+    Maps maps;
+    const uint64_t N = (uint64_t)p.N, K = (uint64_t)p.K, E = (uint64_t)p.E, rows = (uint64_t)p.rows;
+    cudaError_t err = cudaSuccess;
+    if (kind == kWeight) {
+        // no rows at all: nothing is loaded, and any address will do
+        const void* dy = rows ? static_cast<const void*>(p.a) : p.out;
+        const void* x = rows ? static_cast<const void*>(p.b) : p.out;
+        const uint32_t box[2] = {64, 64};
+        const uint64_t da[2] = {N, rows ? rows : 1}, sa[1] = {N * 2};
+        const uint64_t db[2] = {K, rows ? rows : 1}, sb[1] = {K * 2};
+        err = bf16_map(&maps.a, dy, 2, da, sa, box);
+        if (err == cudaSuccess) err = bf16_map(&maps.b64, x, 2, db, sb, box);
+        maps.b16 = maps.b64;
+    } else {
+        if (kind == kForward && swiglu) {
+            const uint64_t I = N / 2;
+            const uint64_t d[5] = {K, 16, 2, I / 16, E}, s[4] = {K * 2, I * K * 2, 16 * K * 2, N * K * 2};
+            const uint32_t box[5] = {64, 16, 2, 4, 1};
+            err = bf16_map(&maps.a, p.b, 5, d, s, box);
+        } else {
+            const uint64_t d[3] = {K, N, E}, s[2] = {K * 2, N * K * 2};
+            const uint32_t box[3] = {64, kind == kForward ? 128u : 64u, 1};
+            err = bf16_map(&maps.a, p.b, 3, d, s, box);
+        }
+        const uint64_t width = kind == kForward ? K : N;
+        const uint64_t d[2] = {width, rows}, s[1] = {width * 2};
+        const uint32_t box64[2] = {64, 64}, box16[2] = {64, 16};
+        if (err == cudaSuccess) err = bf16_map(&maps.b64, p.a, 2, d, s, box64);
+        if (err == cudaSuccess) err = bf16_map(&maps.b16, p.a, 2, d, s, box16);
+    }
+    if (err != cudaSuccess) return err;
+    static std::atomic<int> sm_cache[64];
+    const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    static std::atomic<uint64_t> configured[5];
+    const int which = kind == kForward ? swiglu : kind == kInput ? 2 + swiglu : 4;
+    auto kernel = which == 0   ? product_kernel<kForward, false>
+                  : which == 1 ? product_kernel<kForward, true>
+                  : which == 2 ? product_kernel<kInput, false>
+                  : which == 3 ? product_kernel<kInput, true>
+                               : product_kernel<kWeight, false>;
+    err = raise_smem_limit(kernel, kSmem, configured[which]);
+    if (err != cudaSuccess) return err;
+    const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmem, stream, maps, p, most);
 }
 
 }  // namespace ep
