@@ -2,61 +2,135 @@
 //     dz[m, n]  = dy[m, n] * act'(z[m, n])        (SwiGLU: both halves)
 //     dbias[n]  = sum_m dz[m, n], of the unrounded values
 //
-// One block per 64 columns walks all rows, its warps every 8th; their sums meet
-// in shared memory in a fixed order.
+// Bound by the bytes of dy, z and dz.  A cluster of eight blocks owns a strip of
+// columns: a thread has 8 of them (one 16-byte vector) of every so many rows and
+// keeps their sums in registers; the block's rows meet in shared memory and
+// the blocks' sums in the first block's, all in a fixed order, so that no
+// workspace, second launch or atomic is needed.  A strip is 64 columns wide, or
+// narrower (down to the 16 of a 32-byte sector) where N has too few strips to
+// fill the SMs.
 #include "ep_products.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256, kCluster = 8;
+constexpr int kUnroll = 4;  // rows of a thread whose loads are issued together
 
-__global__ void __launch_bounds__(kWarps * 32)
+template <int ACT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M,
-                    int64_t N, int activation, uint16_t* __restrict__ dz,
-                    float* __restrict__ dbias) {
-    __shared__ float sums[kWarps][2][32];
+                    int64_t N, int vecs, uint16_t* __restrict__ dz, float* __restrict__ dbias) {
+    constexpr bool kGated = ACT == EP_ACT_SWIGLU;
+    constexpr int H = kGated ? 2 : 1;
+    __shared__ float sums[kThreads][H * 8 + 1];
+    __shared__ float total[8 * 8 * H];  // of the strip's columns
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = (int64_t)blockIdx.x * 32 + lane;
-    float sg = 0.0f, su = 0.0f;
+    const int rank = (int)cluster_rank();
+    const int col = threadIdx.x % vecs, lane_row = threadIdx.x / vecs;
+    const int per = kThreads / vecs;  // rows of a block's step
+    const int64_t n = ((int64_t)(blockIdx.x / kCluster) * vecs + col) * 8;
+    const int64_t wide = H * N;
+    float sum[H * 8];
+#pragma unroll
+    for (int i = 0; i < H * 8; ++i) sum[i] = 0.0f;
     if (n < N) {
-        for (int64_t m = warp; m < M; m += kWarps) {
-            const float d = bf16_value(dy[m * N + n]);
-            if (activation == EP_ACT_SWIGLU) {
-                float dg, du;
-                swiglu_back(bf16_value(z[m * 2 * N + n]), bf16_value(z[m * 2 * N + N + n]), d, dg, du);
-                dz[m * 2 * N + n] = bf16_bits(dg);
-                dz[m * 2 * N + N + n] = bf16_bits(du);
-                sg += dg;
-                su += du;
-            } else {
-                const float v = activation == EP_ACT_NONE ? d : activate_back(bf16_value(z[m * N + n]), d, activation);
-                if (dz) dz[m * N + n] = bf16_bits(v);
-                sg += v;
+        const int64_t step = (int64_t)kCluster * per;
+        for (int64_t m0 = (int64_t)rank * per + lane_row; m0 < M; m0 += kUnroll * step) {
+            uint4 d[kUnroll], q[kUnroll][H];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t m = m0 + u * step;
+                if (m < M) {
+                    d[u] = ld_stream_v4(dy + m * N + n);
+                    if (ACT != EP_ACT_NONE) {
+#pragma unroll
+                        for (int h = 0; h < H; ++h) q[u][h] = ld_stream_v4(z + m * wide + h * N + n);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t m = m0 + u * step;
+                if (m >= M) break;
+                const uint32_t dd[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+                float g[H][8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float v = i & 1 ? bf16hi_to_f32(dd[i / 2]) : bf16lo_to_f32(dd[i / 2]);
+                    if constexpr (ACT == EP_ACT_NONE) {
+                        g[0][i] = v;
+                    } else {
+                        float x[H];
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t w[4] = {q[u][h].x, q[u][h].y, q[u][h].z, q[u][h].w};
+                            x[h] = i & 1 ? bf16hi_to_f32(w[i / 2]) : bf16lo_to_f32(w[i / 2]);
+                        }
+                        if constexpr (kGated)
+                            swiglu_back(x[0], x[H - 1], v, g[0][i], g[H - 1][i]);
+                        else
+                            g[0][i] = activate_back(x[0], v, ACT);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (ACT != EP_ACT_NONE)
+                        st_v4(dz + m * wide + h * N + n,
+                              make_uint4(pack_bf16x2_rn(g[h][0], g[h][1]), pack_bf16x2_rn(g[h][2], g[h][3]),
+                                         pack_bf16x2_rn(g[h][4], g[h][5]), pack_bf16x2_rn(g[h][6], g[h][7])));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[h * 8 + i] += g[h][i];
+                }
             }
         }
     }
-    sums[warp][0][lane] = sg;
-    sums[warp][1][lane] = su;
+    if (dbias == nullptr) return;  // for all blocks
+#pragma unroll
+    for (int i = 0; i < H * 8; ++i) sums[threadIdx.x][i] = sum[i];
     __syncthreads();
-    if (warp == 0 && n < N && dbias) {
-        for (int w = 1; w < kWarps; ++w) {
-            sg += sums[w][0][lane];
-            su += sums[w][1][lane];
-        }
-        dbias[n] = sg;
-        if (activation == EP_ACT_SWIGLU) dbias[N + n] = su;
+    for (int i = threadIdx.x; i < vecs * H * 8; i += kThreads) {
+        float s = 0.0f;
+        for (int r = 0; r < per; ++r) s += sums[r * vecs + i / (H * 8)][i % (H * 8)];
+        total[i] = s;
     }
+    cluster_sync();
+    if (rank == 0) {
+        for (int i = threadIdx.x; i < vecs * H * 8; i += kThreads) {
+            float s = 0.0f;
+            for (int r = 0; r < kCluster; ++r) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(v)
+                             : "r"(cluster_addr(smem_addr(total + i), r))
+                             : "memory");
+                s += v;
+            }
+            const int64_t at = ((int64_t)(blockIdx.x / kCluster) * vecs + i / (H * 8)) * 8 + i % 8;
+            if (at < N) dbias[(i % (H * 8) / 8) * N + at] = s;
+        }
+    }
+    cluster_sync();  // the other blocks' sums stay until they are read
 }
 
 }  // namespace
 
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M, int64_t N,
                                 int activation, uint16_t* dz, float* dbias, cudaStream_t stream) {
-    return launch_pdl(act_backward_kernel, dim3((unsigned)((N + 31) / 32)), dim3(kWarps * 32), 0, stream, dy, z, M,
-                      N, activation, dz, dbias);
+    static std::atomic<int> sm_cache[64];
+    const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    const int64_t all = N / 8;
+    int vecs = 8;
+    while (vecs > 2 && (all + vecs - 1) / vecs * kCluster < 2 * sms) vecs /= 2;
+    auto kernel = activation == EP_ACT_NONE   ? act_backward_kernel<EP_ACT_NONE>
+                  : activation == EP_ACT_RELU ? act_backward_kernel<EP_ACT_RELU>
+                  : activation == EP_ACT_SILU ? act_backward_kernel<EP_ACT_SILU>
+                  : activation == EP_ACT_GELU ? act_backward_kernel<EP_ACT_GELU>
+                                              : act_backward_kernel<EP_ACT_SWIGLU>;
+    const unsigned grid = (unsigned)((all + vecs - 1) / vecs) * kCluster;
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, dy, z, M, N, vecs, dz, dbias);
 }
 
 }  // namespace ep

@@ -37,30 +37,35 @@ namespace ep {
 namespace {
 
 constexpr int kTileM = 256, kTileN = 256, kBlockK = 64;  // per pair
-constexpr int kStages = 6;
+constexpr int kMaxStages = 6;
 constexpr int kABytes = 128 * kBlockK * 2, kBBytes = 128 * kBlockK * 2;  // per block and stage
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kThreads = 256;
 constexpr int kEpiWarps = 4;
 constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels
-constexpr int kSlots = 2;        // per warp
+constexpr int kBox = 32 * 128;   // weight: 32 rows of 128 bytes
+// per warp: two slots (weight: two boxes, at the expense of a stage)
+__host__ __device__ constexpr int staging(bool weight) { return 2 * (weight ? kBox : kSlot); }
+__host__ __device__ constexpr int stage_count(bool weight) { return weight ? 5 : kMaxStages; }
 constexpr int kBand = 16;        // channel tiles that share the tokens while they are in L2
 
 struct Shared {
-    alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], acc_full[2], acc_empty[2], drain;
+    alignas(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int gave_up;
     int first[EP_MAX_EXPERTS], count[EP_MAX_EXPERTS];
     int tiles[EP_MAX_EXPERTS + 1];  // exclusive scan of the experts' token tiles
 };
 
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kSlots * kSlot + sizeof(Shared);
-static_assert(kSmem <= 227 * 1024, "");
+constexpr size_t smem_bytes(bool weight) {
+    return 1024 + stage_count(weight) * kStageBytes + kEpiWarps * staging(weight) + sizeof(Shared);
+}
+static_assert(smem_bytes(false) <= 227 * 1024 && smem_bytes(true) <= 227 * 1024, "");
 
 struct Maps {
-    CUtensorMap a;    // the 256-row side: weights; dy
-    CUtensorMap b64;  // the other: boxes of 64 tokens (weight: of 64 tokens x 64 channels of x)
-    CUtensorMap b16;  // boxes of 16 tokens
+    CUtensorMap a;     // the 256-row side: weights; dy
+    CUtensorMap b[8];  // the other: boxes of 16, 32, .. 128 tokens, one copy per stage and block
+                       // (weight: b[0] x, boxes of 64 tokens x 64 channels; b[1] dw, of 32 rows)
 };
 
 struct Tile {
@@ -121,9 +126,9 @@ struct Walk {
         const int count = sh.count[e];
         t.e = e;
         t.m0 = (int)(band * kBand + in % wide) * g.per;
-        t.width = (int)(((uint32_t)(count + tokens - 1) / tokens + 31) / 32 * 32);
-        t.row = sh.first[e] + (int)tt * t.width;
-        t.n = min(t.width, count - (int)tt * t.width);  // more than (tokens - 1) * most >= (tokens - 1) * width
+        t.row = sh.first[e] + (int)tt * g.most;
+        t.n = min(g.most, count - (int)tt * g.most);
+        t.width = (t.n + 31) / 32 * 32;
         t.n0 = 0;
         t.blocks = g.blocks;
         t.tail = 0;
@@ -132,6 +137,34 @@ struct Walk {
 };
 
 // ---- the epilogue's pieces ---------------------------------------------------
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// The addend of a box of 32 rows x 128 bytes: `rows` and `cols` exist, the
+// first of them at element `at`, rows ld apart.
+__device__ __forceinline__ void add_to_box(uint32_t box, const void* add, int size, int64_t at, int64_t ld, int rows,
+                                           int cols) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const uint8_t* base = static_cast<const uint8_t*>(add) + (at + piece * (16 / size)) * size;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (r < rows && piece * (16 / size) < cols)
+            st_shared_v4(box + r * 128 + ((piece ^ (r & 7)) << 4), *reinterpret_cast<const uint4*>(base + r * ld * size));
+    }
+    __syncwarp();
+}
 
 // A warp's 32 tokens x 32 channels (SwiGLU forward: 16) of bf16 in shared
 // memory, 16-byte pieces exchanged so that neither the fragments' nor the rows'
@@ -183,19 +216,10 @@ __device__ __forceinline__ void move_rows(uint32_t slot, uint16_t* at, int64_t l
         const uint32_t s = slot_at<PIECES>(slot, t, piece);
         if (t < tokens && piece * 8 < channels) {
             uint16_t* p = at + t * ld + piece * 8;
-            uint4 v;
-            if (LOAD) {
-                v = ld_stream_v4(p);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(s), "r"(v.x), "r"(v.y), "r"(v.z),
-                             "r"(v.w)
-                             : "memory");
-            } else {
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(s)
-                             : "memory");
-                st_v4(p, v);
-            }
+            if (LOAD)
+                st_shared_v4(s, *reinterpret_cast<const uint4*>(p));
+            else
+                st_v4(p, ld_shared_v4(s));
         }
     }
 }
@@ -236,8 +260,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     constexpr bool kGated = SWIGLU && KIND == kForward;  // two rows of weights per output channel
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    constexpr int kStages = stage_count(KIND == kWeight), kStaging = staging(KIND == kWeight);
     uint8_t* slots = stages + kStages * kStageBytes;
-    Shared& sh = *reinterpret_cast<Shared*>(slots + kEpiWarps * kSlots * kSlot);
+    Shared& sh = *reinterpret_cast<Shared*>(slots + kEpiWarps * kStaging);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty), tail = smem_addr(sh.tail);
@@ -248,8 +273,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     if (warp == 0) tmem_alloc_pair(smem_addr(&sh.tmem), 512);
     if (tid == 32) {
         tma_prefetch_map(&maps.a);
-        tma_prefetch_map(&maps.b64);
-        if (KIND != kWeight) tma_prefetch_map(&maps.b16);
+        tma_prefetch_map(&maps.b[KIND == kWeight ? 0 : most / 32 - 1]);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, KIND == kWeight ? 2 : 1);
             mbar_init(empty + 8 * i, 1);
@@ -342,7 +366,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         tma_pair_2d(a, &maps.a, m, r0, bar);
                         tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
                         const int n = t.n0 + rank * half;
-                        for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b64, n + j, r0, bar);
+                        for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b[0], n + j, r0, bar);
                     } else {
                         if (kGated) {
                             tma_pair_5d(a, &maps.a, k0, 0, 0, m / 16, t.e, bar);
@@ -352,9 +376,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             tma_pair_3d(a, &maps.a, m, k0, t.e, bar);
                             tma_pair_3d(a + kABytes / 2, &maps.a, m + 64, k0, t.e, bar);
                         }
-                        int j = 0;
-                        for (; j + 64 <= half; j += 64) tma_pair_2d(b + j * 128, &maps.b64, k0, brow + j, bar);
-                        for (; j < half; j += 16) tma_pair_2d(b + j * 128, &maps.b16, k0, brow + j, bar);
+                        tma_pair_2d(b, &maps.b[half / 16 - 1], k0, brow, bar);
                     }
                 }
                 __syncwarp();
@@ -389,7 +411,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     ok = false;
                     break;
                 }
-                if (KIND == kWeight) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                // the zeros behind a tail were written by threads of both blocks
+                if (KIND == kWeight && t.tail != 0 && kb == t.blocks - 1)
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 tc_fence_after();
                 const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
                 // 16 values of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
@@ -440,9 +464,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         // ---- output
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t slot = smem_addr(slots) + quarter * kSlots * kSlot;
+        const uint32_t slot = smem_addr(slots) + quarter * kStaging;
         const uint32_t bar0 = cluster_addr(acc_empty, 0);
-        uint32_t done = 0;
+        uint32_t done = 0, boxes = 0;
         Walk<KIND> walk;
         for (uint64_t i = pair; i < g.total; i += step) {
             const Tile t = walk.tile(sh, g, p.E, i);
@@ -458,57 +482,71 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
             };
             if (KIND == kWeight) {
-                // a lane is a row of dw
-                const int64_t n = t.m0 + (int64_t)rank * 128 + quarter * 32 + lane;
-                const int64_t at = ((int64_t)t.e * N + n) * K + t.n0;
-                const int cols = min(t.width, K - t.n0);  // a multiple of 8
-                for (int c = 0; c < t.width; c += 32) {
-                    uint32_t v[2][16];
-                    __syncwarp();
-                    if (t.blocks > 0) {
-                        tmem_load(v[0], src + c);
-                        tmem_load(v[1], src + c + 16);
-                        tmem_wait_for(v[0]);
-                        tmem_wait_for(v[1]);
-                        if (c + 32 >= t.width) release();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[0][j] = v[1][j] = 0;
+                // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
+                const bool f32 = p.out_type == EP_TYPE_F32;
+                const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
+                const int cols = min(t.width, K - t.n0);              // a multiple of 8
+                const int wide = f32 ? 32 : 64;                       // columns of a box
+                for (int c = 0; c < t.width; c += wide) {
+                    const uint32_t box = slot + (boxes & 1) * kBox;
+                    const bool write = n < N && c < cols;
+                    if (write) {
+                        if (lane == 0) tma_store_wait<1>();
+                        __syncwarp();
+                        if (p.add) add_to_box(box, p.add, f32 ? 4 : 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
                     }
-                    if (n >= N) continue;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // 8 columns at a time
-                        if (c + 8 * j >= cols) continue;
-                        float f[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) f[x] = __uint_as_float(v[j >> 1][(j & 1) * 8 + x]);
-                        const int64_t o = at + c + 8 * j;
-                        if (p.out_type == EP_TYPE_F32) {
-                            if (p.add) {
-                                const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.add) + o);
-                                const float4 lo = q[0], hi = q[1];
-                                f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-                                f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
-                            }
-                            uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
-                            st_v4(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                                __float_as_uint(f[3])));
-                            st_v4(q + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
-                                                    __float_as_uint(f[6]), __float_as_uint(f[7])));
+                    for (int h = 0; h < 4; ++h) {  // 16 columns of 64
+                        if (h * 16 >= wide) break;
+                        uint32_t v[16];
+                        if (t.blocks > 0) {
+                            __syncwarp();
+                            tmem_load(v, src + c + h * 16);
+                            tmem_wait_for(v);
+                            if (c + h * 16 + 16 >= t.width) release();
                         } else {
-                            if (p.add) {
-                                const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.add) + o);
-                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    f[2 * x] += bf16lo_to_f32(w[x]);
-                                    f[2 * x + 1] += bf16hi_to_f32(w[x]);
-                                }
-                            }
-                            st_v4(static_cast<uint16_t*>(p.out) + o,
-                                  make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]),
-                                             pack_bf16x2_rn(f[4], f[5]), pack_bf16x2_rn(f[6], f[7])));
+                            for (int j = 0; j < 16; ++j) v[j] = 0;
                         }
+                        if (!write) continue;
+                        float f[16];
+                        as_floats(v, f);
+                        if (f32) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t at = box + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4);
+                                if (p.add) {
+                                    const uint4 q = ld_shared_v4(at);
+                                    f[4 * j] += __uint_as_float(q.x), f[4 * j + 1] += __uint_as_float(q.y);
+                                    f[4 * j + 2] += __uint_as_float(q.z), f[4 * j + 3] += __uint_as_float(q.w);
+                                }
+                                st_shared_v4(at, make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]),
+                                                            __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3])));
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t at = box + lane * 128 + (((h * 2 + j) ^ (lane & 7)) << 4);
+                                float* q8 = f + 8 * j;
+                                if (p.add) {
+                                    const uint4 q = ld_shared_v4(at);
+                                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        q8[2 * x] += bf16lo_to_f32(w[x]);
+                                        q8[2 * x + 1] += bf16hi_to_f32(w[x]);
+                                    }
+                                }
+                                st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
+                                                            pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
+                            }
+                        }
+                    }
+                    if (write) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) tma_store_3d(&maps.b[1], t.n0 + c, n, t.e, box);
+                        ++boxes;
                     }
                 }
                 if (t.blocks > 0) ++done;
@@ -664,6 +702,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             }
             ++done;
         }
+        if (KIND == kWeight && lane == 0) tma_store_wait<0>();
     }
     __syncwarp();
     __syncthreads();
@@ -688,25 +727,30 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
         const uint32_t box[2] = {64, 64};
         const uint64_t da[2] = {N, rows ? rows : 1}, sa[1] = {N * 2};
         const uint64_t db[2] = {K, rows ? rows : 1}, sb[1] = {K * 2};
-        err = bf16_map(&maps.a, dy, 2, da, sa, box);
-        if (err == cudaSuccess) err = bf16_map(&maps.b64, x, 2, db, sb, box);
-        maps.b16 = maps.b64;
+        err = typed_map(&maps.a, EP_TYPE_BF16, dy, 2, da, sa, box);
+        if (err == cudaSuccess) err = typed_map(&maps.b[0], EP_TYPE_BF16, x, 2, db, sb, box);
+        const bool f32 = p.out_type == EP_TYPE_F32;
+        const uint64_t size = f32 ? 4 : 2;
+        const uint64_t dc[3] = {K, N, E}, sc[2] = {K * size, N * K * size};
+        const uint32_t cbox[3] = {f32 ? 32u : 64u, 32, 1};
+        if (err == cudaSuccess) err = typed_map(&maps.b[1], p.out_type, p.out, 3, dc, sc, cbox);
     } else {
         if (kind == kForward && swiglu) {
             const uint64_t I = N / 2;
             const uint64_t d[5] = {K, 16, 2, I / 16, E}, s[4] = {K * 2, I * K * 2, 16 * K * 2, N * K * 2};
             const uint32_t box[5] = {64, 16, 2, 4, 1};
-            err = bf16_map(&maps.a, p.b, 5, d, s, box);
+            err = typed_map(&maps.a, EP_TYPE_BF16, p.b, 5, d, s, box);
         } else {
             const uint64_t d[3] = {K, N, E}, s[2] = {K * 2, N * K * 2};
             const uint32_t box[3] = {64, kind == kForward ? 128u : 64u, 1};
-            err = bf16_map(&maps.a, p.b, 3, d, s, box);
+            err = typed_map(&maps.a, EP_TYPE_BF16, p.b, 3, d, s, box);
         }
         const uint64_t width = kind == kForward ? K : N;
         const uint64_t d[2] = {width, rows}, s[1] = {width * 2};
-        const uint32_t box64[2] = {64, 64}, box16[2] = {64, 16};
-        if (err == cudaSuccess) err = bf16_map(&maps.b64, p.a, 2, d, s, box64);
-        if (err == cudaSuccess) err = bf16_map(&maps.b16, p.a, 2, d, s, box16);
+        for (uint32_t j = 0; j < 8 && err == cudaSuccess; ++j) {
+            const uint32_t box[2] = {64, 16 * (j + 1)};
+            err = typed_map(&maps.b[j], EP_TYPE_BF16, p.a, 2, d, s, box);
+        }
     }
     if (err != cudaSuccess) return err;
     static std::atomic<int> sm_cache[64];
@@ -718,10 +762,11 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
                   : which == 2 ? product_kernel<kInput, false>
                   : which == 3 ? product_kernel<kInput, true>
                                : product_kernel<kWeight, false>;
-    err = raise_smem_limit(kernel, kSmem, configured[which]);
+    const size_t smem = smem_bytes(kind == kWeight);
+    err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmem, stream, maps, p, most);
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, maps, p, most);
 }
 
 }  // namespace ep

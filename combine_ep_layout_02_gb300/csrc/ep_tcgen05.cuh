@@ -241,6 +241,22 @@ __device__ __forceinline__ void mbar_expect_tx_pair(uint32_t bar, uint32_t bytes
                  : "memory");
 }
 
+// A box from this block's shared memory to a 3-D map; what lies outside the
+// map is not written.  The thread's bulk groups say when it has been read.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                             uint32_t src) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int LEFT>  // all but the last LEFT groups have been read
+__device__ __forceinline__ void tma_store_wait() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+
 // Instruction descriptor of kind::f16: bf16 x bf16 -> fp32; `a_mn`, `b_mn`: the
 // operand's rows, not the summed index, are contiguous in memory.
 __host__ __device__ constexpr uint32_t bf16_instr_desc(int m, int n, bool a_mn, bool b_mn) {
@@ -343,10 +359,10 @@ cudaError_t byte_matrix_map(CUtensorMap* map, const void* base, int64_t rows, in
 cudaError_t byte_blocks_map(CUtensorMap* map, const void* base, int64_t rows, int64_t width,
                             int box_rows, int blocks);
 
-// Map of bf16 values with up to five dimensions, innermost first; `strides` in
-// bytes from the second dimension on, boxes 64 values wide with the 128-byte
-// swizzle.  What lies outside reads 0.
-cudaError_t bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box);
+// Map of bf16 or fp32 values (EP_TYPE_*) with up to five dimensions, innermost
+// first; `strides` in bytes from the second dimension on, boxes 128 bytes wide
+// with the 128-byte swizzle.  What lies outside reads 0 and is not written.
+cudaError_t typed_map(CUtensorMap* map, int type, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box);
 
 }  // namespace ep

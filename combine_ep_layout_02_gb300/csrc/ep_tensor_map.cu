@@ -58,8 +58,8 @@ cudaError_t byte_blocks_map(CUtensorMap* map, const void* base, int64_t rows, in
     return encode(map, base, 3, dims, strides, box);
 }
 
-cudaError_t bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box) {
+cudaError_t typed_map(CUtensorMap* map, int type, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
     cuuint64_t d[5], s[4];
     cuuint32_t b[5];
     for (int i = 0; i < rank; ++i) {
@@ -67,7 +67,8 @@ cudaError_t bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_
         b[i] = box[i];
         if (i > 0) s[i - 1] = strides[i - 1];
     }
-    return encode(map, base, rank, d, s, b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    return encode(map, base, rank, d, s, b,
+                  type == EP_TYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 }  // namespace ep
