@@ -40,12 +40,13 @@ constexpr int kTileM = 256, kTileN = 256, kBlockK = 64;  // per pair
 constexpr int kMaxStages = 6;
 constexpr int kABytes = 128 * kBlockK * 2, kBBytes = 128 * kBlockK * 2;  // per block and stage
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kThreads = 256;
-constexpr int kEpiWarps = 4;
+// warps that write the output (weight: two column shares of four)
+__host__ __device__ constexpr int epi_warps(bool weight) { return weight ? 8 : 4; }
+__host__ __device__ constexpr int threads_of(bool weight) { return 128 + 32 * epi_warps(weight); }
 constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels
 constexpr int kBox = 32 * 128;   // weight: 32 rows of 128 bytes
-// per warp: two slots (weight: two boxes, at the expense of a stage)
-__host__ __device__ constexpr int staging(bool weight) { return 2 * (weight ? kBox : kSlot); }
+// per warp: two slots (weight: a box, at the expense of a stage)
+__host__ __device__ constexpr int staging(bool weight) { return weight ? kBox : 2 * kSlot; }
 __host__ __device__ constexpr int stage_count(bool weight) { return weight ? 5 : kMaxStages; }
 constexpr int kBand = 16;        // channel tiles that share the tokens while they are in L2
 
@@ -58,7 +59,7 @@ struct Shared {
 };
 
 constexpr size_t smem_bytes(bool weight) {
-    return 1024 + stage_count(weight) * kStageBytes + kEpiWarps * staging(weight) + sizeof(Shared);
+    return 1024 + stage_count(weight) * kStageBytes + epi_warps(weight) * staging(weight) + sizeof(Shared);
 }
 static_assert(smem_bytes(false) <= 227 * 1024 && smem_bytes(true) <= 227 * 1024, "");
 
@@ -255,12 +256,13 @@ __device__ __forceinline__ void activate16(float (&f)[16], int act) {
 }
 
 template <ProductKind KIND, bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND == kWeight), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p, int most) {
     constexpr bool kGated = SWIGLU && KIND == kForward;  // two rows of weights per output channel
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     constexpr int kStages = stage_count(KIND == kWeight), kStaging = staging(KIND == kWeight);
+    constexpr int kEpiWarps = epi_warps(KIND == kWeight), kThreads = threads_of(KIND == kWeight);
     uint8_t* slots = stages + kStages * kStageBytes;
     Shared& sh = *reinterpret_cast<Shared*>(slots + kEpiWarps * kStaging);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -411,9 +413,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     ok = false;
                     break;
                 }
-                // the zeros behind a tail were written by threads of both blocks
-                if (KIND == kWeight && t.tail != 0 && kb == t.blocks - 1)
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 tc_fence_after();
                 const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
                 // 16 values of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
@@ -421,10 +420,13 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const uint64_t db = KIND != kWeight ? operand_desc(b) : operand_desc_mn(b, 64 * 128);
                 constexpr uint64_t sa = (KIND == kForward ? 32 : 16 * 128) >> 4;
                 constexpr uint64_t sb = (KIND != kWeight ? 32 : 16 * 128) >> 4;
+                // of a tail the 16 values that hold its last row are the last
+                const int steps = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1 ? (t.tail + 15) / 16 : kBlockK / 16;
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < kBlockK / 16; ++j)
-                        mma_pair_bf16(d, da + j * sa, db + j * sb, instr, kb > 0 || j > 0);
+                        if (KIND != kWeight || j < steps)
+                            mma_pair_bf16(d, da + j * sa, db + j * sb, instr, kb > 0 || j > 0);
                     mma_commit_pair(empty + 8 * s);
                     if (kb == t.blocks - 1) mma_commit_pair(acc_full + 8 * buf);
                 }
@@ -453,20 +455,23 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             phases ^= 1u << s;
             uint8_t* a = stages + s * kStageBytes;
             const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
-            for (int q = t.tail * 8 + lane; q < 64 * 8; q += 32)
+            const int end = (t.tail + 15) / 16 * 16 * 8;  // the MMAs stop there
+            for (int q = t.tail * 8 + lane; q < end; q += 32)
                 for (int j = 0; j < boxes; ++j)
                     reinterpret_cast<uint4*>(a + j * 8192)[q] = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(bar0 + 8 * s);
+            // the zeros are in this block's shared memory, where its tensor core
+            // reads them: a release at cluster scope took 2,000 cycles per tail
+            if (lane == 0) mbar_arrive_pair(bar0 + 8 * s);
         }
     } else if (warp >= 4) {
         // ---- output
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t slot = smem_addr(slots) + quarter * kStaging;
+        const uint32_t slot = smem_addr(slots) + (warp - 4) * kStaging;
         const uint32_t bar0 = cluster_addr(acc_empty, 0);
-        uint32_t done = 0, boxes = 0;
+        uint32_t done = 0;
         Walk<KIND> walk;
         for (uint64_t i = pair; i < g.total; i += step) {
             const Tile t = walk.tile(sh, g, p.E, i);
@@ -487,11 +492,12 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
                 const int cols = min(t.width, K - t.n0);              // a multiple of 8
                 const int wide = f32 ? 32 : 64;                       // columns of a box
-                for (int c = 0; c < t.width; c += wide) {
-                    const uint32_t box = slot + (boxes & 1) * kBox;
+                const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
+                for (int c = end - share; c < end; c += wide) {
+                    const uint32_t box = slot;
                     const bool write = n < N && c < cols;
                     if (write) {
-                        if (lane == 0) tma_store_wait<1>();
+                        if (lane == 0) tma_store_wait<0>();
                         __syncwarp();
                         if (p.add) add_to_box(box, p.add, f32 ? 4 : 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
                     }
@@ -503,7 +509,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                             __syncwarp();
                             tmem_load(v, src + c + h * 16);
                             tmem_wait_for(v);
-                            if (c + h * 16 + 16 >= t.width) release();
+                            if (c + h * 16 + 16 >= end) release();
                         } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[j] = 0;
@@ -546,7 +552,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) tma_store_3d(&maps.b[1], t.n0 + c, n, t.e, box);
-                        ++boxes;
                     }
                 }
                 if (t.blocks > 0) ++done;
@@ -766,7 +771,8 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, maps, p, most);
+    return launch_pdl(kernel, dim3(grid), dim3(threads_of(kind == kWeight)), smem, stream, maps, p,
+                      most);
 }
 
 }  // namespace ep
