@@ -127,9 +127,12 @@ struct Walk {
         const int count = sh.count[e];
         t.e = e;
         t.m0 = (int)(band * kBand + in % wide) * g.per;
-        t.row = sh.first[e] + (int)tt * g.most;
-        t.n = min(g.most, count - (int)tt * g.most);
-        t.width = (t.n + 31) / 32 * 32;
+        // the tokens in units of 32, split as evenly as they go: two widths that differ by a unit
+        const uint32_t units = (uint32_t)(count + 31) / 32, base = units / tokens, more = units - base * tokens;
+        const int before = (int)(tt * base + min(tt, more)) * 32;
+        t.row = sh.first[e] + before;
+        t.width = (int)(base + (tt < more)) * 32;
+        t.n = min(t.width, count - before);
         t.n0 = 0;
         t.blocks = g.blocks;
         t.tail = 0;
