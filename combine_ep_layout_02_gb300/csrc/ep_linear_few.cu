@@ -1,0 +1,237 @@
+// ep_linear_few.cu -- the dense layer for a few tokens: y[m, n] = sum_k x[m, k]
+// w[n, k], where the weights' bytes set the time.
+//
+// A block has 16 or 32 rows of weights; its eight warps, and where there are few
+// rows the blocks of a cluster, split the summed index.  A warp multiplies the
+// rows as the 16-row operand of mma.m16n8k16 with the tokens as its columns.
+// The order of the summed index inside a product is free as long as both
+// operands share it: a lane's operand values are taken from 8 neighbouring ones
+// (16 bytes) of a row, so that every load is a whole vector and no shared memory
+// or shuffle stands between memory and the product.  The warps' sums meet in
+// shared memory and the blocks' over the cluster, in a fixed order.
+//
+// With SwiGLU rows g and g + 8 of a product are gate and up of one channel.
+#include "ep_products.cuh"
+#include "ep_tcgen05.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kChunk = 32;  // of the summed index: two products
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to 8 * NT tokens, RT * 16 rows of weights per block at most: `per` output
+// channels.
+template <int NT, int RT, bool GATED, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, RT == 1 && !AHEAD ? 3 : 2)
+linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
+    constexpr int kRows = RT * 16, kTokens = NT * 8;
+    constexpr int kUnroll = RT == 1 ? 4 : 2;
+    __shared__ float part[kWarps][kTokens][kRows + 1];
+    __shared__ float total[kTokens][kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+    const int64_t group = blockIdx.x / cluster;
+    const int M = (int)p.rows;
+    const int64_t K = p.K, channels = GATED ? p.N / 2 : p.N;
+    const int64_t n0 = group * per;  // first output channel
+    const uint16_t* w[RT][2];
+    bool live[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = GATED ? r * 8 + g : r * 16 + h * 8 + g;
+            const int64_t n = n0 + c;
+            live[r][h] = c < per && n < channels;
+            w[r][h] = p.b + ((GATED && h ? channels : 0) + n) * K + 8 * t;
+        }
+    const uint16_t* x[NT];
+    bool token[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        token[j] = j * 8 + g < M;
+        x[j] = p.a + (int64_t)(j * 8 + g) * K + 8 * t;
+    }
+    const int chunks = (int)((K + kChunk - 1) / kChunk), slices = cluster * kWarps;
+    const int share = (chunks + slices - 1) / slices;
+    const int c0 = min(chunks, (rank * kWarps + warp) * share), c1 = min(chunks, c0 + share);
+    // The weights are asked for from L2 while the preceding kernel ends; nothing
+    // is read before the wait.
+    if (c0 < c1 && t < 2 * RT) {
+        const int64_t first = (int64_t)c0 * kChunk, left = K - first, share_k = (int64_t)(c1 - c0) * kChunk;
+        const uint32_t bytes = (uint32_t)(left < share_k ? left : share_k) * 2;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (t == 2 * r + h && live[r][h])
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w[r][h] - 8 * t + first), "r"(bytes)
+                                 : "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
+    float acc[RT][NT][4] = {};
+    struct Operands {
+        uint4 a[kUnroll][RT][2], b[kUnroll][NT];
+    };
+    auto load = [&](Operands& o, int c) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t k = (int64_t)(c + u) * kChunk;
+            const bool in = c + u < c1 && k + 8 * t < K;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    o.a[u][r][h] = in && live[r][h] ? ld_stream_v4(w[r][h] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                o.b[u][j] = in && token[j] ? __ldg(reinterpret_cast<const uint4*>(x[j] + k)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto multiply = [&](const Operands& o) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint4 &lo = o.a[u][r][0], &hi = o.a[u][r][1], &v = o.b[u][j];
+                    mma_bf16(acc[r][j], lo.x, hi.x, lo.y, hi.y, v.x, v.y);
+                    mma_bf16(acc[r][j], lo.z, hi.z, lo.w, hi.w, v.z, v.w);
+                }
+    };
+    if (AHEAD) {  // the next step's operands are on their way while one is multiplied
+        Operands even, odd;
+        load(even, c0);
+        for (int c = c0; c < c1; c += 2 * kUnroll) {
+            load(odd, c + kUnroll);
+            multiply(even);
+            load(even, c + 2 * kUnroll);
+            multiply(odd);
+        }
+    } else {
+        for (int c = c0; c < c1; c += kUnroll) {
+            Operands o;
+            load(o, c);
+            multiply(o);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[warp][j * 8 + 2 * t + (i & 1)][r * 16 + g + (i >> 1) * 8] = acc[r][j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * kTokens; i += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) s += part[k][i / kRows][i % kRows];
+        total[i / kRows][i % kRows] = s;
+    }
+    if (cluster > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    // the blocks take the tokens in turn
+    auto sum = [&](int m, int row) {
+        if (cluster == 1) return total[m][row];
+        float s = 0.0f;
+        for (int r = 0; r < cluster; ++r) {
+            float v;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(v)
+                         : "r"(cluster_addr(smem_addr(&total[m][row]), r))
+                         : "memory");
+            s += v;
+        }
+        return s;
+    };
+    constexpr int kOut = GATED ? RT * 8 : kRows;
+    for (int i = threadIdx.x; i < kOut * kTokens; i += kThreads) {
+        const int m = i / kOut, c = i % kOut;
+        const int64_t n = n0 + c;
+        if (m >= M || c >= per || n >= channels || m % cluster != rank) continue;
+        const int row = GATED ? (c >> 3) * 16 + (c & 7) : c;
+        float v = sum(m, row);
+        if (p.bias) v += load_typed(p.bias, p.bias_type, n);
+        if (GATED) {
+            float u = sum(m, row + 8);
+            if (p.bias) u += load_typed(p.bias, p.bias_type, channels + n);
+            if (p.z) {
+                p.z[(int64_t)m * p.N + n] = bf16_bits(v);
+                p.z[(int64_t)m * p.N + channels + n] = bf16_bits(u);
+            }
+            v = swiglu(v, u);
+        } else {
+            if (p.z) p.z[(int64_t)m * p.N + n] = bf16_bits(v);
+            v = activate(v, p.activation);
+        }
+        const int64_t at = (int64_t)m * channels + n;
+        if (p.out_type == EP_TYPE_F32) {
+            if (p.residual) v += static_cast<const float*>(p.residual)[at];
+            static_cast<float*>(p.out)[at] = v;
+        } else {
+            if (p.residual) v += bf16_value(static_cast<const uint16_t*>(p.residual)[at]);
+            static_cast<uint16_t*>(p.out)[at] = bf16_bits(v);
+        }
+    }
+    if (cluster > 1) cluster_sync();  // the other blocks' sums stay until they are read
+}
+
+template <int NT, int RT, bool AHEAD>
+cudaError_t launch(const ProductArgs& p, int sms, cudaStream_t stream) {
+    const bool gated = p.activation == EP_ACT_SWIGLU;
+    const int64_t channels = gated ? p.N / 2 : p.N, most = gated ? RT * 8 : RT * 16;
+    // As few rounds over the SMs as `most` channels per block allow, and then as
+    // many channels per block as the rounds need: equal shares.  Where one
+    // round is not full, clusters, while a warp's share of the summed index is
+    // four steps.
+    const int64_t rounds = (channels + most * sms - 1) / (most * sms);
+    const int64_t per = (channels + rounds * sms - 1) / (rounds * sms);
+    const int64_t blocks = (channels + (rounds > 1 ? per : most) - 1) / (rounds > 1 ? per : most);
+    int cluster = 1;
+    while (cluster < 8 && blocks * cluster <= sms && p.K >= kChunk * kWarps * cluster * 4) cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    auto kernel = gated ? linear_few_kernel<NT, RT, true, AHEAD> : linear_few_kernel<NT, RT, false, AHEAD>;
+    return cudaLaunchKernelEx(&cfg, kernel, p, cluster, (int)(rounds > 1 ? per : most));
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream) {
+    static std::atomic<int> sm_cache[64];
+    int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    if (sms < 1) sms = 1;
+    if (p.rows > 8) return launch<2, 2, false>(p, sms, stream);
+    // A warp with four steps or more of the summed index loads a step ahead (two
+    // blocks per SM): 4,096 rows of 7,168: 10.5 against 12.3 us; with less to do
+    // the third block per SM gives more (7,168 rows of 2,048: 5.8 against 8.3 us).
+    if (p.K < 4 * 4 * kChunk * kWarps) return launch<1, 1, false>(p, sms, stream);
+    return p.N <= 2 * 16 * (int64_t)sms ? launch<1, 1, true>(p, sms, stream) : launch<1, 2, true>(p, sms, stream);
+}
+
+}  // namespace ep

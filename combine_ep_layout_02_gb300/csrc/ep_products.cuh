@@ -89,6 +89,10 @@ __device__ __forceinline__ float load_typed(const void* p, int type, int64_t i) 
 
 cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream);
 
+// kForward of one expert for up to kLinearFew tokens
+constexpr int kLinearFew = 16;
+cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream);
+
 // dz (unless nullptr) and column sums of the unrounded dz (unless nullptr)
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M, int64_t N,
                                 int activation, uint16_t* dz, float* dbias, cudaStream_t stream);

@@ -1,6 +1,7 @@
 // ep_products_api.cu -- C entry points of the BF16 products, the dense layer
 // and the gradient of the combine: argument checks on the host, then the
 // launches.  Every check that can fail happens before anything is enqueued.
+#include <stdlib.h>
 #include "ep_products.cuh"
 
 namespace {
@@ -170,6 +171,7 @@ int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N, con
     p.out = out;
     p.out_type = out_type;
     p.z = static_cast<uint16_t*>(z);
+    if (M <= (getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : ep::kLinearFew)) return cuda_status(ep::launch_linear_few(p, as_stream(stream)));
     return cuda_status(ep::launch_product(p, ep::kForward, as_stream(stream)));
 }
 
