@@ -11,6 +11,9 @@
 // shared memory and the blocks' over the cluster, in a fixed order.
 //
 // With SwiGLU rows g and g + 8 of a product are gate and up of one channel.
+//
+// Below it: the epilogue of a product whose summed index the tcgen05 kernel split
+// into parts, a pass over the parts' fp32 sums.
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
 
@@ -220,6 +223,56 @@ cudaError_t launch(const ProductArgs& p, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, p, cluster, (int)(rounds > 1 ? per : most));
 }
 
+// A thread's four channels of a token.
+template <bool GATED>
+__global__ void __launch_bounds__(256)
+linear_finish_kernel(const __grid_constant__ ProductArgs p, const float* __restrict__ parts, int splits) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t channels = GATED ? p.N / 2 : p.N, vecs = channels / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.rows * vecs) return;
+    const int64_t m = i / vecs, n = (i - m * vecs) * 4;
+    constexpr int H = GATED ? 2 : 1;
+    float f[H][4];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const float4* src = reinterpret_cast<const float4*>(parts + m * p.N + h * channels + n);
+        const int64_t step = p.rows * p.N / 4;
+        float4 s = src[0];
+        for (int k = 1; k < splits; ++k) {
+            const float4 v = src[k * step];
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        f[h][0] = s.x, f[h][1] = s.y, f[h][2] = s.z, f[h][3] = s.w;
+        if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[h][j] += load_typed(p.bias, p.bias_type, h * channels + n + j);
+        }
+        if (p.z)
+            *reinterpret_cast<uint2*>(p.z + m * p.N + h * channels + n) =
+                make_uint2(pack_bf16x2_rn(f[h][0], f[h][1]), pack_bf16x2_rn(f[h][2], f[h][3]));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[0][j] = GATED ? swiglu(f[0][j], f[H - 1][j]) : activate(f[0][j], p.activation);
+    const int64_t at = m * channels + n;
+    if (p.out_type == EP_TYPE_F32) {
+        if (p.residual) {
+            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + at);
+            f[0][0] += r.x, f[0][1] += r.y, f[0][2] += r.z, f[0][3] += r.w;
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(f[0][0], f[0][1], f[0][2], f[0][3]);
+    } else {
+        if (p.residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) + at);
+            f[0][0] += bf16lo_to_f32(r.x), f[0][1] += bf16hi_to_f32(r.x);
+            f[0][2] += bf16lo_to_f32(r.y), f[0][3] += bf16hi_to_f32(r.y);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+            make_uint2(pack_bf16x2_rn(f[0][0], f[0][1]), pack_bf16x2_rn(f[0][2], f[0][3]));
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream) {
@@ -232,6 +285,13 @@ cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream) {
     // the third block per SM gives more (7,168 rows of 2,048: 5.8 against 8.3 us).
     if (p.K < 4 * 4 * kChunk * kWarps) return launch<1, 1, false>(p, sms, stream);
     return p.N <= 2 * 16 * (int64_t)sms ? launch<1, 1, true>(p, sms, stream) : launch<1, 2, true>(p, sms, stream);
+}
+
+cudaError_t launch_linear_finish(const ProductArgs& p, const float* parts, int splits, cudaStream_t stream) {
+    const bool gated = p.activation == EP_ACT_SWIGLU;
+    const int64_t threads = p.rows * (gated ? p.N / 2 : p.N) / 4;
+    auto kernel = gated ? linear_finish_kernel<true> : linear_finish_kernel<false>;
+    return launch_pdl(kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p, parts, splits);
 }
 
 }  // namespace ep

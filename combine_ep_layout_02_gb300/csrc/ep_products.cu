@@ -78,6 +78,8 @@ struct Tile {
     int n0;       // weight: first channel of x
     int blocks;   // of the summed index
     int tail;     // weight: rows of the last block that count, 0: all
+    int k0;       // first value of the summed index
+    int part;     // of the summed index
 };
 
 // Sizes of a call that every role derives its tiles from.
@@ -87,7 +89,8 @@ struct Grid {
     int mtiles;       // tiles of them
     int ntiles;       // weight: tiles of x's channels
     int most;         // columns of a tile at most
-    int blocks;       // of the summed index (not weight)
+    int blocks;       // of the summed index, per part (not weight)
+    int splits, last; // parts of it, and the last part's blocks
     uint64_t total;   // tiles
 };
 
@@ -109,8 +112,16 @@ struct Walk {
             t.tail = count % kBlockK;
             t.width = g.most;
             t.n = g.most;
+            t.k0 = t.part = 0;
             return t;
         }
+        t.part = 0;
+        if (KIND == kForward && g.splits > 1) {
+            t.part = (int)(i % (uint32_t)g.splits);
+            i /= (uint32_t)g.splits;
+        }
+        t.k0 = t.part * g.blocks * kBlockK;
+        t.blocks = t.part == g.splits - 1 ? g.last : g.blocks;
         const int lane = threadIdx.x & 31;
         const uint64_t at = i / (uint32_t)g.mtiles;  // the expert's share: mtiles for each of its token tiles
         unsigned past;
@@ -134,7 +145,6 @@ struct Walk {
         t.width = (int)(base + (tt < more)) * 32;
         t.n = min(t.width, count - before);
         t.n0 = 0;
-        t.blocks = g.blocks;
         t.tail = 0;
         return t;
     }
@@ -329,8 +339,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     g.mtiles = (g.channels + g.per - 1) / g.per;
     g.most = most;
     g.ntiles = KIND == kWeight ? (K + most - 1) / most : 1;
-    g.blocks = ((KIND == kInput ? N : K) + kBlockK - 1) / kBlockK;
-    g.total = KIND == kWeight ? (uint64_t)p.E * g.mtiles * g.ntiles : (uint64_t)sh.tiles[p.E] * g.mtiles;
+    const int blocks = ((KIND == kInput ? N : K) + kBlockK - 1) / kBlockK;
+    g.splits = KIND == kForward ? p.splits : 1;
+    g.blocks = (blocks + g.splits - 1) / g.splits;
+    g.last = blocks - (g.splits - 1) * g.blocks;
+    g.total = KIND == kWeight ? (uint64_t)p.E * g.mtiles * g.ntiles : (uint64_t)sh.tiles[p.E] * g.mtiles * g.splits;
     const uint32_t pair = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -365,7 +378,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     } else if (rank == 0) {
                         mbar_expect_tx(full + 8 * s, 2 * bytes);
                     }
-                    const int k0 = kb * kBlockK;
+                    const int k0 = t.k0 + kb * kBlockK;
                     if (KIND == kWeight) {
                         const int r0 = t.row + k0;
                         tma_pair_2d(a, &maps.a, m, r0, bar);
@@ -570,43 +583,45 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 continue;
             }
             if (KIND == kForward && !SWIGLU && p.out_type == EP_TYPE_F32) {
-                // a lane's channel for one token after the other: whole lines of fp32
-                const int n = ch + lane;
-                const bool live = n < g.channels;
-                const float b = p.bias && live ? load_typed(p.bias, p.bias_type, n) : 0.0f;
-                for (int c = 0; c < t.n; c += 16) {
-                    uint32_t v[16];
+                // 32 tokens of 32 channels turn in shared memory (a lane's channel in, four channels of a token
+                // out), so that a store is 16 bytes a lane: single words took 2.5 times as long
+                const int piece = lane & 7, n = ch + piece * 4;
+                const bool live = piece * 4 < chans;
+                float bias[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bias[j] = p.bias && live ? load_typed(p.bias, p.bias_type, n + j) : 0.0f;
+                float* out = static_cast<float*>(p.out) + (int64_t)t.part * p.rows * g.channels;
+                for (int c = 0; c < t.n; c += 32) {
+                    uint32_t v[2][16];
                     __syncwarp();
-                    tmem_load(v, src + c);
-                    tmem_wait_for(v);
-                    if (c + 16 >= t.n) release();
-                    float f[16];
-                    as_floats(v, f);
-                    const int64_t at = (int64_t)(t.row + c) * g.channels + n;
-                    const int tokens = min(16, t.n - c);
-                    if (p.bias) {
+                    tmem_load(v[0], src + c);
+                    tmem_load(v[1], src + c + 16);
+                    tmem_wait_for(v[0]);
+                    tmem_wait_for(v[1]);
+                    if (c + 32 >= t.n) release();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[j] += b;
-                    }
-                    if (p.z && live) {
+                    for (int j = 0; j < 32; ++j)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + j * 128 + lane * 4), "r"(v[j >> 4][j & 15])
+                                     : "memory");
+                    __syncwarp();
+                    for (int j = lane >> 3; j < min(32, t.n - c) && live; j += 4) {
+                        const uint4 q = ld_shared_v4(slot + j * 128 + piece * 16);
+                        float f[4] = {__uint_as_float(q.x) + bias[0], __uint_as_float(q.y) + bias[1],
+                                      __uint_as_float(q.z) + bias[2], __uint_as_float(q.w) + bias[3]};
+                        const int64_t at = (int64_t)(t.row + c + j) * g.channels + n;
+                        if (p.z)
+                            *reinterpret_cast<uint2*>(p.z + at) =
+                                make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
+                        if (p.activation != EP_ACT_NONE) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < tokens) p.z[at + (int64_t)j * g.channels] = bf16_bits(f[j]);
-                    }
-                    activate16(f, p.activation);
-                    if (live) {
-                        const float* res = static_cast<const float*>(p.residual);
-                        if (res) {
-                            float r[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) r[j] = j < tokens ? res[at + (int64_t)j * g.channels] : 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) f[j] += r[j];
+                            for (int x = 0; x < 4; ++x) f[x] = activate(f[x], p.activation);
                         }
-                        float* out = static_cast<float*>(p.out);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (j < tokens) out[at + (int64_t)j * g.channels] = f[j];
+                        if (p.residual) {
+                            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + at);
+                            f[0] += r.x, f[1] += r.y, f[2] += r.z, f[3] += r.w;
+                        }
+                        st_v4(out + at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                                   __float_as_uint(f[3])));
                     }
                 }
                 ++done;
@@ -722,9 +737,40 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 
 }  // namespace
 
+DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated) {
+    static std::atomic<int> sm_cache[64];
+    const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    const int64_t pairs = sms >= 2 ? sms / 2 : 1;
+    // Cycles of a stage for 32, 64, .. 256 columns, measured on a dense layer of
+    // 4,096 channels: the narrow ones wait for the weights from L2.
+    static const int stage[8] = {276, 285, 311, 330, 357, 421, 458, 512};
+    const int64_t blocks = (K + kBlockK - 1) / kBlockK;
+    DensePlan best = {kTileN, 1};
+    double least = 0.0;
+    for (int u = 8; u >= 1; --u) {
+        const int64_t tokens = (M + 32 * u - 1) / (32 * u);
+        for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= blocks); ++want) {
+            const int64_t per = (blocks + want - 1) / want, splits = (blocks + per - 1) / per;
+            if (splits != want) continue;
+            // parts are products with all rows of w alike, written and read again in fp32
+            const int64_t rows = gated ? 2 * channels : channels;
+            const int64_t mtiles = splits > 1 || !gated ? (rows + kTileM - 1) / kTileM
+                                                        : (channels + kTileM / 2 - 1) / (kTileM / 2);
+            const int64_t units = mtiles * tokens * splits, rounds = (units + pairs - 1) / pairs;
+            double cost = (double)rounds * (double)(per * stage[u - 1] + 400) + 2000.0 + 400.0 * u;
+            if (splits > 1) cost += 4000.0 + (double)(splits * M * rows) * 8.0 / 4000.0;
+            if (least == 0.0 || cost < least * 0.98) {
+                least = cost;
+                best = {32 * u, (int)splits};
+            }
+        }
+    }
+    return best;
+}
+
 cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream) {
     const bool swiglu = p.activation == EP_ACT_SWIGLU;
-    const int most = kind == kWeight && p.K <= 128 ? 128 : kTileN;
+    const int most = kind == kWeight && p.K <= 128 ? 128 : p.most ? p.most : kTileN;
     Maps maps;
     const uint64_t N = (uint64_t)p.N, K = (uint64_t)p.K, E = (uint64_t)p.E, rows = (uint64_t)p.rows;
     cudaError_t err = cudaSuccess;

@@ -33,7 +33,16 @@ struct ProductArgs {
     int out_type;
     uint16_t* z;          // kForward: pre-activations out or nullptr; kInput with SwiGLU: in
     uint32_t* status;
+    // kForward of one expert: columns of a tile at most (0: 256), and parts of the
+    // summed index, each with its own fp32 [rows, N] in `out`
+    int most, splits;
 };
+
+// How a dense product of more than kLinearFew tokens is cut.
+struct DensePlan {
+    int most, splits;
+};
+DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated);
 
 // Rows of expert e (of the whole buffer where there are no experts).
 __device__ __forceinline__ Segment product_segment(const ProductArgs& p, int e) {
@@ -92,6 +101,9 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
 // kForward of one expert for up to kLinearFew tokens
 constexpr int kLinearFew = 16;
 cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream);
+
+// the epilogue over the parts' sums [splits, rows, N]
+cudaError_t launch_linear_finish(const ProductArgs& p, const float* parts, int splits, cudaStream_t stream);
 
 // dz (unless nullptr) and column sums of the unrounded dz (unless nullptr)
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M, int64_t N,

@@ -1,7 +1,6 @@
 // ep_products_api.cu -- C entry points of the BF16 products, the dense layer
 // and the gradient of the combine: argument checks on the host, then the
 // launches.  Every check that can fail happens before anything is enqueued.
-#include <stdlib.h>
 #include "ep_products.cuh"
 
 namespace {
@@ -59,6 +58,7 @@ ep::ProductArgs group_args(const void* a, const void* b, int64_t rows, int64_t N
     p.capacity = capacity;
     p.out_type = EP_TYPE_BF16;
     p.status = status;
+    p.splits = 1;
     return p;
 }
 
@@ -144,8 +144,10 @@ int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int64_t N, 
 }
 
 size_t ep_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation) {
-    (void)M, (void)K, (void)N, (void)activation;
-    return 0;
+    if (M <= ep::kLinearFew || check_linear(M, K, N, activation) != EP_OK) return 0;
+    const int64_t wide = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    const int splits = ep::dense_plan(M, K, N, activation == EP_ACT_SWIGLU).splits;
+    return splits > 1 ? (size_t)splits * M * wide * 4 : 0;
 }
 
 int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N, const void* bias,
@@ -171,8 +173,20 @@ int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N, con
     p.out = out;
     p.out_type = out_type;
     p.z = static_cast<uint16_t*>(z);
-    if (M <= (getenv("EP_FEW") ? atoi(getenv("EP_FEW")) : ep::kLinearFew)) return cuda_status(ep::launch_linear_few(p, as_stream(stream)));
-    return cuda_status(ep::launch_product(p, ep::kForward, as_stream(stream)));
+    if (M <= ep::kLinearFew) return cuda_status(ep::launch_linear_few(p, as_stream(stream)));
+    const ep::DensePlan plan = ep::dense_plan(M, K, N, gated);
+    p.most = plan.most;
+    if (plan.splits == 1) return cuda_status(ep::launch_product(p, ep::kForward, as_stream(stream)));
+    // the parts' sums as they are, all rows of w alike, then everything that follows a sum
+    ep::ProductArgs part = group_args(x, w, M, p.N, K, 1, nullptr, nullptr, 0, 0, status);
+    part.most = plan.most;
+    part.splits = plan.splits;
+    part.out = workspace;
+    part.out_type = EP_TYPE_F32;
+    cudaError_t err = ep::launch_product(part, ep::kForward, as_stream(stream));
+    if (err == cudaSuccess)
+        err = ep::launch_linear_finish(p, static_cast<const float*>(workspace), plan.splits, as_stream(stream));
+    return cuda_status(err);
 }
 
 int ep_linear_backward(const void* dy, const void* x, const void* w, const void* z, int64_t M,
