@@ -2,9 +2,9 @@
 //     dz[m, n]  = dy[m, n] * act'(z[m, n])        (SwiGLU: both halves)
 //     dbias[n]  = sum_m dz[m, n], of the unrounded values
 //
-// Bound by the bytes of dy, z and dz.  A cluster of eight blocks owns a strip of
+// Bound by the bytes of dy, z and dz.  A cluster of up to eight blocks owns a strip of
 // columns: a thread has 8 of them (one 16-byte vector) of every so many rows and
-// keeps their sums in registers; the block's rows meet in shared memory and
+// keeps their sums in registers; the block's rows meet by shuffles and in shared memory and
 // the blocks' sums in the first block's, all in a fixed order, so that no
 // workspace, second launch or atomic is needed.  A strip is 64 columns wide, or
 // narrower (down to the 16 of a 32-byte sector) where N has too few strips to
@@ -15,29 +15,29 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256, kCluster = 8;
+constexpr int kThreads = 256, kMaxCluster = 8;
 constexpr int kUnroll = 4;  // rows of a thread whose loads are issued together
 
 template <int ACT>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int64_t M,
-                    int64_t N, int vecs, uint16_t* __restrict__ dz, float* __restrict__ dbias) {
+                    int64_t N, int vecs, int cluster, uint16_t* __restrict__ dz, float* __restrict__ dbias) {
     constexpr bool kGated = ACT == EP_ACT_SWIGLU;
     constexpr int H = kGated ? 2 : 1;
-    __shared__ float sums[kThreads][H * 8 + 1];
+    __shared__ float sums[kThreads / 32][8][H * 8];
     __shared__ float total[8 * 8 * H];  // of the strip's columns
     pdl_wait();
     pdl_trigger();
-    const int rank = (int)cluster_rank();
+    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int col = threadIdx.x % vecs, lane_row = threadIdx.x / vecs;
     const int per = kThreads / vecs;  // rows of a block's step
-    const int64_t n = ((int64_t)(blockIdx.x / kCluster) * vecs + col) * 8;
+    const int64_t n = ((int64_t)(blockIdx.x / cluster) * vecs + col) * 8;
     const int64_t wide = H * N;
     float sum[H * 8];
 #pragma unroll
     for (int i = 0; i < H * 8; ++i) sum[i] = 0.0f;
     if (n < N) {
-        const int64_t step = (int64_t)kCluster * per;
+        const int64_t step = (int64_t)cluster * per;
         for (int64_t m0 = (int64_t)rank * per + lane_row; m0 < M; m0 += kUnroll * step) {
             uint4 d[kUnroll], q[kUnroll][H];
 #pragma unroll
@@ -88,19 +88,27 @@ act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict_
         }
     }
     if (dbias == nullptr) return;  // for all blocks
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int o = vecs; o < 32; o *= 2) {
 #pragma unroll
-    for (int i = 0; i < H * 8; ++i) sums[threadIdx.x][i] = sum[i];
+        for (int i = 0; i < H * 8; ++i) sum[i] += __shfl_xor_sync(kFullMask, sum[i], o);
+    }
+    if (lane < vecs) {
+#pragma unroll
+        for (int i = 0; i < H * 8; ++i) sums[warp][lane][i] = sum[i];
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < vecs * H * 8; i += kThreads) {
         float s = 0.0f;
-        for (int r = 0; r < per; ++r) s += sums[r * vecs + i / (H * 8)][i % (H * 8)];
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) s += sums[w][i / (H * 8)][i % (H * 8)];
         total[i] = s;
     }
     cluster_sync();
     if (rank == 0) {
         for (int i = threadIdx.x; i < vecs * H * 8; i += kThreads) {
             float s = 0.0f;
-            for (int r = 0; r < kCluster; ++r) {
+            for (int r = 0; r < cluster; ++r) {
                 float v;
                 asm volatile("ld.shared::cluster.f32 %0, [%1];"
                              : "=f"(v)
@@ -108,7 +116,7 @@ act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict_
                              : "memory");
                 s += v;
             }
-            const int64_t at = ((int64_t)(blockIdx.x / kCluster) * vecs + i / (H * 8)) * 8 + i % 8;
+            const int64_t at = ((int64_t)(blockIdx.x / cluster) * vecs + i / (H * 8)) * 8 + i % 8;
             if (at < N) dbias[(i % (H * 8) / 8) * N + at] = s;
         }
     }
@@ -121,16 +129,35 @@ cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M
                                 int activation, uint16_t* dz, float* dbias, cudaStream_t stream) {
     static std::atomic<int> sm_cache[64];
     const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    // strips of 64 columns, clusters while every thread has four rows, and
+    // narrower strips while there are fewer blocks than SMs
     const int64_t all = N / 8;
     int vecs = 8;
-    while (vecs > 2 && (all + vecs - 1) / vecs * kCluster < 2 * sms) vecs /= 2;
+    auto blocks_of = [&](int v) {
+        const int64_t rows = 4 * (kThreads / v);
+        const int64_t c = M <= rows ? 1 : M <= 2 * rows ? 2 : M <= 4 * rows ? 4 : kMaxCluster;
+        return std::pair<int64_t, int>((all + v - 1) / v, (int)c);
+    };
+    while (vecs > 2 && blocks_of(vecs).first * blocks_of(vecs).second < sms) vecs /= 2;
+    const auto [strips, cluster] = blocks_of(vecs);
     auto kernel = activation == EP_ACT_NONE   ? act_backward_kernel<EP_ACT_NONE>
                   : activation == EP_ACT_RELU ? act_backward_kernel<EP_ACT_RELU>
                   : activation == EP_ACT_SILU ? act_backward_kernel<EP_ACT_SILU>
                   : activation == EP_ACT_GELU ? act_backward_kernel<EP_ACT_GELU>
                                               : act_backward_kernel<EP_ACT_SWIGLU>;
-    const unsigned grid = (unsigned)((all + vecs - 1) / vecs) * kCluster;
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, dy, z, M, N, vecs, dz, dbias);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(strips * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, dy, z, M, N, vecs, cluster, dz, dbias);
 }
 
 }  // namespace ep

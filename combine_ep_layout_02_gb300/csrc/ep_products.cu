@@ -219,35 +219,44 @@ __device__ __forceinline__ void get_fragments(uint32_t slot, int h, float (&v)[1
     }
 }
 
-// Rows of the slot to memory (or back): `tokens` of 32, the first `channels`
-// (a multiple of 8) of a token's channels, ld apart.
-template <int PIECES, bool LOAD>
-__device__ __forceinline__ void move_rows(uint32_t slot, uint16_t* at, int64_t ld, int tokens, int channels) {
-    const int lane = threadIdx.x & 31, piece = lane % PIECES;
+// 32 rows of PIECES * 16 bytes, of which `tokens` and `bytes` exist, `ld` bytes
+// apart in memory: a lane has one piece of every 32 / PIECES-th row.
+template <int PIECES>
+struct Rows {
+    uint4 v[PIECES];
+    static __device__ __forceinline__ int token(int i) { return i * (32 / PIECES) + (threadIdx.x & 31) / PIECES; }
+    static __device__ __forceinline__ int piece() { return (threadIdx.x & 31) % PIECES; }
+    __device__ __forceinline__ void load(const void* at, int64_t ld, int tokens, int bytes) {
+        const uint8_t* p = static_cast<const uint8_t*>(at) + piece() * 16;
 #pragma unroll
-    for (int t0 = 0; t0 < 32; t0 += 32 / PIECES) {
-        const int t = t0 + lane / PIECES;
-        const uint32_t s = slot_at<PIECES>(slot, t, piece);
-        if (t < tokens && piece * 8 < channels) {
-            uint16_t* p = at + t * ld + piece * 8;
-            if (LOAD)
-                st_shared_v4(s, *reinterpret_cast<const uint4*>(p));
-            else
-                st_v4(p, ld_shared_v4(s));
-        }
+        for (int i = 0; i < PIECES; ++i)
+            if (token(i) < tokens && piece() * 16 < bytes) v[i] = *reinterpret_cast<const uint4*>(p + token(i) * ld);
     }
-}
+    __device__ __forceinline__ void store(void* at, int64_t ld, int tokens, int bytes) const {
+        uint8_t* p = static_cast<uint8_t*>(at) + piece() * 16;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            if (token(i) < tokens && piece() * 16 < bytes) st_v4(p + token(i) * ld, v[i]);
+    }
+    __device__ __forceinline__ void put(uint32_t slot) const {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) st_shared_v4(slot_at<PIECES>(slot, token(i), piece()), v[i]);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void get(uint32_t slot) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) v[i] = ld_shared_v4(slot_at<PIECES>(slot, token(i), piece()));
+        __syncwarp();
+    }
+};
 
+// The slot's rows to memory.
 template <int PIECES>
 __device__ __forceinline__ void write_rows(uint32_t slot, uint16_t* at, int64_t ld, int tokens, int channels) {
-    __syncwarp();
-    move_rows<PIECES, false>(slot, at, ld, tokens, channels);
-    __syncwarp();
-}
-template <int PIECES>
-__device__ __forceinline__ void read_rows(uint32_t slot, const uint16_t* at, int64_t ld, int tokens, int channels) {
-    move_rows<PIECES, true>(slot, const_cast<uint16_t*>(at), ld, tokens, channels);
-    __syncwarp();
+    Rows<PIECES> r;
+    r.get(slot);
+    r.store(at, ld * 2, tokens, channels * 2);
 }
 
 __device__ __forceinline__ void as_floats(const uint32_t (&v)[16], float (&f)[16]) {
@@ -266,6 +275,11 @@ __device__ __forceinline__ void activate16(float (&f)[16], int act) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = activate(f[i], EP_ACT_GELU);
     }
+}
+
+__device__ __noinline__ void activate4(float (&f)[4], int act) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = activate(f[i], act);
 }
 
 template <ProductKind KIND, bool SWIGLU>
@@ -487,12 +501,35 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t slot = smem_addr(slots) + (warp - 4) * kStaging;
         const uint32_t bar0 = cluster_addr(acc_empty, 0);
+        const bool f32 = p.out_type == EP_TYPE_F32;
+        constexpr int kReads = KIND == kInput && SWIGLU ? 2 : 1, kReadPieces = kGated ? 2 : 4;
         uint32_t done = 0;
         Walk<KIND> walk;
         for (uint64_t i = pair; i < g.total; i += step) {
             const Tile t = walk.tile(sh, g, p.E, i);
             const uint32_t buf = done & 1;
             const uint32_t src = lanes + buf * kTileN;
+            // forward and input: lanes are channels, columns tokens
+            const int span = kGated ? 16 : 32;  // output channels of this warp
+            const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
+            const int chans = min(span, g.channels - ch);
+            // What the epilogue reads (a residual, or the pre-activations of gate and up) is asked for a chunk of 32
+            // tokens ahead, the first one before the sums are there.
+            Rows<kReadPieces> ahead[kReads];
+            auto ask = [&](int c) {
+                if (c >= t.n || chans <= 0) return;
+                const int tokens = min(32, t.n - c);
+                const int64_t row = t.row + c;
+                if (KIND == kInput && SWIGLU) {
+                    const uint16_t* z = p.z + row * 2 * K + ch;
+                    ahead[0].load(z, K * 4, tokens, chans * 2);
+                    ahead[kReads - 1].load(z + K, K * 4, tokens, chans * 2);
+                } else if (KIND == kForward && p.residual && !f32) {
+                    ahead[0].load(static_cast<const uint16_t*>(p.residual) + row * g.channels + ch,
+                                  (int64_t)g.channels * 2, tokens, chans * 2);
+                }
+            };
+            if (KIND != kWeight) ask(0);
             if (t.blocks > 0) {
                 if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) break;
                 tc_fence_after();
@@ -504,7 +541,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             };
             if (KIND == kWeight) {
                 // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
-                const bool f32 = p.out_type == EP_TYPE_F32;
                 const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
                 const int cols = min(t.width, K - t.n0);              // a multiple of 8
                 const int wide = f32 ? 32 : 64;                       // columns of a box
@@ -573,16 +609,12 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 if (t.blocks > 0) ++done;
                 continue;
             }
-            // lanes are channels, columns tokens
-            const int span = kGated ? 16 : 32;  // output channels of this warp
-            const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
-            const int chans = min(span, g.channels - ch);
             if (chans <= 0) {
                 release();
                 ++done;
                 continue;
             }
-            if (KIND == kForward && !SWIGLU && p.out_type == EP_TYPE_F32) {
+            if (KIND == kForward && !SWIGLU && f32) {
                 // 32 tokens of 32 channels turn in shared memory (a lane's channel in, four channels of a token
                 // out), so that a store is 16 bytes a lane: single words took 2.5 times as long
                 const int piece = lane & 7, n = ch + piece * 4;
@@ -603,26 +635,32 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     for (int j = 0; j < 32; ++j)
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + j * 128 + lane * 4), "r"(v[j >> 4][j & 15])
                                      : "memory");
+                    const int tokens = live ? min(32, t.n - c) : 0;
+                    const int64_t at = (int64_t)(t.row + c) * g.channels + ch;
+                    Rows<8> res;
+                    if (p.residual)
+                        res.load(static_cast<const float*>(p.residual) + at, (int64_t)g.channels * 4, tokens, 128);
                     __syncwarp();
-                    for (int j = lane >> 3; j < min(32, t.n - c) && live; j += 4) {
-                        const uint4 q = ld_shared_v4(slot + j * 128 + piece * 16);
+                    Rows<8> rows;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int token = Rows<8>::token(j);
+                        const uint4 q = ld_shared_v4(slot + token * 128 + piece * 16);
                         float f[4] = {__uint_as_float(q.x) + bias[0], __uint_as_float(q.y) + bias[1],
                                       __uint_as_float(q.z) + bias[2], __uint_as_float(q.w) + bias[3]};
-                        const int64_t at = (int64_t)(t.row + c + j) * g.channels + n;
-                        if (p.z)
-                            *reinterpret_cast<uint2*>(p.z + at) =
+                        if (p.z && token < tokens)
+                            *reinterpret_cast<uint2*>(p.z + at + (int64_t)token * g.channels + piece * 4) =
                                 make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
-                        if (p.activation != EP_ACT_NONE) {
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) f[x] = activate(f[x], p.activation);
-                        }
+                        if (p.activation != EP_ACT_NONE) activate4(f, p.activation);
                         if (p.residual) {
-                            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + at);
-                            f[0] += r.x, f[1] += r.y, f[2] += r.z, f[3] += r.w;
+                            const uint4 r = res.v[j];
+                            f[0] += __uint_as_float(r.x), f[1] += __uint_as_float(r.y);
+                            f[2] += __uint_as_float(r.z), f[3] += __uint_as_float(r.w);
                         }
-                        st_v4(out + at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                                   __float_as_uint(f[3])));
+                        rows.v[j] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                               __float_as_uint(f[3]));
                     }
+                    rows.store(out + at, (int64_t)g.channels * 4, tokens, 128);
                 }
                 ++done;
                 continue;
@@ -667,8 +705,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 #pragma unroll
                     for (int j = 0; j < 16; ++j) f[0][j] = swiglu(f[0][j], f[1][j]);
                     if (p.residual) {
-                        const uint16_t* res = static_cast<const uint16_t*>(p.residual) + row * g.channels + ch;
-                        read_rows<2>(slot + 3 * kSlot / 2, res, g.channels, tokens, 16);
+                        ahead[0].put(slot + 3 * kSlot / 2);
+                        ask(c + 32);
                         get_fragments<2>(slot + 3 * kSlot / 2, 0, f[1]);
                         __syncwarp();
 #pragma unroll
@@ -677,9 +715,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     put_fragments<2>(slot + kSlot, 0, f[0]);
                     write_rows<2>(slot + kSlot, out + row * g.channels + ch, g.channels, tokens, 16);
                 } else if (KIND == kInput && SWIGLU) {
-                    const uint16_t* z = p.z + row * 2 * K + ch;
-                    read_rows<4>(slot, z, 2 * K, tokens, chans);
-                    read_rows<4>(slot + kSlot, z + K, 2 * K, tokens, chans);
+                    ahead[0].put(slot);
+                    ahead[kReads - 1].put(slot + kSlot);
+                    ask(c + 32);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float gate[16], up[16];
@@ -706,8 +744,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         activate16(f[0], p.activation);
                         activate16(f[1], p.activation);
                         if (p.residual) {
-                            read_rows<4>(slot + kSlot, static_cast<const uint16_t*>(p.residual) + at, g.channels,
-                                         tokens, chans);
+                            ahead[0].put(slot + kSlot);
+                            ask(c + 32);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 float r[16];

@@ -54,11 +54,58 @@ __device__ __forceinline__ Segment product_segment(const ProductArgs& p, int e) 
 // below zero the divisor reaches 2^126, for which the quotient is 0, the limit.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, __fadd_rn(1.0f, expf(-v))); }
 
+// Good to 1 and 2 ulp for arguments in the normal range.
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Normal distribution function and e = exp(-v^2 / 2), good to some 10 parts in
+// 2^24 on either side of zero.  With z = |v| / sqrt 2 the tail is erfc(z) / 2 =
+// exp(-z^2) erfcx(z) / 2, and erfcx(z) = t p(t) for t = 1 / (1 + 0.4 z), p being
+// smooth on (0, 1]: a polynomial fitted to the relative error (6e-9) with z up
+// to 9.3.  The exponent -v^2 / 2 log2(e) is taken with its rounding error, which
+// the power of two would otherwise multiply.  From |v| = 15 on e is 0.  (With
+// normcdff and a second exp the elementwise pass of 16,384 x 4,096 took 218 us.)
+__device__ __forceinline__ float normal_cdf(float v, float& e) {
+    const float a = fminf(fabsf(v), 15.0f);
+    const float t = rcp_approx(fmaf(a, 0.28284271247461901f, 1.0f));
+    float p = -0.0310080519f;
+    p = fmaf(p, t, 0.205737795f);
+    p = fmaf(p, t, -0.517100257f);
+    p = fmaf(p, t, 0.57201353f);
+    p = fmaf(p, t, -0.30498704f);
+    p = fmaf(p, t, 0.283243945f);
+    p = fmaf(p, t, 0.125772253f);
+    p = fmaf(p, t, 0.215766981f);
+    p = fmaf(p, t, 0.224848533f);
+    p = fmaf(p, t, 0.225712317f);
+    // -log2(e) / 2 = kHi + kLo
+    constexpr float kHi = -0.72134752044448169f;
+    constexpr float kLo = (float)(-0.72134752044448169 - (double)kHi);
+    const float square = a * a, left = fmaf(a, a, -square);
+    const float power = square * kHi;
+    const float rest = fmaf(left, kHi, fmaf(square, kLo, fmaf(square, kHi, -power)));
+    e = exp2_approx(power);
+    e = fmaf(e, rest * 0.69314718055994531f, e);
+    const float tail = 0.5f * t * p * e;
+    return v < 0.0f ? tail : 1.0f - tail;
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case EP_ACT_RELU: return v < 0.0f ? 0.0f : v;  // keeps NaN
         case EP_ACT_SILU: return v * sigmoid(v);
-        case EP_ACT_GELU: return v * normcdff(v);  // 1 + erf would cancel far below zero
+        case EP_ACT_GELU: {
+            float e;
+            return v * normal_cdf(v, e);
+        }
         default: return v;
     }
 }
@@ -73,7 +120,9 @@ __device__ __forceinline__ float activate_back(float v, float dy, int act) {
             return dy * s * fmaf(v, 1.0f - s, 1.0f);
         }
         case EP_ACT_GELU: {
-            return dy * fmaf(v * 0.39894228040143268f, expf(-0.5f * v * v), normcdff(v));
+            float e;
+            const float cdf = normal_cdf(v, e);
+            return dy * fmaf(v * 0.39894228040143268f, e, cdf);
         }
         default: return dy;
     }

@@ -12,8 +12,9 @@ Bounds, with u = 2^-24 (half an ulp of fp32):
     0, off by less than 2^-126 (TINY allows that twice, for the quotient's own
     limit and for a product that rounds below it), which what s is multiplied
     by carries into the result: |u| (1 + |g|) |dh|, or |g| |dh|.
-  * The normal distribution function is good to 5 ulp (10 u), exp(-v^2 / 2) to
-    (v^2 / 2 + 4) u * 2 of itself (its argument is rounded twice).
+  * The normal distribution function is good to 10 u of itself (a polynomial of
+    6e-9, ten steps of it, an exponential and a quotient of 4 u each),
+    exp(-v^2 / 2) to (v^2 / 2 + 4) u * 2 of itself.
 """
 import math
 
