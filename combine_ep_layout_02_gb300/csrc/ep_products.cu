@@ -40,14 +40,19 @@ constexpr int kTileM = 256, kTileN = 256, kBlockK = 64;  // per pair
 constexpr int kMaxStages = 6;
 constexpr int kABytes = 128 * kBlockK * 2, kBBytes = 128 * kBlockK * 2;  // per block and stage
 constexpr int kStageBytes = kABytes + kBBytes;
-// warps that write the output (weight: two column shares of four)
-__host__ __device__ constexpr int epi_warps(bool weight) { return weight ? 8 : 4; }
-__host__ __device__ constexpr int threads_of(bool weight) { return 128 + 32 * epi_warps(weight); }
-constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels
-constexpr int kBox = 32 * 128;   // weight: 32 rows of 128 bytes
-// per warp: two slots (weight: a box, at the expense of a stage)
-__host__ __device__ constexpr int staging(bool weight) { return weight ? kBox : 2 * kSlot; }
-__host__ __device__ constexpr int stage_count(bool weight) { return weight ? 5 : kMaxStages; }
+// Warps that write the output: four, or two column shares of four (`eight`:
+// gradients of weights and fp32 outputs).
+__host__ __device__ constexpr int epi_warps(bool eight) { return eight ? 8 : 4; }
+__host__ __device__ constexpr int threads_of(bool eight) { return 128 + 32 * epi_warps(eight); }
+constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels in bf16
+constexpr int kBox = 32 * 128;   // 32 rows of 128 bytes
+// per warp: two slots, or a box, at the expense of a stage
+__host__ __device__ constexpr int staging(bool eight) { return eight ? kBox : 2 * kSlot; }
+__host__ __device__ constexpr int stage_count(bool eight) { return eight ? 5 : kMaxStages; }
+// fp32 outputs: blocks of the summed index whose sum the tensor core makes, and
+// registers of the first warps and of those that add
+constexpr int kSeg = 8;
+constexpr int kIssueRegs = 72, kAddRegs = 216;  // 128 * 72 + 256 * 216 = 384 * 168
 constexpr int kBand = 16;        // channel tiles that share the tokens while they are in L2
 
 struct Shared {
@@ -58,8 +63,8 @@ struct Shared {
     int tiles[EP_MAX_EXPERTS + 1];  // exclusive scan of the experts' token tiles
 };
 
-constexpr size_t smem_bytes(bool weight) {
-    return 1024 + stage_count(weight) * kStageBytes + epi_warps(weight) * staging(weight) + sizeof(Shared);
+constexpr size_t smem_bytes(bool eight) {
+    return 1024 + stage_count(eight) * kStageBytes + epi_warps(eight) * staging(eight) + sizeof(Shared);
 }
 static_assert(smem_bytes(false) <= 227 * 1024 && smem_bytes(true) <= 227 * 1024, "");
 
@@ -277,19 +282,111 @@ __device__ __forceinline__ void activate16(float (&f)[16], int act) {
     }
 }
 
-__device__ __noinline__ void activate4(float (&f)[4], int act) {
+__device__ __forceinline__ void activate4(float (&f)[4], int act) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = activate(f[i], act);
 }
 
-template <ProductKind KIND, bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND == kWeight), 1)
+// A lane's row and piece of 16 bytes in a box with the TMA's 128-byte swizzle.
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int row, int piece) {
+    return box + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void store_box(uint32_t box, const CUtensorMap& map, int x, int y, int z) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tma_store_3d(&map, x, y, z, box);
+}
+
+// fp32 gradients of weights: rows n.. of dw (a lane's each), `share` columns from k.
+__device__ __forceinline__ void write_weights(const float (&acc)[8][16], const ProductArgs& p, const CUtensorMap& map,
+                                              uint32_t box, const Tile& t, int n, int k, int share, int N, int K) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {  // 32 columns
+        if (c * 16 >= share || n >= N || k + c * 16 >= K) break;
+        if (lane == 0) tma_store_wait<0>();
+        __syncwarp();
+        if (p.add) add_to_box(box, p.add, 4, ((int64_t)t.e * N + n) * K + k + c * 16, K, N - n, K - k - c * 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t at = box_at(box, lane, j);
+            float f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f[x] = acc[c + (j >> 2)][(j & 3) * 4 + x];
+            if (p.add) {
+                const uint4 q = ld_shared_v4(at);
+                f[0] += __uint_as_float(q.x), f[1] += __uint_as_float(q.y);
+                f[2] += __uint_as_float(q.z), f[3] += __uint_as_float(q.w);
+            }
+            st_shared_v4(at, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                        __float_as_uint(f[3])));
+        }
+        store_box(box, map, k + c * 16, n, t.e);
+    }
+}
+
+// fp32 outputs of a dense layer: channels ch.. (a lane's each), `share` columns
+// of the tile from c0.  32 tokens of 32 channels turn in shared memory (a lane's
+// channel in, four channels of a token out), so that a store is 16 bytes a lane.
+__device__ __forceinline__ void write_tokens(const float (&acc)[8][16], const ProductArgs& p, uint32_t slot,
+                                             const Tile& t, int ch, int c0, int share, int channels) {
+    const int lane = threadIdx.x & 31, piece = lane & 7, n = ch + piece * 4;
+    const bool live = n < channels;
+    float bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = p.bias && live ? load_typed(p.bias, p.bias_type, n + j) : 0.0f;
+    float* out = static_cast<float*>(p.out) + (int64_t)t.part * p.rows * channels;
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+        const int left = min(share, t.n - c0) - c * 16;  // tokens from here on
+        if (left <= 0 || ch >= channels) break;
+        const int tokens = live ? min(32, left) : 0;
+        const int64_t at = (int64_t)(t.row + c0 + c * 16) * channels + ch;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + j * 128 + lane * 4), "f"(acc[c + (j >> 4)][j & 15])
+                         : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {  // 16 tokens, their residuals' loads together
+            float4 r[4];
+            const int64_t mine = at + (int64_t)Rows<8>::token(h) * channels + piece * 4;
+            if (p.residual) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (Rows<8>::token(h + j) < tokens)
+                        r[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + mine + (int64_t)j * 4 * channels);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int token = Rows<8>::token(h + j);
+                if (token >= tokens) continue;
+                const int64_t to = mine + (int64_t)j * 4 * channels;
+                const uint4 q = ld_shared_v4(slot + token * 128 + piece * 16);
+                float f[4] = {__uint_as_float(q.x) + bias[0], __uint_as_float(q.y) + bias[1],
+                              __uint_as_float(q.z) + bias[2], __uint_as_float(q.w) + bias[3]};
+                if (p.z)
+                    *reinterpret_cast<uint2*>(p.z + to) =
+                        make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
+                if (p.activation != EP_ACT_NONE) activate4(f, p.activation);
+                if (p.residual) f[0] += r[j].x, f[1] += r[j].y, f[2] += r[j].z, f[3] += r[j].w;
+                st_v4(out + to, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                           __float_as_uint(f[3])));
+            }
+        }
+    }
+}
+
+template <ProductKind KIND, bool SWIGLU, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND == kWeight || F32), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p, int most) {
     constexpr bool kGated = SWIGLU && KIND == kForward;  // two rows of weights per output channel
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    constexpr int kStages = stage_count(KIND == kWeight), kStaging = staging(KIND == kWeight);
-    constexpr int kEpiWarps = epi_warps(KIND == kWeight), kThreads = threads_of(KIND == kWeight);
+    constexpr bool kEight = KIND == kWeight || F32;
+    constexpr int kStages = stage_count(kEight), kStaging = staging(kEight);
+    constexpr int kEpiWarps = epi_warps(kEight), kThreads = threads_of(kEight);
     uint8_t* slots = stages + kStages * kStageBytes;
     Shared& sh = *reinterpret_cast<Shared*>(slots + kEpiWarps * kStaging);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -360,6 +457,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     g.total = KIND == kWeight ? (uint64_t)p.E * g.mtiles * g.ntiles : (uint64_t)sh.tiles[p.E] * g.mtiles * g.splits;
     const uint32_t pair = blockIdx.x >> 1, step = gridDim.x >> 1;
 
+    if (warp < 4) {
+    if (F32) registers_down<kIssueRegs>();
     if (warp == 0) {
         // ---- loads: this block's 128 rows of A and its half of B's columns
         const uint32_t bar0 = cluster_addr(full, 0);
@@ -429,16 +528,22 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         for (uint64_t i = pair; i < g.total && ok; i += step) {
             const Tile t = walk.tile(sh, g, p.E, i);
             if (t.blocks == 0) continue;
-            const uint32_t buf = done & 1;
-            if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, gave_up)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + buf * kTileN;
+            uint32_t buf = 0, d = 0;
             const uint32_t instr = bf16_instr_desc(kTileM, t.width, KIND != kForward, KIND == kWeight);
             for (int kb = 0; kb < t.blocks; ++kb, ++it) {
                 const uint32_t s = it % kStages;
+                // a new sum: the tile's, or with fp32 outputs a part of it
+                const bool first = kb == 0 || (F32 && kb % kSeg == 0);
+                const bool last = kb == t.blocks - 1 || (F32 && kb % kSeg == kSeg - 1);
+                if (first) {
+                    buf = done & 1;
+                    d = tmem + buf * kTileN;
+                    if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    ++done;
+                }
                 if (!mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up)) {
                     ok = false;
                     break;
@@ -456,13 +561,12 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 #pragma unroll
                     for (int j = 0; j < kBlockK / 16; ++j)
                         if (KIND != kWeight || j < steps)
-                            mma_pair_bf16(d, da + j * sa, db + j * sb, instr, kb > 0 || j > 0);
+                            mma_pair_bf16(d, da + j * sa, db + j * sb, instr, !first || j > 0);
                     mma_commit_pair(empty + 8 * s);
-                    if (kb == t.blocks - 1) mma_commit_pair(acc_full + 8 * buf);
+                    if (last) mma_commit_pair(acc_full + 8 * buf);
                 }
                 __syncwarp();
             }
-            ++done;
         }
         if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
             if (elect_one()) mma_commit_pair(drain);
@@ -495,16 +599,62 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             // reads them: a release at cluster scope took 2,000 cycles per tail
             if (lane == 0) mbar_arrive_pair(bar0 + 8 * s);
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        if (F32) registers_up<kAddRegs>();
         // ---- output
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t slot = smem_addr(slots) + (warp - 4) * kStaging;
         const uint32_t bar0 = cluster_addr(acc_empty, 0);
-        const bool f32 = p.out_type == EP_TYPE_F32;
         constexpr int kReads = KIND == kInput && SWIGLU ? 2 : 1, kReadPieces = kGated ? 2 : 4;
         uint32_t done = 0;
         Walk<KIND> walk;
+        if constexpr (F32) {
+            // The tensor core truncates where it adds to a sum, which over 4,096 values costs 4e-6 of the result. So
+            // it makes sums of 512 values, and they are added here, rounded, in registers.
+            bool ok = true;
+            for (uint64_t i = pair; i < g.total && ok; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
+                const int share = t.width / 2, c0 = ((warp >> 2) - 1) * share;  // this warp's columns
+                float acc[8][16];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c][j] = 0.0f;
+                for (int kb = 0; kb < t.blocks; kb += kSeg, ++done) {
+                    const uint32_t buf = done & 1, src = lanes + buf * kTileN + c0;
+                    if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        if (c * 16 >= share) break;
+                        uint32_t v[2][16];
+                        tmem_load(v[0], src + c * 16);
+                        tmem_load(v[1], src + c * 16 + 16);  // of an odd share: columns past it, not used
+                        tmem_wait_for(v[0]);
+                        tmem_wait_for(v[1]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            acc[c][j] += __uint_as_float(v[0][j]);
+                            acc[c + 1][j] += __uint_as_float(v[1][j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                }
+                if (!ok) break;
+                if (KIND == kWeight)
+                    write_weights(acc, p, maps.b[1], slot, t, t.m0 + (int)rank * 128 + quarter * 32, t.n0 + c0, share, N, K);
+                else
+                    write_tokens(acc, p, slot, t, t.m0 + (int)rank * 128 + quarter * 32, c0, share, g.channels);
+            }
+            if (KIND == kWeight && lane == 0) tma_store_wait<0>();
+        } else {
         for (uint64_t i = pair; i < g.total; i += step) {
             const Tile t = walk.tile(sh, g, p.E, i);
             const uint32_t buf = done & 1;
@@ -524,7 +674,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     const uint16_t* z = p.z + row * 2 * K + ch;
                     ahead[0].load(z, K * 4, tokens, chans * 2);
                     ahead[kReads - 1].load(z + K, K * 4, tokens, chans * 2);
-                } else if (KIND == kForward && p.residual && !f32) {
+                } else if (KIND == kForward && p.residual) {
                     ahead[0].load(static_cast<const uint16_t*>(p.residual) + row * g.channels + ch,
                                   (int64_t)g.channels * 2, tokens, chans * 2);
                 }
@@ -543,19 +693,16 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
                 const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
                 const int cols = min(t.width, K - t.n0);              // a multiple of 8
-                const int wide = f32 ? 32 : 64;                       // columns of a box
                 const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
-                for (int c = end - share; c < end; c += wide) {
-                    const uint32_t box = slot;
+                for (int c = end - share; c < end; c += 64) {
                     const bool write = n < N && c < cols;
                     if (write) {
                         if (lane == 0) tma_store_wait<0>();
                         __syncwarp();
-                        if (p.add) add_to_box(box, p.add, f32 ? 4 : 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
+                        if (p.add) add_to_box(slot, p.add, 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
                     }
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {  // 16 columns of 64
-                        if (h * 16 >= wide) break;
+                    for (int h = 0; h < 4; ++h) {
                         uint32_t v[16];
                         if (t.blocks > 0) {
                             __syncwarp();
@@ -569,99 +716,30 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         if (!write) continue;
                         float f[16];
                         as_floats(v, f);
-                        if (f32) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t at = box + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4);
-                                if (p.add) {
-                                    const uint4 q = ld_shared_v4(at);
-                                    f[4 * j] += __uint_as_float(q.x), f[4 * j + 1] += __uint_as_float(q.y);
-                                    f[4 * j + 2] += __uint_as_float(q.z), f[4 * j + 3] += __uint_as_float(q.w);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t at = box_at(slot, lane, h * 2 + j);
+                            float* q8 = f + 8 * j;
+                            if (p.add) {
+                                const uint4 q = ld_shared_v4(at);
+                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    q8[2 * x] += bf16lo_to_f32(w[x]);
+                                    q8[2 * x + 1] += bf16hi_to_f32(w[x]);
                                 }
-                                st_shared_v4(at, make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]),
-                                                            __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3])));
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t at = box + lane * 128 + (((h * 2 + j) ^ (lane & 7)) << 4);
-                                float* q8 = f + 8 * j;
-                                if (p.add) {
-                                    const uint4 q = ld_shared_v4(at);
-                                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x) {
-                                        q8[2 * x] += bf16lo_to_f32(w[x]);
-                                        q8[2 * x + 1] += bf16hi_to_f32(w[x]);
-                                    }
-                                }
-                                st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
-                                                            pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
-                            }
+                            st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
+                                                        pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
                         }
                     }
-                    if (write) {
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) tma_store_3d(&maps.b[1], t.n0 + c, n, t.e, box);
-                    }
+                    if (write) store_box(slot, maps.b[1], t.n0 + c, n, t.e);
                 }
                 if (t.blocks > 0) ++done;
                 continue;
             }
             if (chans <= 0) {
                 release();
-                ++done;
-                continue;
-            }
-            if (KIND == kForward && !SWIGLU && f32) {
-                // 32 tokens of 32 channels turn in shared memory (a lane's channel in, four channels of a token
-                // out), so that a store is 16 bytes a lane: single words took 2.5 times as long
-                const int piece = lane & 7, n = ch + piece * 4;
-                const bool live = piece * 4 < chans;
-                float bias[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) bias[j] = p.bias && live ? load_typed(p.bias, p.bias_type, n + j) : 0.0f;
-                float* out = static_cast<float*>(p.out) + (int64_t)t.part * p.rows * g.channels;
-                for (int c = 0; c < t.n; c += 32) {
-                    uint32_t v[2][16];
-                    __syncwarp();
-                    tmem_load(v[0], src + c);
-                    tmem_load(v[1], src + c + 16);
-                    tmem_wait_for(v[0]);
-                    tmem_wait_for(v[1]);
-                    if (c + 32 >= t.n) release();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(slot + j * 128 + lane * 4), "r"(v[j >> 4][j & 15])
-                                     : "memory");
-                    const int tokens = live ? min(32, t.n - c) : 0;
-                    const int64_t at = (int64_t)(t.row + c) * g.channels + ch;
-                    Rows<8> res;
-                    if (p.residual)
-                        res.load(static_cast<const float*>(p.residual) + at, (int64_t)g.channels * 4, tokens, 128);
-                    __syncwarp();
-                    Rows<8> rows;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int token = Rows<8>::token(j);
-                        const uint4 q = ld_shared_v4(slot + token * 128 + piece * 16);
-                        float f[4] = {__uint_as_float(q.x) + bias[0], __uint_as_float(q.y) + bias[1],
-                                      __uint_as_float(q.z) + bias[2], __uint_as_float(q.w) + bias[3]};
-                        if (p.z && token < tokens)
-                            *reinterpret_cast<uint2*>(p.z + at + (int64_t)token * g.channels + piece * 4) =
-                                make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
-                        if (p.activation != EP_ACT_NONE) activate4(f, p.activation);
-                        if (p.residual) {
-                            const uint4 r = res.v[j];
-                            f[0] += __uint_as_float(r.x), f[1] += __uint_as_float(r.y);
-                            f[2] += __uint_as_float(r.z), f[3] += __uint_as_float(r.w);
-                        }
-                        rows.v[j] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                               __float_as_uint(f[3]));
-                    }
-                    rows.store(out + at, (int64_t)g.channels * 4, tokens, 128);
-                }
                 ++done;
                 continue;
             }
@@ -764,6 +842,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             ++done;
         }
         if (KIND == kWeight && lane == 0) tma_store_wait<0>();
+        }
     }
     __syncwarp();
     __syncthreads();
@@ -847,19 +926,21 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     if (err != cudaSuccess) return err;
     static std::atomic<int> sm_cache[64];
     const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
-    static std::atomic<uint64_t> configured[5];
-    const int which = kind == kForward ? swiglu : kind == kInput ? 2 + swiglu : 4;
-    auto kernel = which == 0   ? product_kernel<kForward, false>
-                  : which == 1 ? product_kernel<kForward, true>
-                  : which == 2 ? product_kernel<kInput, false>
-                  : which == 3 ? product_kernel<kInput, true>
-                               : product_kernel<kWeight, false>;
-    const size_t smem = smem_bytes(kind == kWeight);
+    const bool f32 = p.out_type == EP_TYPE_F32, eight = kind == kWeight || f32;
+    static std::atomic<uint64_t> configured[7];
+    const int which = kind == kForward ? (swiglu ? 1 : f32 ? 2 : 0) : kind == kInput ? 3 + swiglu : 5 + f32;
+    auto kernel = which == 0   ? product_kernel<kForward, false, false>
+                  : which == 1 ? product_kernel<kForward, true, false>
+                  : which == 2 ? product_kernel<kForward, false, true>
+                  : which == 3 ? product_kernel<kInput, false, false>
+                  : which == 4 ? product_kernel<kInput, true, false>
+                  : which == 5 ? product_kernel<kWeight, false, false>
+                               : product_kernel<kWeight, false, true>;
+    const size_t smem = smem_bytes(eight);
     err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
-    return launch_pdl(kernel, dim3(grid), dim3(threads_of(kind == kWeight)), smem, stream, maps, p,
-                      most);
+    return launch_pdl(kernel, dim3(grid), dim3(threads_of(eight)), smem, stream, maps, p, most);
 }
 
 }  // namespace ep
