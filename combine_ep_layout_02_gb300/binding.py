@@ -667,7 +667,7 @@ def _result(name, t, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _want(name, t, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # a torch.Size compares as the tuple it is
         raise ValueError("%s must be %s" % (name, list(shape)))
     return t
 
@@ -760,6 +760,8 @@ def group_gemm_wgrad(dy, x, expert_counts, expert_offsets, kind="contiguous", ca
     _want("x", x, torch.bfloat16, dev)
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be [rows, N] and x [rows, K]")
+    if dw is not None and dw.dim() != 3:
+        raise ValueError("dw must be [E, N, K]")
     E = expert_counts.numel() if dw is None else dw.shape[0]
     _check_segments(expert_counts, expert_offsets, kind, E, dev)
     dw = _result_of_types("dw", dw, (E, dy.shape[1], x.shape[1]), dtype, dev)
@@ -772,6 +774,9 @@ def group_gemm_wgrad(dy, x, expert_counts, expert_offsets, kind="contiguous", ca
     return dw
 
 
+LINEAR_FEW_TOKENS = 16
+
+
 def linear_workspace_bytes(M, K, N, activation="none"):
     return int(load().ep_linear_workspace_bytes(M, K, N, ACTIVATIONS[activation]))
 
@@ -781,15 +786,17 @@ def _check_linear(x, w, activation):
     if activation not in ACTIVATIONS:
         raise ValueError("activation must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
     _check_dev("x", x, torch.bfloat16)
-    _want("w", w, torch.bfloat16, x.device)
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    dev = x.device
+    _want("w", w, torch.bfloat16, dev)
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
         raise ValueError("x must be [M, K] and w [N, K]")
-    n = w.shape[0]
+    n = ws[0]
     if activation == "swiglu":
         if n % 2 != 0:
             raise ValueError("w must hold as many gate as up rows")
         n //= 2
-    return x.device, x.shape[0], x.shape[1], n
+    return dev, xs[0], xs[1], n
 
 
 def linear(x, w, bias=None, activation="none", residual=None, out=None, dtype=torch.bfloat16, z=None,
@@ -802,26 +809,31 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, dtype=to
     ``linear_backward`` takes (see ``ep_linear``)."""
     dev, M, K, N = _check_linear(x, w, activation)
     out = _result_of_types("out", out, (M, N), dtype, dev)
-    if activation == "swiglu" and out.dtype is not torch.bfloat16:
+    out_type = TYPES[out.dtype]
+    if out_type == 0 and activation == "swiglu":
         raise ValueError("swiglu gives bfloat16")
+    bias_type = 0
     if bias is not None:
         _result_of_types("bias", bias, (w.shape[0],), None, dev)
+        bias_type = TYPES[bias.dtype]
     if residual is not None:
         _result("residual", residual, (M, N), out.dtype, dev)
     if z is not None:
         _result("z", z, (M, w.shape[0]), torch.bfloat16, dev)
-    lib = load()
+    lib = _lib or load()
     act = ACTIVATIONS[activation]
-    need = lib.ep_linear_workspace_bytes(M, K, N, act)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None and M > LINEAR_FEW_TOKENS:
+        need = _on_current(dev, lib.ep_linear_workspace_bytes, M, K, N, act)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    size = 0
     if workspace is not None:
         _want("workspace", workspace, workspace.dtype, dev)
+        size = workspace.numel() * workspace.element_size()
     _rc("ep_linear", _on_current(
-        dev, lib.ep_linear, x.data_ptr(), M, K, w.data_ptr(), N, _addr(bias),
-        TYPES[torch.float32 if bias is None else bias.dtype], act, _addr(residual), out.data_ptr(),
-        TYPES[out.dtype], _addr(z), _status_addr(status, dev), _addr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_of(dev)))
+        dev, lib.ep_linear, x.data_ptr(), M, K, w.data_ptr(), N, _addr(bias), bias_type, act,
+        _addr(residual), out.data_ptr(), out_type, _addr(z), _status_addr(status, dev), _addr(workspace), size,
+        _stream_of(dev)))
     return out
 
 
@@ -868,19 +880,19 @@ def combine_backward(dout, y, topk_w, dst_row, dy=None, dw=None, status=None):
     ``ep_combine_backward``)."""
     _check_dev("dout", dout, torch.bfloat16)
     dev = dout.device
-    for name, t, dt in (("y", y, torch.bfloat16), ("topk_w", topk_w, torch.float32), ("dst_row", dst_row, torch.int32)):
-        _want(name, t, dt, dev)
-    if dout.dim() != 2 or y.dim() != 2 or y.shape[1] != dout.shape[1]:
+    _want("y", y, torch.bfloat16, dev)
+    _want("topk_w", topk_w, torch.float32, dev)
+    _want("dst_row", dst_row, torch.int32, dev)
+    ds, ys, pairs = dout.shape, y.shape, dst_row.shape
+    if len(ds) != 2 or len(ys) != 2 or ys[1] != ds[1]:
         raise ValueError("dout must be [T, H] and y [rows, H]")
-    T, H = dout.shape
-    if dst_row.dim() != 2 or dst_row.shape[0] != T or topk_w.shape != dst_row.shape:
+    if len(pairs) != 2 or pairs[0] != ds[0] or topk_w.shape != pairs:
         raise ValueError("topk_w and dst_row must be [T, k]")
-    dy = _result("dy", dy, y.shape, torch.bfloat16, dev)
-    dw = _result("dw", dw, topk_w.shape, torch.float32, dev)
+    dy = _result("dy", dy, ys, torch.bfloat16, dev)
+    dw = _result("dw", dw, pairs, torch.float32, dev)
     _rc("ep_combine_backward", _on_current(
         dev, load().ep_combine_backward, dout.data_ptr(), y.data_ptr(), topk_w.data_ptr(), dst_row.data_ptr(),
-        T, H, dst_row.shape[1], y.shape[0], dy.data_ptr(), dw.data_ptr(), _status_addr(status, dev),
-        _stream_of(dev)))
+        ds[0], ds[1], pairs[1], ys[0], dy.data_ptr(), dw.data_ptr(), _status_addr(status, dev), _stream_of(dev)))
     return dy, dw
 
 

@@ -155,6 +155,10 @@ struct Walk {
     }
 };
 
+// How long a wait for a whole tile may last: a second, and 2 us per block of the
+// summed index, several times what a block takes.
+__device__ __forceinline__ uint64_t tile_limit(int blocks) { return 1000000000ull + 2000ull * (uint32_t)blocks; }
+
 // ---- the epilogue's pieces ---------------------------------------------------
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
@@ -585,7 +589,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             it += t.blocks;
             if (t.blocks == 0 || t.tail == 0) continue;
             const uint32_t s = (it - 1) % kStages;
-            if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up)) break;
+            if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up, tile_limit(t.blocks))) break;
             phases ^= 1u << s;
             uint8_t* a = stages + s * kStageBytes;
             const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
@@ -681,7 +685,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             };
             if (KIND != kWeight) ask(0);
             if (t.blocks > 0) {
-                if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) break;
+                if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
                 tc_fence_after();
             }
             auto release = [&]() {  // the buffer's last sums are in registers
@@ -854,7 +858,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
 
 }  // namespace
 
-DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated) {
+DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool split) {
     static std::atomic<int> sm_cache[64];
     const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
     const int64_t pairs = sms >= 2 ? sms / 2 : 1;
@@ -866,7 +870,7 @@ DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated) {
     double least = 0.0;
     for (int u = 8; u >= 1; --u) {
         const int64_t tokens = (M + 32 * u - 1) / (32 * u);
-        for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= blocks); ++want) {
+        for (int64_t want = 1; want <= (split ? 16 : 1) && (want == 1 || want * 4 <= blocks); ++want) {
             const int64_t per = (blocks + want - 1) / want, splits = (blocks + per - 1) / per;
             if (splits != want) continue;
             // parts are products with all rows of w alike, written and read again in fp32
@@ -885,9 +889,22 @@ DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated) {
     return best;
 }
 
+// Columns of a weight gradient's tile: 256, or 128 where that is all there is or
+// where one expert's tiles would leave pairs without work (a block of the summed
+// index takes 330 cycles instead of 512, for half of the columns).
+static int weight_columns(const ProductArgs& p) {
+    if (p.K <= 128) return 128;
+    if (p.E > 1) return kTileN;
+    static std::atomic<int> sm_cache[64];
+    const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
+    const int64_t pairs = sms >= 2 ? sms / 2 : 1, mtiles = (p.N + kTileM - 1) / kTileM;
+    auto rounds = [&](int columns) { return (mtiles * ((p.K + columns - 1) / columns) + pairs - 1) / pairs; };
+    return rounds(128) * 330 < rounds(256) * 512 ? 128 : kTileN;
+}
+
 cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream) {
     const bool swiglu = p.activation == EP_ACT_SWIGLU;
-    const int most = kind == kWeight && p.K <= 128 ? 128 : p.most ? p.most : kTileN;
+    const int most = kind == kWeight ? weight_columns(p) : p.most ? p.most : kTileN;
     Maps maps;
     const uint64_t N = (uint64_t)p.N, K = (uint64_t)p.K, E = (uint64_t)p.E, rows = (uint64_t)p.rows;
     cudaError_t err = cudaSuccess;

@@ -38,11 +38,11 @@ struct ProductArgs {
     int most, splits;
 };
 
-// How a dense product of more than kLinearFew tokens is cut.
+// How a dense product of more than EP_LINEAR_FEW_TOKENS tokens is cut.
 struct DensePlan {
     int most, splits;
 };
-DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated);
+DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool split);
 
 // Rows of expert e (of the whole buffer where there are no experts).
 __device__ __forceinline__ Segment product_segment(const ProductArgs& p, int e) {
@@ -147,8 +147,7 @@ __device__ __forceinline__ float load_typed(const void* p, int type, int64_t i) 
 
 cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t stream);
 
-// kForward of one expert for up to kLinearFew tokens
-constexpr int kLinearFew = 16;
+// kForward of one expert for up to EP_LINEAR_FEW_TOKENS tokens
 cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream);
 
 // the epilogue over the parts' sums [splits, rows, N]

@@ -16,12 +16,15 @@ inline int cuda_status(cudaError_t e) {
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 inline const uint16_t* bf16(const void* p) { return static_cast<const uint16_t*>(p); }
 
+// A tile's last row and channel still have 32-bit coordinates.
+constexpr int64_t kMaxRows = INT32_MAX - 256, kMaxWidth = 1 << 30;
+
 // Sizes, segments and the word that the experts' products have in common.
 // `weight_rows` per expert, `width` of every operand a multiple of 8.
 int check_group(int64_t rows, int64_t weight_rows, int64_t width, int E, const int32_t* counts,
                 const int32_t* offsets, int kind, int capacity, const uint32_t* status) {
-    if (rows < 0 || rows > INT32_MAX || weight_rows < 1 || width < 1 || width > INT32_MAX || E < 1 ||
-        E > EP_MAX_EXPERTS || weight_rows > INT32_MAX / E)
+    if (rows < 0 || rows > kMaxRows || weight_rows < 1 || weight_rows > kMaxWidth || width < 1 ||
+        width > kMaxWidth || E < 1 || E > EP_MAX_EXPERTS || weight_rows > INT32_MAX / E)
         return EP_ERR_INVALID_ARG;
     if (kind != EP_LAYOUT_CONTIGUOUS && kind != EP_LAYOUT_MASKED) return EP_ERR_INVALID_ARG;
     if (kind == EP_LAYOUT_MASKED && (capacity < 0 || (int64_t)E * capacity > rows)) return EP_ERR_INVALID_ARG;
@@ -35,8 +38,8 @@ bool known_type(int t) { return t == EP_TYPE_F32 || t == EP_TYPE_BF16; }
 
 // Sizes and pointers that ep_linear and ep_linear_backward have in common.
 int check_linear(int64_t M, int64_t K, int64_t N, int activation) {
-    if (M < 0 || M > INT32_MAX || K < 1 || K > INT32_MAX || N < 1 || N > INT32_MAX / 2 || activation < EP_ACT_NONE ||
-        activation > EP_ACT_SWIGLU)
+    if (M < 0 || M > kMaxRows || K < 1 || K > kMaxWidth || N < 1 || activation < EP_ACT_NONE ||
+        activation > EP_ACT_SWIGLU || N > kMaxWidth / (activation == EP_ACT_SWIGLU ? 2 : 1))
         return EP_ERR_INVALID_ARG;
     if (K % 8 != 0 || N % (activation == EP_ACT_SWIGLU ? 16 : 8) != 0) return EP_ERR_ALIGNMENT;
     return EP_OK;
@@ -82,7 +85,7 @@ int ep_group_gemm(const void* a, int64_t rows, int64_t K, const void* w, int64_t
 int ep_group_gemm_swiglu(const void* a, int64_t rows, int64_t K, const void* w13, int64_t I, int E,
                          const int32_t* expert_counts, const int32_t* expert_offsets, int kind,
                          int capacity, void* out, void* z, uint32_t* status, void* stream) {
-    if (I < 1 || I > INT32_MAX / 2) return EP_ERR_INVALID_ARG;
+    if (I < 1 || I > kMaxWidth / 2) return EP_ERR_INVALID_ARG;
     const int rc = check_group(rows, 2 * I, K, E, expert_counts, expert_offsets, kind, capacity, status);
     if (rc != EP_OK) return rc;
     if (I % 16 != 0) return EP_ERR_ALIGNMENT;
@@ -114,7 +117,7 @@ int ep_group_gemm_swiglu_dgrad(const void* dy, int64_t rows, int64_t H, const vo
                                int E, const void* z, const int32_t* expert_counts,
                                const int32_t* expert_offsets, int kind, int capacity, void* dz,
                                uint32_t* status, void* stream) {
-    if (I > INT32_MAX / 2) return EP_ERR_INVALID_ARG;
+    if (I > kMaxWidth / 2) return EP_ERR_INVALID_ARG;
     const int rc = check_group(rows, H, I, E, expert_counts, expert_offsets, kind, capacity, status);
     if (rc != EP_OK) return rc;
     if (I % 16 != 0) return EP_ERR_ALIGNMENT;
@@ -144,9 +147,9 @@ int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int64_t N, 
 }
 
 size_t ep_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation) {
-    if (M <= ep::kLinearFew || check_linear(M, K, N, activation) != EP_OK) return 0;
+    if (M <= EP_LINEAR_FEW_TOKENS || check_linear(M, K, N, activation) != EP_OK) return 0;
     const int64_t wide = activation == EP_ACT_SWIGLU ? 2 * N : N;
-    const int splits = ep::dense_plan(M, K, N, activation == EP_ACT_SWIGLU).splits;
+    const int splits = ep::dense_plan(M, K, N, activation == EP_ACT_SWIGLU, true).splits;
     return splits > 1 ? (size_t)splits * M * wide * 4 : 0;
 }
 
@@ -173,8 +176,8 @@ int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N, con
     p.out = out;
     p.out_type = out_type;
     p.z = static_cast<uint16_t*>(z);
-    if (M <= ep::kLinearFew) return cuda_status(ep::launch_linear_few(p, as_stream(stream)));
-    const ep::DensePlan plan = ep::dense_plan(M, K, N, gated);
+    if (M <= EP_LINEAR_FEW_TOKENS) return cuda_status(ep::launch_linear_few(p, as_stream(stream)));
+    const ep::DensePlan plan = ep::dense_plan(M, K, N, gated, true);
     p.most = plan.most;
     if (plan.splits == 1) return cuda_status(ep::launch_product(p, ep::kForward, as_stream(stream)));
     // the parts' sums as they are, all rows of w alike, then everything that follows a sum
@@ -212,6 +215,7 @@ int ep_linear_backward(const void* dy, const void* x, const void* w, const void*
     if (err == cudaSuccess && dx && M > 0) {
         ep::ProductArgs p = group_args(g, w, M, wide, K, 1, nullptr, nullptr, 0, 0, status);
         p.out = dx;
+        p.most = ep::dense_plan(M, wide, K, false, false).most;
         err = ep::launch_product(p, ep::kInput, as_stream(stream));
     }
     if (err == cudaSuccess && dw) {

@@ -75,15 +75,17 @@ __device__ __forceinline__ uint64_t global_ns() {
 // leaves its loop on false, so that a broken run ends instead of hanging.  A
 // whole warp waits, converged, and asks one barrier and one word: its lanes get
 // the same answer (65,536 waits that completed while another warp gave up: all
-// of them).  A vote on each answer cost the prefill products 1.3 %.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// of them).  A vote on each answer cost the prefill products 1.3 %.  `limit`: for
+// waits that a long sum is due to outlast.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint64_t limit = 1000000000ull) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     const uint64_t start = global_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (*gave_up) return false;
-        if (global_ns() - start > 1000000000ull) {
+        if (global_ns() - start > limit) {
             *gave_up = 1;
             return false;
         }

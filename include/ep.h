@@ -71,6 +71,7 @@ extern "C" {
 #define EP_MAX_EXPERTS 1024
 #define EP_MOE_FEW_MAX_TOKENS 64   /* tokens of one ep_moe_few() call */
 #define EP_MOE_FEW_MAX_WIDTH 16384 /* H and I of ep_moe_few() */
+#define EP_LINEAR_FEW_TOKENS 16    /* ep_linear() needs no workspace up to this M */
 #define EP_MAX_GROUPS 32       /* groups of experts that ep_route() can choose among */
 #define EP_STATIC_WS_BYTES (2u << 20) /* scratch held by ep_layout_static_ws() */
 
@@ -476,8 +477,9 @@ EP_API int ep_moe_few(const void* x, int64_t T, int H, int k, const int32_t* top
  *             whatever they hold; up to 255 rows that follow a segment in the
  *             buffer may be read.
  * Outputs overlap no input (but dw may be add).
- * Limits: all widths multiples of 8, I a multiple of 16; rows < 2^31; E <=
- * EP_MAX_EXPERTS; E * (rows of weights per expert) < 2^31.
+ * Limits: all widths multiples of 8 and at most 2^30 (2*I included), I a
+ * multiple of 16; rows < 2^31 - 256; E <= EP_MAX_EXPERTS; E * (rows of weights
+ * per expert) < 2^31.
  */
 EP_API int ep_group_gemm(const void* a, int64_t rows, int64_t K, const void* w, int64_t N, int E,
                          const int32_t* expert_counts, const int32_t* expert_offsets, int kind,
@@ -515,10 +517,13 @@ EP_API int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int6
  *  residual  [M, N] of out_type, 16-byte aligned, or NULL; may be out itself.
  *  out       [M, N] float32 or bf16 (out_type), 16-byte aligned.
  *  z         [M, N or 2*N] bf16, 16-byte aligned, or NULL.
- *  workspace ep_linear_workspace_bytes(M, K, N, activation) bytes, 16-byte
- *            aligned, no initialisation needed; may be NULL where that is 0.
+ *  workspace ep_linear_workspace_bytes(M, K, N, activation) bytes (for the
+ *            current device; 0 for M <= EP_LINEAR_FEW_TOKENS), 16-byte aligned,
+ *            no initialisation needed, the call's own until its work is done;
+ *            may be NULL where the size is 0.
  * Limits: K and N multiples of 8; with EP_ACT_SWIGLU N a multiple of 16 and
- * out_type EP_TYPE_BF16; M < 2^31, rows of w < 2^31.  M == 0 is valid.
+ * out_type EP_TYPE_BF16; M < 2^31 - 256, K and the rows of w at most 2^30.
+ * M == 0 is valid.
  */
 EP_API size_t ep_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation);
 EP_API int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N,
@@ -552,7 +557,8 @@ EP_API int ep_linear_backward(const void* dy, const void* x, const void* w, cons
  *     dy[r, h]    = bf16_rne( topk_w[t, j] * dout[t, h] )
  *     dw[t, j]    = sum over h of dout[t, h] * y[r, h]                  (fp32)
  * and dw[t, j] = 0 for the others.  Rows of dy that no pair maps to are not
- * touched.  The order of each sum is fixed.
+ * touched; no two pairs share a row, as a layout never lets them.  The order of
+ * each sum is fixed.
  *
  *  dout [T, H], y [rows, H], dy [rows, H] bf16, 16-byte aligned;  topk_w, dw
  *  [T, k] float32;  dst_row [T, k] int32 as for ep_combine, a dst_row outside

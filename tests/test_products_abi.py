@@ -50,7 +50,8 @@ def test_group_argument_validation(lib, which):
         return lib.ep_group_gemm_wgrad(a, w, rows, N, K, E, *seg, z, out, ty, status, None)
     if which != "wgrad":
         assert call(rows=0, a=None) == 0
-    assert call(rows=-1) == 1 and call(rows=1 << 31) == 1
+    assert call(rows=-1) == 1 and call(rows=1 << 31) == 1 and call(rows=(1 << 31) - 256) == 1
+    assert call(N=(1 << 30) + 16, E=1) == 1 and call(K=(1 << 30) + 16, E=1) == 1
     assert call(K=0) == 1 and call(N=0) == 1 and call(E=0) == 1 and call(E=1025) == 1
     assert call(E=1024, N=1 << 21, K=1 << 21) == 1      # weight rows beyond 31 bits
     assert call(K=100) == 2 and call(N=100) == 2
@@ -74,7 +75,8 @@ def test_linear_argument_validation(lib):
              ws=FAKE, wsb=1 << 30):
         return lib.ep_linear(x, M, K, w, N, bias, bt, act, res, out, ty, z, status, ws, wsb, None)
     assert call(M=0, x=None, out=None) == 0
-    assert call(M=-1) == 1 and call(M=1 << 31) == 1 and call(K=0) == 1 and call(N=0) == 1 and call(N=1 << 30) == 1
+    assert call(M=-1) == 1 and call(M=(1 << 31) - 256) == 1 and call(K=0) == 1 and call(N=0) == 1
+    assert call(N=(1 << 30) + 8) == 1 and call(K=(1 << 30) + 8) == 1 and call(N=(1 << 29) + 16, act=4) == 1
     assert call(act=5) == 1 and call(act=-1) == 1 and call(ty=2) == 1 and call(bt=2) == 1 and call(act=4, ty=0) == 1
     assert call(K=60) == 2 and call(N=60) == 2 and call(act=4, N=24) == 2
     for name in ("x", "w", "out"):
