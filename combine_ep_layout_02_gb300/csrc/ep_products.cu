@@ -466,6 +466,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     if (warp == 0) {
         // ---- loads: this block's 128 rows of A and its half of B's columns
         const uint32_t bar0 = cluster_addr(full, 0);
+        // widths of whole blocks of 64 channels: one copy brings a stage's two blocks
+        const bool awhole = KIND != kForward && g.channels % 64 == 0;
+        const bool bwhole = KIND == kWeight && K % 64 == 0 && most == kTileN;
         uint32_t it = 0;
         bool ok = true;
         Walk<KIND> walk;
@@ -498,15 +501,24 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     const int k0 = t.k0 + kb * kBlockK;
                     if (KIND == kWeight) {
                         const int r0 = t.row + k0;
-                        tma_pair_2d(a, &maps.a, m, r0, bar);
-                        tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
+                        if (awhole) {
+                            tma_pair_3d(a, &maps.a, 0, r0, m / 64, bar);
+                        } else {
+                            tma_pair_2d(a, &maps.a, m, r0, bar);
+                            tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
+                        }
                         const int n = t.n0 + rank * half;
-                        for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b[0], n + j, r0, bar);
+                        if (bwhole)
+                            tma_pair_3d(b, &maps.b[0], 0, r0, n / 64, bar);
+                        else
+                            for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b[0], n + j, r0, bar);
                     } else {
                         if (kGated) {
                             tma_pair_5d(a, &maps.a, k0, 0, 0, m / 16, t.e, bar);
                         } else if (KIND == kForward) {
                             tma_pair_3d(a, &maps.a, k0, m, t.e, bar);
+                        } else if (awhole) {
+                            tma_pair_4d(a, &maps.a, 0, k0, m / 64, t.e, bar);
                         } else {
                             tma_pair_3d(a, &maps.a, m, k0, t.e, bar);
                             tma_pair_3d(a + kABytes / 2, &maps.a, m + 64, k0, t.e, bar);
@@ -889,6 +901,19 @@ DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool sp
     return best;
 }
 
+// Blocks of 64 tokens x 64 channels of a row-major matrix; `two`: a copy is two
+// such blocks, side by side in the matrix and one after the other in shared memory.
+static cudaError_t token_blocks_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t width, bool two) {
+    if (two) {
+        const uint64_t d[3] = {64, rows, width / 64}, s[2] = {width * 2, 128};
+        const uint32_t box[3] = {64, 64, 2};
+        return typed_map(map, EP_TYPE_BF16, base, 3, d, s, box);
+    }
+    const uint64_t d[2] = {width, rows}, s[1] = {width * 2};
+    const uint32_t box[2] = {64, 64};
+    return typed_map(map, EP_TYPE_BF16, base, 2, d, s, box);
+}
+
 // Columns of a weight gradient's tile: 256, or 128 where that is all there is or
 // where one expert's tiles would leave pairs without work (a block of the summed
 // index takes 330 cycles instead of 512, for half of the columns).
@@ -912,11 +937,8 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
         // no rows at all: nothing is loaded, and any address will do
         const void* dy = rows ? static_cast<const void*>(p.a) : p.out;
         const void* x = rows ? static_cast<const void*>(p.b) : p.out;
-        const uint32_t box[2] = {64, 64};
-        const uint64_t da[2] = {N, rows ? rows : 1}, sa[1] = {N * 2};
-        const uint64_t db[2] = {K, rows ? rows : 1}, sb[1] = {K * 2};
-        err = typed_map(&maps.a, EP_TYPE_BF16, dy, 2, da, sa, box);
-        if (err == cudaSuccess) err = typed_map(&maps.b[0], EP_TYPE_BF16, x, 2, db, sb, box);
+        err = token_blocks_map(&maps.a, dy, rows ? rows : 1, N, N % 64 == 0);
+        if (err == cudaSuccess) err = token_blocks_map(&maps.b[0], x, rows ? rows : 1, K, K % 64 == 0 && most == kTileN);
         const bool f32 = p.out_type == EP_TYPE_F32;
         const uint64_t size = f32 ? 4 : 2;
         const uint64_t dc[3] = {K, N, E}, sc[2] = {K * size, N * K * size};
@@ -928,6 +950,10 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
             const uint64_t d[5] = {K, 16, 2, I / 16, E}, s[4] = {K * 2, I * K * 2, 16 * K * 2, N * K * 2};
             const uint32_t box[5] = {64, 16, 2, 4, 1};
             err = typed_map(&maps.a, EP_TYPE_BF16, p.b, 5, d, s, box);
+        } else if (kind == kInput && K % 64 == 0) {
+            const uint64_t d[4] = {64, N, K / 64, E}, s[3] = {K * 2, 128, N * K * 2};
+            const uint32_t box[4] = {64, 64, 2, 1};
+            err = typed_map(&maps.a, EP_TYPE_BF16, p.b, 4, d, s, box);
         } else {
             const uint64_t d[3] = {K, N, E}, s[2] = {K * 2, N * K * 2};
             const uint32_t box[3] = {64, kind == kForward ? 128u : 64u, 1};
