@@ -403,7 +403,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     if (warp == 0) tmem_alloc_pair(smem_addr(&sh.tmem), 512);
     if (tid == 32) {
         tma_prefetch_map(&maps.a);
-        tma_prefetch_map(&maps.b[KIND == kWeight ? 0 : most / 32 - 1]);
+        tma_prefetch_map(&maps.b[0]);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, KIND == kWeight ? 2 : 1);
             mbar_init(empty + 8 * i, 1);
@@ -878,23 +878,31 @@ DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool sp
     // 4,096 channels: the narrow ones wait for the weights from L2.
     static const int stage[8] = {276, 285, 311, 330, 357, 421, 458, 512};
     const int64_t blocks = (K + kBlockK - 1) / kBlockK;
+    // parts are products with all rows of w alike, written and read again in fp32
+    const int64_t rows = gated ? 2 * channels : channels, mtiles = (rows + kTileM - 1) / kTileM;
+    struct Parts {
+        int64_t count, per, mtiles;
+        double more;
+    } parts[16];
+    int kinds = 0;
+    for (int64_t want = 1; want <= (split ? 16 : 1) && (want == 1 || want * 4 <= blocks); ++want) {
+        const int64_t per = (blocks + want - 1) / want;
+        if ((blocks + per - 1) / per != want) continue;
+        if (want == 1)
+            parts[kinds++] = {1, per, gated ? (channels + kTileM / 2 - 1) / (kTileM / 2) : mtiles, 0.0};
+        else
+            parts[kinds++] = {want, per, mtiles, 4000.0 + (double)(want * M) * (double)rows * 8.0 / 4000.0};
+    }
     DensePlan best = {kTileN, 1};
     double least = 0.0;
     for (int u = 8; u >= 1; --u) {
         const int64_t tokens = (M + 32 * u - 1) / (32 * u);
-        for (int64_t want = 1; want <= (split ? 16 : 1) && (want == 1 || want * 4 <= blocks); ++want) {
-            const int64_t per = (blocks + want - 1) / want, splits = (blocks + per - 1) / per;
-            if (splits != want) continue;
-            // parts are products with all rows of w alike, written and read again in fp32
-            const int64_t rows = gated ? 2 * channels : channels;
-            const int64_t mtiles = splits > 1 || !gated ? (rows + kTileM - 1) / kTileM
-                                                        : (channels + kTileM / 2 - 1) / (kTileM / 2);
-            const int64_t units = mtiles * tokens * splits, rounds = (units + pairs - 1) / pairs;
-            double cost = (double)rounds * (double)(per * stage[u - 1] + 400) + 2000.0 + 400.0 * u;
-            if (splits > 1) cost += 4000.0 + (double)(splits * M * rows) * 8.0 / 4000.0;
+        for (int i = 0; i < kinds; ++i) {
+            const int64_t rounds = (parts[i].mtiles * tokens * parts[i].count + pairs - 1) / pairs;
+            const double cost = (double)rounds * (double)(parts[i].per * stage[u - 1] + 400) + 2000.0 + 400.0 * u + parts[i].more;
             if (least == 0.0 || cost < least * 0.98) {
                 least = cost;
-                best = {32 * u, (int)splits};
+                best = {32 * u, (int)parts[i].count};
             }
         }
     }
@@ -961,7 +969,9 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
         }
         const uint64_t width = kind == kForward ? K : N;
         const uint64_t d[2] = {width, rows}, s[1] = {width * 2};
-        for (uint32_t j = 0; j < 8 && err == cudaSuccess; ++j) {
+        // the boxes that a tile of these rows can ask for
+        const uint32_t widest = (uint32_t)((rows < (uint64_t)most ? rows + 31 : (uint64_t)most) / 32);
+        for (uint32_t j = 0; j < widest && err == cudaSuccess; ++j) {
             const uint32_t box[2] = {64, 16 * (j + 1)};
             err = typed_map(&maps.b[j], EP_TYPE_BF16, p.a, 2, d, s, box);
         }
