@@ -26,8 +26,6 @@ act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict_
     constexpr int H = kGated ? 2 : 1;
     __shared__ float sums[kThreads / 32][8][H * 8];
     __shared__ float total[8 * 8 * H];  // of the strip's columns
-    pdl_wait();
-    pdl_trigger();
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int col = threadIdx.x % vecs, lane_row = threadIdx.x / vecs;
     const int per = kThreads / vecs;  // rows of a block's step
@@ -149,14 +147,12 @@ cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M
     cfg.gridDim = dim3((unsigned)(strips * cluster));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;  // an ordinary launch, as the products that follow it
     return cudaLaunchKernelEx(&cfg, kernel, dy, z, M, N, vecs, cluster, dz, dbias);
 }
 

@@ -417,8 +417,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.gave_up = 0;
     }
-    pdl_wait();
-    pdl_trigger();
     for (int e = tid; e < p.E; e += kThreads) {
         const Segment s = product_segment(p, e);
         if (s.bad && blockIdx.x == 0 && p.status) atomicOr(p.status, EP_FLAG_BAD_ROW);
@@ -443,7 +441,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         }
         if (lane == 0) sh.tiles[p.E] = base;
     }
-    __syncwarp();
     cluster_sync();  // both blocks' barriers are set up
 
     const uint32_t tmem = sh.tmem;
@@ -529,6 +526,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 __syncwarp();
             }
         }
+        // The MMAs' last arrivals are here before the block ends: they come from the pair's other block.
+        for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
+            ok = mbar_wait(empty + 8 * (j % kStages), (j / kStages) & 1, gave_up);
         if (!ok && rank == 0) {  // given up: the copies in flight end before the block does
             const uint64_t start = global_ns();
             for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
@@ -645,6 +645,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         break;
                     }
                     tc_fence_after();
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 8; c += 2) {
                         if (c * 16 >= share) break;
@@ -772,6 +773,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const int tokens = min(32, t.n - c);
                 const int64_t row = t.row + c;
                 uint32_t v[2][16];
+                __syncwarp();
                 tmem_load_16x256(v[0], src + c);
                 tmem_load_16x256(v[1], src + c + (16u << 16));
                 tmem_wait_for(v[0]);
@@ -863,9 +865,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     __syncwarp();
     __syncthreads();
     if (tid == 0 && sh.gave_up && p.status) atomicOr(p.status, EP_FLAG_TIMEOUT);
-    __syncwarp();
     cluster_sync();  // no copy, arrival or MMA of the other block reaches this one any more
     if (warp == 0) tmem_dealloc_pair(tmem, 512);
+    cluster_sync();  // the release is a pair's: neither block leaves its SM to another kernel before both are through
 }
 
 }  // namespace
@@ -993,7 +995,15 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
-    return launch_pdl(kernel, dim3(grid), dim3(threads_of(eight)), smem, stream, maps, p, most);
+    // An ordinary launch, and no early one of what follows: blocks of another
+    // kernel that were started on one SM of a pair while the other still held its
+    // TMEM brought a chain of launches to a stop.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads_of(eight));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p, most);
 }
 
 }  // namespace ep
