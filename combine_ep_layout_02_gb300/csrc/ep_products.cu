@@ -25,11 +25,40 @@
 // MMAs read them.
 //
 // One persistent block per SM: warp 0 issues the TMA loads (128-byte swizzle,
-// six stages of 64 values of the summed index), warp 1 of the even block the
-// MMAs, warp 2 clears the tails, warps 4-7 write the output while the next
-// tile's MMAs run into the other half of the TMEM.  TMEM lanes are channels;
-// the output's rows are tokens.  Sums are read in an mma accumulator's layout
-// and turned by stmatrix, so that the stores run along the channels.
+// five or six stages of 64 values of the summed index), warp 1 of the even block
+// the MMAs, warp 2 clears the tails, the warps from 4 on write the output while
+// the next tile's MMAs run into the other half of the TMEM.  Forward and input:
+// TMEM lanes are channels, the output's rows tokens; sums are read in an mma
+// accumulator's layout and turned by stmatrix, so that the stores run along the
+// channels, and what the epilogue reads turns the other way.  Weight: a lane is a
+// row of dw; 128 bytes of 32 rows go through shared memory to a TMA store.
+//
+// The tensor core truncates where it adds to a sum: over n steps of 16 values
+// the result shrinks by about n / 3 parts in 2^24.  That is nothing beside the
+// rounding of a bf16 output, but fp32 outputs (weight gradients, router logits,
+// the parts of a split sum) would show it, so for those a sum ends after 512
+// values and eight warps add the sums, rounded, in registers (128 a thread:
+// setmaxnreg moves registers from the four issuing warps).  1,024 rows: error
+// 1.1e-6 without, 4.4e-7 with; 1.40 against 1.43-1.48 ms for 3.8 GB of gradients.
+//
+// Few tokens per expert: bound by the weights' bytes (4 rows each of 128 experts:
+// 84 us, 6.3 TB/s).  Many: by the tensor pipe, 95 % of its cycles busy (8 experts
+// of 1,024 rows, K 7168: 269 us, 1.79 PFLOP/s; dense 8,192 x 4,096 x 7,168: 247-257
+// us, cuBLAS 254), and on long calls by the power limit (1.5-1.6 PFLOP/s).
+// Behind it lies the copies' rate: a stage brings 32 KB into an SM in the 512
+// cycles of its MMAs, and an SM takes about 60 bytes a cycle.  So narrower tiles
+// wait for their weights (stage times in dense_plan()), and weight gradients of
+// few rows, whose tiles are stored after 16 stages, reach 67 % (fp32) and 83 %
+// (bf16) of the tensor pipe.
+//
+// Measured and not taken: clusters of two pairs that share the columns' copies
+// by multicast (within 2 % everywhere: the bytes into an SM stay the same, and
+// clusters of four leave 8 of 152 SMs idle); weight gradients stored from
+// registers, a lane a channel (111 -> 175 us at 19 rows: 64-byte pieces); full
+// tiles of 256 tokens and a rest (2.79 instead of 2.46 ms); several copies of 16
+// rows per stage (each copy costs the stage some 20 cycles); TMEM loads a chunk ahead (no
+// change: a load takes 100 cycles of a chunk's 1,000); a release at cluster scope
+// behind the tails' zeros (3.49 -> 1.49 ms without).
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
 
@@ -459,163 +488,163 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     const uint32_t pair = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < 4) {
-    if (F32) registers_down<kIssueRegs>();
-    if (warp == 0) {
-        // ---- loads: this block's 128 rows of A and its half of B's columns
-        const uint32_t bar0 = cluster_addr(full, 0);
-        // widths of whole blocks of 64 channels: one copy brings a stage's two blocks
-        const bool awhole = KIND != kForward && g.channels % 64 == 0;
-        const bool bwhole = KIND == kWeight && K % 64 == 0 && most == kTileN;
-        uint32_t it = 0;
-        bool ok = true;
-        Walk<KIND> walk;
-        for (uint64_t i = pair; i < g.total && ok; i += step) {
-            const Tile t = walk.tile(sh, g, p.E, i);
-            const int half = t.width / 2;
-            const uint32_t bytes = kABytes + half * kBlockK * 2;
-            const int m = t.m0 + rank * (g.per / 2);          // this block's first channel
-            const int brow = t.row + rank * half;             // and token
-            for (int kb = 0; kb < t.blocks; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (!mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
-                const bool last = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1;
-                uint32_t bar = bar0 + 8 * s;
-                if (elect_one()) {
-                    if (KIND == kWeight) {
-                        if (last) {  // counted here, and passed on by warp 2
-                            bar = cluster_addr(tail, rank) + 8 * s;
-                            mbar_expect_tx(tail + 8 * s, bytes);
-                        } else {
-                            mbar_expect_tx_pair(bar, bytes);
-                        }
-                    } else if (rank == 0) {
-                        mbar_expect_tx(full + 8 * s, 2 * bytes);
-                    }
-                    const int k0 = t.k0 + kb * kBlockK;
-                    if (KIND == kWeight) {
-                        const int r0 = t.row + k0;
-                        if (awhole) {
-                            tma_pair_3d(a, &maps.a, 0, r0, m / 64, bar);
-                        } else {
-                            tma_pair_2d(a, &maps.a, m, r0, bar);
-                            tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
-                        }
-                        const int n = t.n0 + rank * half;
-                        if (bwhole)
-                            tma_pair_3d(b, &maps.b[0], 0, r0, n / 64, bar);
-                        else
-                            for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b[0], n + j, r0, bar);
-                    } else {
-                        if (kGated) {
-                            tma_pair_5d(a, &maps.a, k0, 0, 0, m / 16, t.e, bar);
-                        } else if (KIND == kForward) {
-                            tma_pair_3d(a, &maps.a, k0, m, t.e, bar);
-                        } else if (awhole) {
-                            tma_pair_4d(a, &maps.a, 0, k0, m / 64, t.e, bar);
-                        } else {
-                            tma_pair_3d(a, &maps.a, m, k0, t.e, bar);
-                            tma_pair_3d(a + kABytes / 2, &maps.a, m + 64, k0, t.e, bar);
-                        }
-                        tma_pair_2d(b, &maps.b[half / 16 - 1], k0, brow, bar);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        // The MMAs' last arrivals are here before the block ends: they come from the pair's other block.
-        for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
-            ok = mbar_wait(empty + 8 * (j % kStages), (j / kStages) & 1, gave_up);
-        if (!ok && rank == 0) {  // given up: the copies in flight end before the block does
-            const uint64_t start = global_ns();
-            for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
-                while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) &&
-                       global_ns() - start < 1000000000ull) {
-                }
-        }
-    } else if (warp == 1 && rank == 0) {
-        // ---- MMAs of the pair
-        uint32_t it = 0, done = 0;
-        bool ok = true;
-        Walk<KIND> walk;
-        for (uint64_t i = pair; i < g.total && ok; i += step) {
-            const Tile t = walk.tile(sh, g, p.E, i);
-            if (t.blocks == 0) continue;
-            uint32_t buf = 0, d = 0;
-            const uint32_t instr = bf16_instr_desc(kTileM, t.width, KIND != kForward, KIND == kWeight);
-            for (int kb = 0; kb < t.blocks; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                // a new sum: the tile's, or with fp32 outputs a part of it
-                const bool first = kb == 0 || (F32 && kb % kSeg == 0);
-                const bool last = kb == t.blocks - 1 || (F32 && kb % kSeg == kSeg - 1);
-                if (first) {
-                    buf = done & 1;
-                    d = tmem + buf * kTileN;
-                    if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, gave_up)) {
+        if (F32) registers_down<kIssueRegs>();
+        if (warp == 0) {
+            // ---- loads: this block's 128 rows of A and its half of B's columns
+            const uint32_t bar0 = cluster_addr(full, 0);
+            // widths of whole blocks of 64 channels: one copy brings a stage's two blocks
+            const bool awhole = KIND != kForward && g.channels % 64 == 0;
+            const bool bwhole = KIND == kWeight && K % 64 == 0 && most == kTileN;
+            uint32_t it = 0;
+            bool ok = true;
+            Walk<KIND> walk;
+            for (uint64_t i = pair; i < g.total && ok; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
+                const int half = t.width / 2;
+                const uint32_t bytes = kABytes + half * kBlockK * 2;
+                const int m = t.m0 + rank * (g.per / 2);          // this block's first channel
+                const int brow = t.row + rank * half;             // and token
+                for (int kb = 0; kb < t.blocks; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!mbar_wait(empty + 8 * s, ((it / kStages) & 1) ^ 1, gave_up)) {
                         ok = false;
                         break;
                     }
-                    ++done;
+                    const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
+                    const bool last = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1;
+                    uint32_t bar = bar0 + 8 * s;
+                    if (elect_one()) {
+                        if (KIND == kWeight) {
+                            if (last) {  // counted here, and passed on by warp 2
+                                bar = cluster_addr(tail, rank) + 8 * s;
+                                mbar_expect_tx(tail + 8 * s, bytes);
+                            } else {
+                                mbar_expect_tx_pair(bar, bytes);
+                            }
+                        } else if (rank == 0) {
+                            mbar_expect_tx(full + 8 * s, 2 * bytes);
+                        }
+                        const int k0 = t.k0 + kb * kBlockK;
+                        if (KIND == kWeight) {
+                            const int r0 = t.row + k0;
+                            if (awhole) {
+                                tma_pair_3d(a, &maps.a, 0, r0, m / 64, bar);
+                            } else {
+                                tma_pair_2d(a, &maps.a, m, r0, bar);
+                                tma_pair_2d(a + kABytes / 2, &maps.a, m + 64, r0, bar);
+                            }
+                            const int n = t.n0 + rank * half;
+                            if (bwhole)
+                                tma_pair_3d(b, &maps.b[0], 0, r0, n / 64, bar);
+                            else
+                                for (int j = 0; j < half; j += 64) tma_pair_2d(b + j * 128, &maps.b[0], n + j, r0, bar);
+                        } else {
+                            if (kGated) {
+                                tma_pair_5d(a, &maps.a, k0, 0, 0, m / 16, t.e, bar);
+                            } else if (KIND == kForward) {
+                                tma_pair_3d(a, &maps.a, k0, m, t.e, bar);
+                            } else if (awhole) {
+                                tma_pair_4d(a, &maps.a, 0, k0, m / 64, t.e, bar);
+                            } else {
+                                tma_pair_3d(a, &maps.a, m, k0, t.e, bar);
+                                tma_pair_3d(a + kABytes / 2, &maps.a, m + 64, k0, t.e, bar);
+                            }
+                            tma_pair_2d(b, &maps.b[half / 16 - 1], k0, brow, bar);
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (!mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
-                // 16 values of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
-                const uint64_t da = KIND == kForward ? operand_desc(a) : operand_desc_mn(a, kABytes / 2);
-                const uint64_t db = KIND != kWeight ? operand_desc(b) : operand_desc_mn(b, 64 * 128);
-                constexpr uint64_t sa = (KIND == kForward ? 32 : 16 * 128) >> 4;
-                constexpr uint64_t sb = (KIND != kWeight ? 32 : 16 * 128) >> 4;
-                // of a tail the 16 values that hold its last row are the last
-                const int steps = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1 ? (t.tail + 15) / 16 : kBlockK / 16;
-                if (elect_one()) {
+            }
+            // The MMAs' last arrivals are here before the block ends: they come from the pair's other block.
+            for (uint32_t j = it < kStages ? 0 : it - kStages; ok && j < it; ++j)
+                ok = mbar_wait(empty + 8 * (j % kStages), (j / kStages) & 1, gave_up);
+            if (!ok && rank == 0) {  // given up: the copies in flight end before the block does
+                const uint64_t start = global_ns();
+                for (uint32_t j = it < kStages ? 0 : it - kStages; j < it; ++j)
+                    while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) &&
+                           global_ns() - start < 1000000000ull) {
+                    }
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ---- MMAs of the pair
+            uint32_t it = 0, done = 0;
+            bool ok = true;
+            Walk<KIND> walk;
+            for (uint64_t i = pair; i < g.total && ok; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
+                if (t.blocks == 0) continue;
+                uint32_t buf = 0, d = 0;
+                const uint32_t instr = bf16_instr_desc(kTileM, t.width, KIND != kForward, KIND == kWeight);
+                for (int kb = 0; kb < t.blocks; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    // a new sum: the tile's, or with fp32 outputs a part of it
+                    const bool first = kb == 0 || (F32 && kb % kSeg == 0);
+                    const bool last = kb == t.blocks - 1 || (F32 && kb % kSeg == kSeg - 1);
+                    if (first) {
+                        buf = done & 1;
+                        d = tmem + buf * kTileN;
+                        if (!mbar_wait(acc_empty + 8 * buf, ((done >> 1) & 1) ^ 1, gave_up)) {
+                            ok = false;
+                            break;
+                        }
+                        ++done;
+                    }
+                    if (!mbar_wait(full + 8 * s, (it / kStages) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_addr(stages) + s * kStageBytes, b = a + kABytes;
+                    // 16 values of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
+                    const uint64_t da = KIND == kForward ? operand_desc(a) : operand_desc_mn(a, kABytes / 2);
+                    const uint64_t db = KIND != kWeight ? operand_desc(b) : operand_desc_mn(b, 64 * 128);
+                    constexpr uint64_t sa = (KIND == kForward ? 32 : 16 * 128) >> 4;
+                    constexpr uint64_t sb = (KIND != kWeight ? 32 : 16 * 128) >> 4;
+                    // of a tail the 16 values that hold its last row are the last
+                    const int steps = KIND == kWeight && t.tail != 0 && kb == t.blocks - 1 ? (t.tail + 15) / 16 : kBlockK / 16;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kBlockK / 16; ++j)
-                        if (KIND != kWeight || j < steps)
-                            mma_pair_bf16(d, da + j * sa, db + j * sb, instr, !first || j > 0);
-                    mma_commit_pair(empty + 8 * s);
-                    if (last) mma_commit_pair(acc_full + 8 * buf);
+                        for (int j = 0; j < kBlockK / 16; ++j)
+                            if (KIND != kWeight || j < steps)
+                                mma_pair_bf16(d, da + j * sa, db + j * sb, instr, !first || j > 0);
+                        mma_commit_pair(empty + 8 * s);
+                        if (last) mma_commit_pair(acc_full + 8 * buf);
+                    }
+                    __syncwarp();
                 }
+            }
+            if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
+                if (elect_one()) mma_commit_pair(drain);
                 __syncwarp();
+                const uint64_t start = global_ns();
+                while (!mbar_try_wait(drain, 0) && global_ns() - start < 1000000000ull) {
+                }
+            }
+        } else if (warp == 2 && KIND == kWeight) {
+            // ---- tails: zeros in the rows behind the segment
+            const uint32_t bar0 = cluster_addr(full, 0);
+            uint32_t it = 0, phases = 0;  // a stage's bit: the parity of its tail barrier
+            Walk<KIND> walk;
+            for (uint64_t i = pair; i < g.total; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
+                it += t.blocks;
+                if (t.blocks == 0 || t.tail == 0) continue;
+                const uint32_t s = (it - 1) % kStages;
+                if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up, tile_limit(t.blocks))) break;
+                phases ^= 1u << s;
+                uint8_t* a = stages + s * kStageBytes;
+                const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
+                const int end = (t.tail + 15) / 16 * 16 * 8;  // the MMAs stop there
+                for (int q = t.tail * 8 + lane; q < end; q += 32)
+                    for (int j = 0; j < boxes; ++j)
+                        reinterpret_cast<uint4*>(a + j * 8192)[q] = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                // the zeros are in this block's shared memory, where its tensor core
+                // reads them: a release at cluster scope took 2,000 cycles per tail
+                if (lane == 0) mbar_arrive_pair(bar0 + 8 * s);
             }
         }
-        if (!ok) {  // given up: the MMAs in flight end before the TMEM is freed
-            if (elect_one()) mma_commit_pair(drain);
-            __syncwarp();
-            const uint64_t start = global_ns();
-            while (!mbar_try_wait(drain, 0) && global_ns() - start < 1000000000ull) {
-            }
-        }
-    } else if (warp == 2 && KIND == kWeight) {
-        // ---- tails: zeros in the rows behind the segment
-        const uint32_t bar0 = cluster_addr(full, 0);
-        uint32_t it = 0, phases = 0;  // a stage's bit: the parity of its tail barrier
-        Walk<KIND> walk;
-        for (uint64_t i = pair; i < g.total; i += step) {
-            const Tile t = walk.tile(sh, g, p.E, i);
-            it += t.blocks;
-            if (t.blocks == 0 || t.tail == 0) continue;
-            const uint32_t s = (it - 1) % kStages;
-            if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up, tile_limit(t.blocks))) break;
-            phases ^= 1u << s;
-            uint8_t* a = stages + s * kStageBytes;
-            const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
-            const int end = (t.tail + 15) / 16 * 16 * 8;  // the MMAs stop there
-            for (int q = t.tail * 8 + lane; q < end; q += 32)
-                for (int j = 0; j < boxes; ++j)
-                    reinterpret_cast<uint4*>(a + j * 8192)[q] = make_uint4(0, 0, 0, 0);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            // the zeros are in this block's shared memory, where its tensor core
-            // reads them: a release at cluster scope took 2,000 cycles per tail
-            if (lane == 0) mbar_arrive_pair(bar0 + 8 * s);
-        }
-    }
     } else {
         if (F32) registers_up<kAddRegs>();
         // ---- output
@@ -672,194 +701,194 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             }
             if (KIND == kWeight && lane == 0) tma_store_wait<0>();
         } else {
-        for (uint64_t i = pair; i < g.total; i += step) {
-            const Tile t = walk.tile(sh, g, p.E, i);
-            const uint32_t buf = done & 1;
-            const uint32_t src = lanes + buf * kTileN;
-            // forward and input: lanes are channels, columns tokens
-            const int span = kGated ? 16 : 32;  // output channels of this warp
-            const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
-            const int chans = min(span, g.channels - ch);
-            // What the epilogue reads (a residual, or the pre-activations of gate and up) is asked for a chunk of 32
-            // tokens ahead, the first one before the sums are there.
-            Rows<kReadPieces> ahead[kReads];
-            auto ask = [&](int c) {
-                if (c >= t.n || chans <= 0) return;
-                const int tokens = min(32, t.n - c);
-                const int64_t row = t.row + c;
-                if (KIND == kInput && SWIGLU) {
-                    const uint16_t* z = p.z + row * 2 * K + ch;
-                    ahead[0].load(z, K * 4, tokens, chans * 2);
-                    ahead[kReads - 1].load(z + K, K * 4, tokens, chans * 2);
-                } else if (KIND == kForward && p.residual) {
-                    ahead[0].load(static_cast<const uint16_t*>(p.residual) + row * g.channels + ch,
-                                  (int64_t)g.channels * 2, tokens, chans * 2);
-                }
-            };
-            if (KIND != kWeight) ask(0);
-            if (t.blocks > 0) {
-                if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
-                tc_fence_after();
-            }
-            auto release = [&]() {  // the buffer's last sums are in registers
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
-            };
-            if (KIND == kWeight) {
-                // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
-                const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
-                const int cols = min(t.width, K - t.n0);              // a multiple of 8
-                const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
-                for (int c = end - share; c < end; c += 64) {
-                    const bool write = n < N && c < cols;
-                    if (write) {
-                        if (lane == 0) tma_store_wait<0>();
-                        __syncwarp();
-                        if (p.add) add_to_box(slot, p.add, 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
+            for (uint64_t i = pair; i < g.total; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
+                const uint32_t buf = done & 1;
+                const uint32_t src = lanes + buf * kTileN;
+                // forward and input: lanes are channels, columns tokens
+                const int span = kGated ? 16 : 32;  // output channels of this warp
+                const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
+                const int chans = min(span, g.channels - ch);
+                // What the epilogue reads (a residual, or the pre-activations of gate and up) is asked for a chunk of 32
+                // tokens ahead, the first one before the sums are there.
+                Rows<kReadPieces> ahead[kReads];
+                auto ask = [&](int c) {
+                    if (c >= t.n || chans <= 0) return;
+                    const int tokens = min(32, t.n - c);
+                    const int64_t row = t.row + c;
+                    if (KIND == kInput && SWIGLU) {
+                        const uint16_t* z = p.z + row * 2 * K + ch;
+                        ahead[0].load(z, (int64_t)K * 4, tokens, chans * 2);
+                        ahead[kReads - 1].load(z + K, (int64_t)K * 4, tokens, chans * 2);
+                    } else if (KIND == kForward && p.residual) {
+                        ahead[0].load(static_cast<const uint16_t*>(p.residual) + row * g.channels + ch,
+                                      (int64_t)g.channels * 2, tokens, chans * 2);
                     }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t v[16];
-                        if (t.blocks > 0) {
+                };
+                if (KIND != kWeight) ask(0);
+                if (t.blocks > 0) {
+                    if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
+                    tc_fence_after();
+                }
+                auto release = [&]() {  // the buffer's last sums are in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                };
+                if (KIND == kWeight) {
+                    // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
+                    const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
+                    const int cols = min(t.width, K - t.n0);              // a multiple of 8
+                    const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
+                    for (int c = end - share; c < end; c += 64) {
+                        const bool write = n < N && c < cols;
+                        if (write) {
+                            if (lane == 0) tma_store_wait<0>();
                             __syncwarp();
-                            tmem_load(v, src + c + h * 16);
-                            tmem_wait_for(v);
-                            if (c + h * 16 + 16 >= end) release();
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = 0;
+                            if (p.add) add_to_box(slot, p.add, 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
                         }
-                        if (!write) continue;
-                        float f[16];
-                        as_floats(v, f);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t at = box_at(slot, lane, h * 2 + j);
-                            float* q8 = f + 8 * j;
-                            if (p.add) {
-                                const uint4 q = ld_shared_v4(at);
-                                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t v[16];
+                            if (t.blocks > 0) {
+                                __syncwarp();
+                                tmem_load(v, src + c + h * 16);
+                                tmem_wait_for(v);
+                                if (c + h * 16 + 16 >= end) release();
+                            } else {
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    q8[2 * x] += bf16lo_to_f32(w[x]);
-                                    q8[2 * x + 1] += bf16hi_to_f32(w[x]);
-                                }
+                                for (int j = 0; j < 16; ++j) v[j] = 0;
                             }
-                            st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
-                                                        pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
-                        }
-                    }
-                    if (write) store_box(slot, maps.b[1], t.n0 + c, n, t.e);
-                }
-                if (t.blocks > 0) ++done;
-                continue;
-            }
-            if (chans <= 0) {
-                release();
-                ++done;
-                continue;
-            }
-            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // biases of this lane's channels
-            if (KIND == kForward && p.bias) {
+                            if (!write) continue;
+                            float f[16];
+                            as_floats(v, f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = 8 * j + lane / 4;  // TMEM lane of the warp
-                    const int n = kGated ? ch + k % 16 + (j >= 2 ? g.channels : 0) : ch + k;
-                    if (kGated || n < g.channels) b[j] = load_typed(p.bias, p.bias_type, n);
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t at = box_at(slot, lane, h * 2 + j);
+                                float* q8 = f + 8 * j;
+                                if (p.add) {
+                                    const uint4 q = ld_shared_v4(at);
+                                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        q8[2 * x] += bf16lo_to_f32(w[x]);
+                                        q8[2 * x + 1] += bf16hi_to_f32(w[x]);
+                                    }
+                                }
+                                st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
+                                                            pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
+                            }
+                        }
+                        if (write) store_box(slot, maps.b[1], t.n0 + c, n, t.e);
+                    }
+                    if (t.blocks > 0) ++done;
+                    continue;
                 }
-            }
-            for (int c = 0; c < t.n; c += 32) {
-                const int tokens = min(32, t.n - c);
-                const int64_t row = t.row + c;
-                uint32_t v[2][16];
-                __syncwarp();
-                tmem_load_16x256(v[0], src + c);
-                tmem_load_16x256(v[1], src + c + (16u << 16));
-                tmem_wait_for(v[0]);
-                tmem_wait_for(v[1]);
-                if (c + 32 >= t.n) release();
-                float f[2][16];
-                as_floats(v[0], f[0]);
-                as_floats(v[1], f[1]);
+                if (chans <= 0) {
+                    release();
+                    ++done;
+                    continue;
+                }
+                float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // biases of this lane's channels
                 if (KIND == kForward && p.bias) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        f[0][j] += b[(j >> 1) & 1];
-                        f[1][j] += b[2 + ((j >> 1) & 1)];
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = 8 * j + lane / 4;  // TMEM lane of the warp
+                        const int n = kGated ? ch + k % 16 + (j >= 2 ? g.channels : 0) : ch + k;
+                        if (kGated || n < g.channels) b[j] = load_typed(p.bias, p.bias_type, n);
                     }
                 }
-                uint16_t* out = static_cast<uint16_t*>(p.out);
-                if (kGated) {
-                    if (p.z) {
-                        uint16_t* z = p.z + row * N + ch;
-                        put_fragments<2>(slot, 0, f[0]);
-                        put_fragments<2>(slot + kSlot / 2, 0, f[1]);
-                        write_rows<2>(slot, z, N, tokens, 16);
-                        write_rows<2>(slot + kSlot / 2, z + g.channels, N, tokens, 16);
-                    }
+                for (int c = 0; c < t.n; c += 32) {
+                    const int tokens = min(32, t.n - c);
+                    const int64_t row = t.row + c;
+                    uint32_t v[2][16];
+                    __syncwarp();
+                    tmem_load_16x256(v[0], src + c);
+                    tmem_load_16x256(v[1], src + c + (16u << 16));
+                    tmem_wait_for(v[0]);
+                    tmem_wait_for(v[1]);
+                    if (c + 32 >= t.n) release();
+                    float f[2][16];
+                    as_floats(v[0], f[0]);
+                    as_floats(v[1], f[1]);
+                    if (KIND == kForward && p.bias) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[0][j] = swiglu(f[0][j], f[1][j]);
-                    if (p.residual) {
-                        ahead[0].put(slot + 3 * kSlot / 2);
-                        ask(c + 32);
-                        get_fragments<2>(slot + 3 * kSlot / 2, 0, f[1]);
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) f[0][j] += f[1][j];
-                    }
-                    put_fragments<2>(slot + kSlot, 0, f[0]);
-                    write_rows<2>(slot + kSlot, out + row * g.channels + ch, g.channels, tokens, 16);
-                } else if (KIND == kInput && SWIGLU) {
-                    ahead[0].put(slot);
-                    ahead[kReads - 1].put(slot + kSlot);
-                    ask(c + 32);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float gate[16], up[16];
-                        get_fragments<4>(slot, h, gate);
-                        get_fragments<4>(slot + kSlot, h, up);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) swiglu_back(gate[j], up[j], f[h][j], gate[j], up[j]);
-                        // a lane's fragments of one half are its own to overwrite once all lanes have read theirs
-                        __syncwarp();
-                        put_fragments<4>(slot, h, gate);
-                        put_fragments<4>(slot + kSlot, h, up);
-                    }
-                    uint16_t* dz = out + row * 2 * K + ch;
-                    write_rows<4>(slot, dz, 2 * K, tokens, chans);
-                    write_rows<4>(slot + kSlot, dz + K, 2 * K, tokens, chans);
-                } else {
-                    const int64_t at = row * g.channels + ch;
-                    if (KIND == kForward) {
-                        if (p.z) {
-                            put_fragments<4>(slot, 0, f[0]);
-                            put_fragments<4>(slot, 1, f[1]);
-                            write_rows<4>(slot, p.z + at, g.channels, tokens, chans);
+                        for (int j = 0; j < 16; ++j) {
+                            f[0][j] += b[(j >> 1) & 1];
+                            f[1][j] += b[2 + ((j >> 1) & 1)];
                         }
-                        activate16(f[0], p.activation);
-                        activate16(f[1], p.activation);
+                    }
+                    uint16_t* out = static_cast<uint16_t*>(p.out);
+                    if (kGated) {
+                        if (p.z) {
+                            uint16_t* z = p.z + row * N + ch;
+                            put_fragments<2>(slot, 0, f[0]);
+                            put_fragments<2>(slot + kSlot / 2, 0, f[1]);
+                            write_rows<2>(slot, z, N, tokens, 16);
+                            write_rows<2>(slot + kSlot / 2, z + g.channels, N, tokens, 16);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[0][j] = swiglu(f[0][j], f[1][j]);
                         if (p.residual) {
-                            ahead[0].put(slot + kSlot);
+                            ahead[0].put(slot + 3 * kSlot / 2);
                             ask(c + 32);
+                            get_fragments<2>(slot + 3 * kSlot / 2, 0, f[1]);
+                            __syncwarp();
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float r[16];
-                                get_fragments<4>(slot + kSlot, h, r);
+                            for (int j = 0; j < 16; ++j) f[0][j] += f[1][j];
+                        }
+                        put_fragments<2>(slot + kSlot, 0, f[0]);
+                        write_rows<2>(slot + kSlot, out + row * g.channels + ch, g.channels, tokens, 16);
+                    } else if (KIND == kInput && SWIGLU) {
+                        ahead[0].put(slot);
+                        ahead[kReads - 1].put(slot + kSlot);
+                        ask(c + 32);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) f[h][j] += r[j];
+                        for (int h = 0; h < 2; ++h) {
+                            float gate[16], up[16];
+                            get_fragments<4>(slot, h, gate);
+                            get_fragments<4>(slot + kSlot, h, up);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) swiglu_back(gate[j], up[j], f[h][j], gate[j], up[j]);
+                            // a lane's fragments of one half are its own to overwrite once all lanes have read theirs
+                            __syncwarp();
+                            put_fragments<4>(slot, h, gate);
+                            put_fragments<4>(slot + kSlot, h, up);
+                        }
+                        uint16_t* dz = out + row * 2 * K + ch;
+                        write_rows<4>(slot, dz, 2 * K, tokens, chans);
+                        write_rows<4>(slot + kSlot, dz + K, 2 * K, tokens, chans);
+                    } else {
+                        const int64_t at = row * g.channels + ch;
+                        if (KIND == kForward) {
+                            if (p.z) {
+                                put_fragments<4>(slot, 0, f[0]);
+                                put_fragments<4>(slot, 1, f[1]);
+                                write_rows<4>(slot, p.z + at, g.channels, tokens, chans);
+                            }
+                            activate16(f[0], p.activation);
+                            activate16(f[1], p.activation);
+                            if (p.residual) {
+                                ahead[0].put(slot + kSlot);
+                                ask(c + 32);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float r[16];
+                                    get_fragments<4>(slot + kSlot, h, r);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) f[h][j] += r[j];
+                                }
                             }
                         }
+                        __syncwarp();
+                        put_fragments<4>(slot, 0, f[0]);
+                        put_fragments<4>(slot, 1, f[1]);
+                        write_rows<4>(slot, out + at, g.channels, tokens, chans);
                     }
-                    __syncwarp();
-                    put_fragments<4>(slot, 0, f[0]);
-                    put_fragments<4>(slot, 1, f[1]);
-                    write_rows<4>(slot, out + at, g.channels, tokens, chans);
                 }
+                ++done;
             }
-            ++done;
-        }
-        if (KIND == kWeight && lane == 0) tma_store_wait<0>();
+            if (KIND == kWeight && lane == 0) tma_store_wait<0>();
         }
     }
     __syncwarp();
