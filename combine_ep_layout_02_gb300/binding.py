@@ -6,6 +6,7 @@ and the current CUDA stream.  If the library is missing this module raises;
 there is no fallback of any kind.
 """
 import ctypes
+import functools
 import os
 from collections import namedtuple
 
@@ -774,7 +775,14 @@ def group_gemm_wgrad(dy, x, expert_counts, expert_offsets, kind="contiguous", ca
     return dw
 
 
-LINEAR_FEW_TOKENS = 16
+LINEAR_FEW_TOKENS = 32
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(device_index, M, K, N, act):
+    """A function of the sizes and of the device's SMs."""
+    with torch.cuda.device(device_index):
+        return int(load().ep_linear_workspace_bytes(M, K, N, act))
 
 
 def linear_workspace_bytes(M, K, N, activation="none"):
@@ -823,7 +831,7 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, dtype=to
     lib = _lib or load()
     act = ACTIVATIONS[activation]
     if workspace is None and M > LINEAR_FEW_TOKENS:
-        need = _on_current(dev, lib.ep_linear_workspace_bytes, M, K, N, act)
+        need = _linear_workspace(dev.index, M, K, N, act)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     size = 0

@@ -12,6 +12,12 @@
 //
 // With SwiGLU rows g and g + 8 of a product are gate and up of one channel.
 //
+// One token and 256 rows of 7,168: 3.4 us, mostly the launch and the two
+// reductions.  Eight tokens and 4,096 rows of 7,168: 10.5 us, 5.6 TB/s; 7,168 rows:
+// 17 us, 6.0 TB/s.  The weights are asked for from L2 while the preceding kernel
+// ends.  Beyond EP_LINEAR_FEW_TOKENS the tcgen05 kernel takes less (32 tokens, 7,168
+// rows of 7,168: 25.9 here, 25.5 us there; 256 rows: 5.5 here, 10.8 us there).
+//
 // Below it: the epilogue of a product whose summed index the tcgen05 kernel split
 // into parts, a pass over the parts' fp32 sums.
 #include "ep_products.cuh"
@@ -35,10 +41,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // Up to 8 * NT tokens, RT * 16 rows of weights per block at most: `per` output
 // channels.
 template <int NT, int RT, bool GATED, bool AHEAD>
-__global__ void __launch_bounds__(kThreads, RT == 1 && !AHEAD ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, RT == 1 && NT < 4 && !AHEAD ? 3 : 2)
 linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
     constexpr int kRows = RT * 16, kTokens = NT * 8;
-    constexpr int kUnroll = RT == 1 ? 4 : 2;
+    constexpr int kUnroll = RT == 1 && NT < 4 ? 4 : 2;
     __shared__ float part[kWarps][kTokens][kRows + 1];
     __shared__ float total[kTokens][kRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -279,6 +285,12 @@ cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream) {
     static std::atomic<int> sm_cache[64];
     int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
     if (sms < 1) sms = 1;
+    // More tokens than the 8 columns of a product: their loads weigh as much as the
+    // weights', and 32 rows per block share them.  With up to 32 tokens 16 rows
+    // are better as long as they come in two rounds (256 rows of 7,168: 5.5
+    // against 6.7 us; 7,168 rows of 2,048: 13.1 against 10.7).
+    if (p.rows > 16)
+        return p.N <= 2 * 16 * (int64_t)sms ? launch<4, 1, false>(p, sms, stream) : launch<4, 2, false>(p, sms, stream);
     if (p.rows > 8) return launch<2, 2, false>(p, sms, stream);
     // A warp with four steps or more of the summed index loads a step ahead (two
     // blocks per SM): 4,096 rows of 7,168: 10.5 against 12.3 us; with less to do

@@ -73,7 +73,7 @@ extern "C" {
 #define EP_MAX_EXPERTS 1024
 #define EP_MOE_FEW_MAX_TOKENS 64   /* tokens of one ep_moe_few() call */
 #define EP_MOE_FEW_MAX_WIDTH 16384 /* H and I of ep_moe_few() */
-#define EP_LINEAR_FEW_TOKENS 16    /* ep_linear() needs no workspace up to this M */
+#define EP_LINEAR_FEW_TOKENS 32    /* ep_linear() needs no workspace up to this M */
 #define EP_MAX_GROUPS 32       /* groups of experts that ep_route() can choose among */
 #define EP_STATIC_WS_BYTES (2u << 20) /* scratch held by ep_layout_static_ws() */
 

@@ -29,6 +29,7 @@ def test_names_match_the_header():
     found = {n.lower(): int(v) for n, v in re.findall(r"\bEP_ACT_(\w+) = (\d)", text)}
     assert found == binding.ACTIVATIONS
     assert [binding.TYPES[t] for t in binding.TYPES] == [0, 1]
+    assert int(re.search(r"#define EP_LINEAR_FEW_TOKENS (\d+)", text).group(1)) == binding.LINEAR_FEW_TOKENS
 
 
 GROUP = ["forward", "swiglu", "dgrad", "swiglu_dgrad", "wgrad"]
