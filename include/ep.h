@@ -92,8 +92,8 @@ enum {
     EP_FLAG_BAD_ROW = 4u,    /* dispatch/combine: dst_row outside [-1, rows): skipped */
     EP_FLAG_TIMEOUT = 8u,    /* a wait inside a kernel lasted over a second and was given
                                 up: in the one-launch cluster layout for the other blocks'
-                                totals, in the expert products and the few-token layer for
-                                a copy, a product or another warp.  The outputs are
+                                totals, in the products and the few-token layer for a copy,
+                                a product or another warp.  The outputs are
                                 incomplete (not expected on a working GPU) */
     EP_FLAG_BAD_LOGIT = 16u  /* ep_route: a logit (or logit + bias) is NaN: that expert
                                 was passed over */
