@@ -303,7 +303,7 @@ int cached_device_attribute(cudaDeviceAttr attr, std::atomic<int> (&cache)[64]);
 
 // Launch `kernel` with programmatic stream serialisation allowed, so that its
 // launch overlaps the tail of the previous kernel in the stream.  Every kernel
-// of this library starts with pdl_wait() before touching global memory.
+// launched so starts with pdl_wait() before touching global memory.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args&&... args) {

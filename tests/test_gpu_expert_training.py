@@ -110,6 +110,15 @@ def test_a_route_without_experts():
     assert (out == 0).all() and all((g == 0).all() for g in got[:4])
 
 
+def test_no_tokens():
+    p = problem(3, 64, 16, 4, 2, 6, shared=16)
+    layer = layer_of(p)
+    out, saved = layer.forward(p["x"][:0], p["idx"][:0], p["w"][:0])
+    got = layer.backward(p["dout"][:0], saved)
+    assert out.shape == (0, 64) and got.dx.shape == (0, 64) and got.dtopk_w.shape == (0, 2)
+    assert all((g == 0).all() for g in got[2:]) and ep.status_read(layer.status) == 0
+
+
 def test_captured_step():
     """Forward and backward in one graph, replayed on other inputs."""
     p, q = problem(90, 128, 64, 8, 2, 3, shared=32), problem(90, 128, 64, 8, 2, 4, shared=32)

@@ -56,6 +56,13 @@ def test_plain_products_are_exact_on_exact_data(M, N, K):
     assert torch.equal(ep.linear(**p, bias=bias, residual=res), (want + bias.double() + res.double()).to(BF16))
 
 
+@pytest.mark.parametrize("M", [40, 100, 300])
+@pytest.mark.parametrize("K", [504, 512, 520, 576, 1024, 1088, 4104])
+def test_float32_sums_in_parts_are_exact(M, K):
+    p, g, n = problem(M, 264, K, "none", 14, exact=True)
+    assert torch.equal(ep.linear(**p, dtype=torch.float32), ref.product(p["x"], p["w"])[0].float())
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M", [1, 5, 8, 16, 19, 40, 64, 130, 300])
 @pytest.mark.parametrize("N,K", [(16, 8), (256, 1024), (400, 136), (144, 2056)])

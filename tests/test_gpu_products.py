@@ -182,6 +182,14 @@ def test_many_experts_and_many_tiles():
     check_wgrad(p, 1032, 1032)
 
 
+def test_sums_that_are_added_in_parts():
+    # fp32 sums are cut every 512 rows: whole parts, one row more, 16 more, and a short last one
+    p = Problem([512, 513, 1024, 1040, 511, 4097], "contiguous", 18, exact=True, gap=1)
+    check_wgrad(p, 136, 200)
+    check_wgrad(p, 64, 328, add=True)
+    check_wgrad(p, 136, 200, BF16)
+
+
 def test_weight_gradients_are_added():
     p = Problem([70, 0, 3], "contiguous", 6, exact=True)
     check_wgrad(p, 264, 136, torch.float32, add=True)
