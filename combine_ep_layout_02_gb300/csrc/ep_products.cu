@@ -57,7 +57,8 @@
 // registers, a lane a channel (111 -> 175 us at 19 rows: 64-byte pieces); full
 // tiles of 256 tokens and a rest (2.79 instead of 2.46 ms); several copies of 16
 // rows per stage (each copy costs the stage some 20 cycles); TMEM loads a chunk ahead (no
-// change: a load takes 100 cycles of a chunk's 1,000); a release at cluster scope
+// change: a load takes 100 cycles of a chunk's 1,000); residuals two chunks ahead
+// instead of one (no change); a release at cluster scope
 // behind the tails' zeros (3.49 -> 1.49 ms without).
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
@@ -742,6 +743,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
                     for (int c = end - share; c < end; c += 64) {
                         const bool write = n < N && c < cols;
+                        uint32_t v[4][16] = {};
+                        if (t.blocks > 0) {
+                            __syncwarp();
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tmem_load(v[h], src + c + h * 16);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tmem_wait_for(v[h]);
+                            if (c + 64 >= end) release();
+                        }
                         if (write) {
                             if (lane == 0) tma_store_wait<0>();
                             __syncwarp();
@@ -749,19 +759,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         }
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            uint32_t v[16];
-                            if (t.blocks > 0) {
-                                __syncwarp();
-                                tmem_load(v, src + c + h * 16);
-                                tmem_wait_for(v);
-                                if (c + h * 16 + 16 >= end) release();
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[j] = 0;
-                            }
-                            if (!write) continue;
+                            if (!write) break;
                             float f[16];
-                            as_floats(v, f);
+                            as_floats(v[h], f);
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const uint32_t at = box_at(slot, lane, h * 2 + j);
