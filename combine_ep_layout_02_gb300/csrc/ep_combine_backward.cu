@@ -9,7 +9,9 @@
 // channels of dout and of all rows of the batch before it computes, so that up to
 // nine 16-byte loads are in flight per lane, and keeps a sum per pair.  The
 // lanes' sums meet in a butterfly and the warps' in shared memory, in a fixed
-// order.
+// order.  16,384 tokens of 7,168 channels, k 8: 593 us, 6.74 TB/s (a plain copy
+// 6.78); pair after pair, one warp per token, took 835 us.  128 tokens of 2,048:
+// 4 us, the call 7 us.
 #include "ep_products.cuh"
 
 namespace ep {
