@@ -11,7 +11,8 @@ from .binding import (  # noqa: F401
     layout_static_ws, route, group_gemm_fp8, group_gemm_swiglu_fp8, moe_few,
     moe_few_workspace_bytes, MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_WIDTH, status_read, status_merge, rank_layout, rank_rows_bound, expand, expand_fp8, combine_partial,
     combine_reduce, group_gemm, group_gemm_swiglu, group_gemm_dgrad, group_gemm_swiglu_dgrad, group_gemm_wgrad,
-    linear, linear_backward, linear_workspace_bytes, LINEAR_FEW_TOKENS, LinearGrads, combine_backward, RankLayoutOut, EP_FLAG_BAD_EXPERT, EP_FLAG_OVERFLOW, EP_FLAG_BAD_ROW, EP_FLAG_TIMEOUT,
+    linear, linear_backward, linear_workspace_bytes, linear_backward_workspace_bytes,
+    LINEAR_FEW_TOKENS, LinearGrads, combine_backward, RankLayoutOut, EP_FLAG_BAD_EXPERT, EP_FLAG_OVERFLOW, EP_FLAG_BAD_ROW, EP_FLAG_TIMEOUT,
     EP_FLAG_BAD_LOGIT,
 )
 from .expert_layer import ExpertLayer  # noqa: F401

@@ -89,7 +89,8 @@ def load():
         "ep_group_gemm_wgrad": ([P, P, i64, i64, i64, i32, P, P, i32, i32, P, P, i32, P, P], i32),
         "ep_linear_workspace_bytes": ([i64, i64, i64, i32], sz),
         "ep_linear": ([P, i64, i64, P, i64, P, i32, i32, P, P, i32, P, P, P, sz, P], i32),
-        "ep_linear_backward": ([P, P, P, P, i64, i64, i64, i32, P, P, P, P, i32, P, P, P], i32),
+        "ep_linear_backward_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "ep_linear_backward": ([P, P, P, P, i64, i64, i64, i32, P, P, P, P, i32, P, P, P, sz, P], i32),
         "ep_combine_backward": ([P, P, P, P, i64, i64, i32, i64, P, P, P, P], i32),
         "ep_status_read": ([P, P, P], i32),
         "ep_status_merge": ([P, P, P], i32),
@@ -779,10 +780,11 @@ LINEAR_FEW_TOKENS = 32
 
 
 @functools.lru_cache(maxsize=1024)
-def _linear_workspace(device_index, M, K, N, act):
+def _linear_workspace(device_index, M, K, N, act, backward=False):
     """A function of the sizes and of the device's SMs."""
+    lib = load()
     with torch.cuda.device(device_index):
-        return int(load().ep_linear_workspace_bytes(M, K, N, act))
+        return int((lib.ep_linear_backward_workspace_bytes if backward else lib.ep_linear_workspace_bytes)(M, K, N, act))
 
 
 def linear_workspace_bytes(M, K, N, activation="none"):
@@ -845,11 +847,15 @@ def linear(x, w, bias=None, activation="none", residual=None, out=None, dtype=to
     return out
 
 
+def linear_backward_workspace_bytes(M, K, N, activation="none"):
+    return int(load().ep_linear_backward_workspace_bytes(M, K, N, ACTIVATIONS[activation]))
+
+
 LinearGrads = namedtuple("LinearGrads", "dx dw dbias dz")
 
 
 def linear_backward(dy, x, w, z=None, activation="none", dz=None, dx=None, dw=None, dbias=None, add=None,
-                    dtype=torch.float32, with_dx=True, with_dw=True, with_dbias=True, status=None):
+                    dtype=torch.float32, with_dx=True, with_dw=True, with_dbias=True, workspace=None, status=None):
     """Gradients of ``linear`` from ``dy`` [M, N] bf16 and the pre-activations
     ``z`` that it kept (none for activation "none"): dx [M, K] bf16, dw of w's
     shape (float32 or bf16, ``dtype`` where ``dw`` is not given) with ``add``,
@@ -874,10 +880,19 @@ def linear_backward(dy, x, w, z=None, activation="none", dz=None, dx=None, dw=No
             raise ValueError("there is nothing to add to without dw")
         _result("add", add, dw.shape, dw.dtype, dev)
     dbias = _result("dbias", dbias, (w.shape[0],), torch.float32, dev) if with_dbias else None
+    act = ACTIVATIONS[activation]
+    if workspace is None and dw is not None:
+        need = _linear_workspace(dev.index, M, K, N, act, True)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    size = 0
+    if workspace is not None:
+        _want("workspace", workspace, workspace.dtype, dev)
+        size = workspace.numel() * workspace.element_size()
     _rc("ep_linear_backward", _on_current(
         dev, load().ep_linear_backward, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _addr(z), M, K, N,
-        ACTIVATIONS[activation], _addr(dz), _addr(dx), _addr(add), _addr(dw),
-        0 if dw is None else TYPES[dw.dtype], _addr(dbias), _status_addr(status, dev), _stream_of(dev)))
+        act, _addr(dz), _addr(dx), _addr(add), _addr(dw), 0 if dw is None else TYPES[dw.dtype], _addr(dbias),
+        _status_addr(status, dev), _addr(workspace), size, _stream_of(dev)))
     return LinearGrads(dx, dw, dbias, dz)
 
 

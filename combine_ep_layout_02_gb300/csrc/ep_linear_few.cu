@@ -18,8 +18,8 @@
 // ends.  Beyond EP_LINEAR_FEW_TOKENS the tcgen05 kernel takes less (32 tokens, 7,168
 // rows of 7,168: 25.9 here, 25.5 us there; 256 rows: 5.5 here, 10.8 us there).
 //
-// Below it: the epilogue of a product whose summed index the tcgen05 kernel split
-// into parts, a pass over the parts' fp32 sums.
+// Below it: what follows products whose summed index the tcgen05 kernel split into
+// parts, passes over the parts' fp32 sums.
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
 
@@ -219,6 +219,34 @@ linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
     if (cluster > 1) cluster_sync();  // the other blocks' sums stay until they are read
 }
 
+// Four elements of a weight gradient whose rows were summed in parts.
+__global__ void __launch_bounds__(256)
+weight_finish_kernel(const float4* __restrict__ parts, int splits, int64_t vecs, const void* add, void* out, int type) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= vecs) return;
+    float4 s = parts[i];
+    for (int k = 1; k < splits; ++k) {
+        const float4 v = parts[k * vecs + i];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if (type == EP_TYPE_F32) {
+        if (add) {
+            const float4 a = static_cast<const float4*>(add)[i];
+            s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
+        }
+        static_cast<float4*>(out)[i] = s;
+    } else {
+        if (add) {
+            const uint2 a = static_cast<const uint2*>(add)[i];
+            s.x += bf16lo_to_f32(a.x), s.y += bf16hi_to_f32(a.x);
+            s.z += bf16lo_to_f32(a.y), s.w += bf16hi_to_f32(a.y);
+        }
+        static_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2_rn(s.x, s.y), pack_bf16x2_rn(s.z, s.w));
+    }
+}
+
 template <int NT, int RT, bool AHEAD>
 cudaError_t launch(const ProductArgs& p, int sms, cudaStream_t stream) {
     const bool gated = p.activation == EP_ACT_SWIGLU;
@@ -316,6 +344,12 @@ cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream) {
     // the third block per SM gives more (7,168 rows of 2,048: 5.8 against 8.3 us).
     if (p.K < 4 * 4 * kChunk * kWarps) return launch<1, 1, false>(p, sms, stream);
     return p.N <= 2 * 16 * (int64_t)sms ? launch<1, 1, true>(p, sms, stream) : launch<1, 2, true>(p, sms, stream);
+}
+
+cudaError_t launch_weight_finish(const float* parts, int splits, int64_t count, const void* add, void* out, int type,
+                                 cudaStream_t stream) {
+    return launch_pdl(weight_finish_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, stream,
+                      reinterpret_cast<const float4*>(parts), splits, count / 4, add, out, type);
 }
 
 cudaError_t launch_linear_finish(const ProductArgs& p, const float* parts, int splits, cudaStream_t stream) {

@@ -33,9 +33,11 @@ struct ProductArgs {
     int out_type;
     uint16_t* z;          // kForward: pre-activations out or nullptr; kInput with SwiGLU: in
     uint32_t* status;
-    // kForward of one expert: columns of a tile at most (0: 256), and parts of the
-    // summed index, each with its own fp32 [rows, N] in `out`
+    // one expert: columns of a tile at most (0: 256); kForward: parts of the summed
+    // index, each with its own fp32 [rows, N] in `out`; kWeight: rows of a part
+    // (0: all), each of E parts with its own fp32 [N, K]
     int most, splits;
+    int64_t part_rows;
 };
 
 // How a dense product of more than EP_LINEAR_FEW_TOKENS tokens is cut.
@@ -43,10 +45,16 @@ struct DensePlan {
     int most, splits;
 };
 DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool split);
+// The same for the gradient of [N, K] weights from M rows.
+DensePlan weight_plan(int64_t M, int64_t N, int64_t K, bool split);
 
 // Rows of expert e (of the whole buffer where there are no experts).
 __device__ __forceinline__ Segment product_segment(const ProductArgs& p, int e) {
-    if (p.counts == nullptr) return Segment{0, p.rows, false};
+    if (p.counts == nullptr) {
+        if (p.part_rows == 0) return Segment{0, p.rows, false};
+        const int64_t first = e * p.part_rows;
+        return Segment{first, first + p.part_rows < p.rows ? p.part_rows : p.rows - first, false};
+    }
     return expert_segment(e, p.counts, p.offsets, p.kind, p.capacity, p.rows);
 }
 
@@ -158,6 +166,10 @@ cudaError_t launch_linear_few(const ProductArgs& p, cudaStream_t stream);
 
 // the epilogue over the parts' sums [splits, rows, N]
 cudaError_t launch_linear_finish(const ProductArgs& p, const float* parts, int splits, cudaStream_t stream);
+
+// add (or nothing) and the parts' sums [splits, count] to `out`
+cudaError_t launch_weight_finish(const float* parts, int splits, int64_t count, const void* add, void* out, int type,
+                                 cudaStream_t stream);
 
 // dz (unless nullptr) and column sums of the unrounded dz (unless nullptr)
 cudaError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, int64_t M, int64_t N,

@@ -143,6 +143,7 @@ int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int64_t N, 
     p.add = add;
     p.out = dw;
     p.out_type = dw_type;
+    if (E == 1) p.most = ep::weight_plan(rows, N, K, false).most;
     return cuda_status(ep::launch_product(p, ep::kWeight, as_stream(stream)));
 }
 
@@ -192,9 +193,17 @@ int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N, con
     return cuda_status(err);
 }
 
+size_t ep_linear_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation) {
+    if (check_linear(M, K, N, activation) != EP_OK) return 0;
+    const int64_t wide = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    const int splits = ep::weight_plan(M, wide, K, true).splits;
+    return splits > 1 ? (size_t)splits * wide * K * 4 : 0;
+}
+
 int ep_linear_backward(const void* dy, const void* x, const void* w, const void* z, int64_t M,
                        int64_t K, int64_t N, int activation, void* dz, void* dx, const void* add,
-                       void* dw, int dw_type, float* dbias, uint32_t* status, void* stream) {
+                       void* dw, int dw_type, float* dbias, uint32_t* status, void* workspace,
+                       size_t workspace_bytes, void* stream) {
     const int rc = check_linear(M, K, N, activation);
     if (rc != EP_OK) return rc;
     if (!known_type(dw_type)) return EP_ERR_INVALID_ARG;
@@ -207,6 +216,9 @@ int ep_linear_backward(const void* dy, const void* x, const void* w, const void*
         !aligned(dx, 16) || !aligned(add, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(status, 4))
         return EP_ERR_ALIGNMENT;
     const int64_t wide = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    const size_t need = dw ? ep_linear_backward_workspace_bytes(M, K, N, activation) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return EP_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return EP_ERR_ALIGNMENT;
     cudaError_t err = cudaSuccess;
     if ((act && M > 0) || dbias)
         err = ep::launch_act_backward(bf16(dy), bf16(z), M, N, activation, static_cast<uint16_t*>(dz), dbias,
@@ -219,11 +231,18 @@ int ep_linear_backward(const void* dy, const void* x, const void* w, const void*
         err = ep::launch_product(p, ep::kInput, as_stream(stream));
     }
     if (err == cudaSuccess && dw) {
-        ep::ProductArgs p = group_args(g, x, M, wide, K, 1, nullptr, nullptr, 0, 0, status);
-        p.add = add;
-        p.out = dw;
-        p.out_type = dw_type;
+        const ep::DensePlan plan = ep::weight_plan(M, wide, K, true);
+        const bool split = plan.splits > 1;
+        ep::ProductArgs p = group_args(g, x, M, wide, K, plan.splits, nullptr, nullptr, 0, 0, status);
+        p.most = plan.most;
+        p.add = split ? nullptr : add;
+        p.out = split ? workspace : dw;
+        p.out_type = split ? EP_TYPE_F32 : dw_type;
+        if (split) p.part_rows = ((M + 63) / 64 + plan.splits - 1) / plan.splits * 64;  // whole blocks of the summed index
         err = ep::launch_product(p, ep::kWeight, as_stream(stream));
+        if (err == cudaSuccess && split)
+            err = ep::launch_weight_finish(static_cast<const float*>(workspace), plan.splits, wide * K, add, dw, dw_type,
+                                           as_stream(stream));
     }
     return cuda_status(err);
 }

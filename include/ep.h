@@ -546,12 +546,16 @@ EP_API int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t
  *  dx        [M, K] bf16 out or NULL;  dw [N or 2*N, K] of dw_type out or NULL
  *            (x may be NULL without dw, w without dx);  dbias [N or 2*N] float32
  *            out or NULL;  add as for ep_group_gemm_wgrad.
+ *  workspace ep_linear_backward_workspace_bytes(M, K, N, activation) bytes, as for
+ *            ep_linear; needed with dw alone.
  *  Alignment and limits as above.  M == 0 gives dw = add (or 0) and dbias = 0.
  */
+EP_API size_t ep_linear_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation);
 EP_API int ep_linear_backward(const void* dy, const void* x, const void* w, const void* z,
                               int64_t M, int64_t K, int64_t N, int activation, void* dz, void* dx,
                               const void* add, void* dw, int dw_type, float* dbias,
-                              uint32_t* status, void* stream);
+                              uint32_t* status, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /*
  * ep_combine_backward -- gradients of ep_combine: for every pair with

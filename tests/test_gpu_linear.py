@@ -143,6 +143,31 @@ def test_backward(act, M, N, K):
     check_back(M, N, K, act, 8, add=True)
 
 
+@pytest.mark.parametrize("M,N,K", [(4000, 64, 512), (5271, 128, 264), (8192, 256, 1032), (9000, 8, 8)])
+def test_weight_gradients_of_rows_in_parts(M, N, K):
+    """Few tiles and many rows: the rows are summed in parts."""
+    assert ep.linear_backward_workspace_bytes(M, K, N) > 0
+    p, g, n = problem(M, N, K, "none", 15, exact=True)
+    dy, base = values((M, N), g, True), values((N, K), g, True)
+    want = ref.product(dy.T, p["x"].T)[0]
+    for dtype in (torch.float32, BF16):
+        got = ep.linear_backward(dy, p["x"], p["w"], dtype=dtype)
+        assert torch.equal(got.dw, want.to(dtype)) and torch.equal(got.dbias, dy.double().sum(0).float())
+        dw = base.to(dtype, copy=True)
+        ep.linear_backward(dy, p["x"], p["w"], dw=dw, add=dw, with_dx=False)
+        assert torch.equal(dw, (want + base.double()).to(dtype))
+    check_back(M, N, K, "relu", 16)
+    need = ep.linear_backward_workspace_bytes(M, K, N)
+    for size, fits in ((need, True), (need - 1, False)):
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        if fits:
+            assert torch.equal(ep.linear_backward(dy, p["x"], p["w"], workspace=ws).dw, want.float())
+        else:
+            with pytest.raises(ep.EpError):
+                ep.linear_backward(dy, p["x"], p["w"], workspace=ws)
+            ep.linear_backward(dy, p["x"], p["w"], workspace=ws, with_dw=False)
+
+
 def test_backward_of_parts():
     dy, p, z, all_ = check_back(130, 64, 72, "silu", 9)
     for with_dx in (False, True):

@@ -90,3 +90,37 @@ def test_products_beside_other_kernels():
         torch.cuda.synchronize()
         assert ep.status_read(status) == 0
         assert all(torch.equal(u, v) for u, v in zip(one, want)) and all(torch.equal(u, v) for u, v in zip(two, also))
+
+
+def test_gradients_of_rows_in_parts_back_to_back():
+    """The elementwise pass, both products and the pass over the parts' sums, called
+    and as one graph replayed, on two streams with a workspace each."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    M, N, K = 8192, 256, 1032
+    dy, x, w, z = normal(g, M, N), normal(g, M, K), normal(g, N, K), normal(g, M, N)
+    assert ep.linear_backward_workspace_bytes(M, K, N, "silu") > 0
+    want = ep.linear_backward(dy, x, w, z, "silu")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for st in streams:
+        with torch.cuda.stream(st):
+            ws = torch.empty(ep.linear_backward_workspace_bytes(M, K, N, "silu"), dtype=torch.uint8, device=DEV)
+            out = ep.linear_backward(dy, x, w, z, "silu", workspace=ws)
+            outs.append((ws, out))
+    for _ in range(300):
+        for st, (ws, out) in zip(streams, outs):
+            with torch.cuda.stream(st):
+                ep.linear_backward(dy, x, w, z, "silu", dz=out.dz, dx=out.dx, dw=out.dw, dbias=out.dbias, workspace=ws)
+    torch.cuda.synchronize()
+    for _, out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [ep.linear_backward(dy, x, w, z, "silu") for _ in range(4)]
+    for _ in range(100):
+        graph.replay()
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))

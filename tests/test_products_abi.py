@@ -90,8 +90,9 @@ def test_linear_argument_validation(lib):
 
 def test_linear_backward_argument_validation(lib):
     def call(dy=FAKE, x=FAKE, w=FAKE, z=FAKE, M=4, K=64, N=64, act=2, dz=FAKE, dx=FAKE, add=None, dw=FAKE, ty=0,
-             db=FAKE, status=None):
-        return lib.ep_linear_backward(dy, x, w, z, M, K, N, act, dz, dx, add, dw, ty, db, status, None)
+             db=FAKE, status=None, ws=FAKE, wsb=1 << 40):
+        return lib.ep_linear_backward(dy, x, w, z, M, K, N, act, dz, dx, add, dw, ty, db, status, ws, wsb, None)
+    assert lib.ep_linear_backward_workspace_bytes(4, 64, 64, 2) == 0
     assert call(M=-1) == 1 and call(M=1 << 31) == 1 and call(K=0) == 1 and call(N=0) == 1
     assert call(act=5) == 1 and call(ty=2) == 1
     assert call(K=60) == 2 and call(N=60) == 2 and call(act=4, N=24) == 2
