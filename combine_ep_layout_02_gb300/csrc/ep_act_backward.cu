@@ -10,11 +10,11 @@
 // narrower (down to the 16 of a 32-byte sector) where N has too few strips to
 // fill the SMs.
 //
-// 16,384 x 4,096: ReLU 79 us (5.1 TB/s), SiLU 88, SwiGLU 123 (5.4 TB/s), GELU 116, by
-// then bound by its instructions (75 % of the issue slots).  4,096 x 2,048: 12 to
-// 20 us.  Clusters of four or two: at best 8 % less at one size and more at the
+// 16,384 x 4,096: ReLU 79 us (5.1 TB/s), SiLU 88, SwiGLU 123 (5.4 TB/s), GELU 129,
+// bound by its instructions (75 % of the issue slots when it took 116 with a less exact
+// slope).  4,096 x 2,048: 12 to 21 us.  Clusters of four or two: at best 8 % less at one size and more at the
 // others; two rows per thread and more blocks: 68 and 116 us, but 142 for
-// SwiGLU; GELU two values per instruction: 135 us.
+// SwiGLU; GELU two values per instruction: 135 us against 116.
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
 

@@ -74,35 +74,43 @@ __device__ __forceinline__ float exp2_approx(float v) {
     return r;
 }
 
-// Normal distribution function and e = exp(-v^2 / 2), good to some 10 parts in
-// 2^24 on either side of zero.  With z = |v| / sqrt 2 the tail is erfc(z) / 2 =
-// exp(-z^2) erfcx(z) / 2, and erfcx(z) = t p(t) for t = 1 / (1 + 0.4 z), p being
-// smooth on (0, 1]: a polynomial fitted to the relative error (6e-9) with z up
-// to 9.3.  Below |v| = 1, where 1/2 is the larger part, an odd polynomial (7e-10).  The exponent -v^2 / 2 log2(e) is taken with its rounding error, which
-// the power of two would otherwise multiply.  From |v| = 15 on e is 0.  (With
-// normcdff and a second exp the elementwise pass of 16,384 x 4,096 took 218 us.)
-__device__ __forceinline__ float normal_cdf(float v, float& e) {
-    const float a = fminf(fabsf(v), 15.0f);
+// Tail of the normal distribution beyond a = |v|, from 1 to 15, and e = exp(-v^2 / 2),
+// good to some 10 parts in 2^24.  With z = |v| / sqrt 2 the tail is erfc(z) / 2 =
+// exp(-z^2) erfcx(z) / 2, and erfcx(z) / 2 = t p(t) for t = 1 / (1 + 0.4 z), p being
+// smooth: a polynomial fitted to the relative error (7e-8) with z from 0.7 to 10.6.
+// The exponent -v^2 / 2 log2(e) is taken with its rounding error, which the power
+// of two would otherwise multiply; kNarrow: v is a bf16 value and its square
+// exact.  From |v| = 15 on e is 0.  (With normcdff and a second exp the elementwise
+// pass of 16,384 x 4,096 took 218 us.)
+template <bool kNarrow>
+__device__ __forceinline__ float normal_tail(float a, float& e) {
     const float t = rcp_approx(fmaf(a, 0.28284271247461901f, 1.0f));
-    float p = -0.0310080519f;
-    p = fmaf(p, t, 0.205737795f);
-    p = fmaf(p, t, -0.517100257f);
-    p = fmaf(p, t, 0.57201353f);
-    p = fmaf(p, t, -0.30498704f);
-    p = fmaf(p, t, 0.283243945f);
-    p = fmaf(p, t, 0.125772253f);
-    p = fmaf(p, t, 0.215766981f);
-    p = fmaf(p, t, 0.224848533f);
-    p = fmaf(p, t, 0.225712317f);
+    float p = 0.00450075557f;
+    p = fmaf(p, t, -0.0721399933f);
+    p = fmaf(p, t, 0.139903709f);
+    p = fmaf(p, t, -0.00842234679f);
+    p = fmaf(p, t, 0.111561485f);
+    p = fmaf(p, t, 0.0982244909f);
+    p = fmaf(p, t, 0.113490656f);
+    p = fmaf(p, t, 0.112806149f);
     // -log2(e) / 2 = kHi + kLo
     constexpr float kHi = -0.72134752044448169f;
     constexpr float kLo = (float)(-0.72134752044448169 - (double)kHi);
-    const float square = a * a, left = fmaf(a, a, -square);
+    const float square = a * a;
     const float power = square * kHi;
-    const float rest = fmaf(left, kHi, fmaf(square, kLo, fmaf(square, kHi, -power)));
+    float rest = fmaf(square, kLo, fmaf(square, kHi, -power));
+    if (!kNarrow) rest = fmaf(fmaf(a, a, -square), kHi, rest);
     e = exp2_approx(power);
     e = fmaf(e, rest * 0.69314718055994531f, e);
-    const float tail = 0.5f * t * p * e;
+    return t * p * e;
+}
+
+// Normal distribution function; below |v| = 1, where 1/2 is the larger part, with
+// an odd polynomial (7e-10).
+__device__ __forceinline__ float normal_cdf(float v) {
+    const float a = fminf(fabsf(v), 15.0f), square = a * a;
+    float e;
+    const float tail = normal_tail<false>(a, e);
     float near = -7.65419899e-06f;
     near = fmaf(near, square, 0.000113486348f);
     near = fmaf(near, square, -0.00118632992f);
@@ -116,12 +124,33 @@ __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case EP_ACT_RELU: return v < 0.0f ? 0.0f : v;  // keeps NaN
         case EP_ACT_SILU: return v * sigmoid(v);
-        case EP_ACT_GELU: {
-            float e;
-            return v * normal_cdf(v, e);
-        }
+        case EP_ACT_GELU: return v * normal_cdf(v);
         default: return v;
     }
+}
+
+// Derivative of v Phi(v) times dy, both v and dy being bf16.  Below |v| = 1 it is
+// dy v q(v^2) + dy / 2, where dy v and dy / 2 are exact and q is smooth (fitted to
+// 6e-9): one rounding is left near v = 0, where most values lie.  At v = -0.752, where
+// the two terms cancel, the rounding of q is what would be left, and is added.  (From
+// the distribution function and v e: 116 us for 16,384 x 4,096, here 129; but 240 of
+// 8.4 million gradients rounded to the other bf16 neighbour, here 65, none of them
+// large, and the weights' gradient 2e-6 to 6e-6 off, here 6e-7.)
+__device__ __forceinline__ float gelu_back(float v, float dy) {
+    const float a = fminf(fabsf(v), 15.0f), square = a * a;
+    float e;
+    const float tail = normal_tail<true>(a, e);
+    float r = 9.34694708e-06f;
+    r = fmaf(r, square, -0.000117826632f);
+    r = fmaf(r, square, 0.00116243132f);
+    r = fmaf(r, square, -0.00950479601f);
+    r = fmaf(r, square, 0.0598436482f);
+    r = fmaf(r, square, -0.265961915f);
+    constexpr float kFirst = 0.797884583f;
+    const float q = fmaf(r, square, kFirst), left = fmaf(r, square, kFirst - q), both = dy * v;
+    const float near = fmaf(both, left, fmaf(both, q, 0.5f * dy));
+    const float far = dy * fmaf(v * 0.39894228040143268f, e, v < 0.0f ? tail : 1.0f - tail);
+    return a < 1.0f && fabsf(dy) < INFINITY ? near : far;  // an infinite dy: no inf - inf
 }
 
 // d act / d v, times dy.  The tails are those of the functions: both factors of
@@ -133,11 +162,7 @@ __device__ __forceinline__ float activate_back(float v, float dy, int act) {
             const float s = sigmoid(v);
             return dy * s * fmaf(v, 1.0f - s, 1.0f);
         }
-        case EP_ACT_GELU: {
-            float e;
-            const float cdf = normal_cdf(v, e);
-            return dy * fmaf(v * 0.39894228040143268f, e, cdf);
-        }
+        case EP_ACT_GELU: return gelu_back(v, dy);
         default: return dy;
     }
 }

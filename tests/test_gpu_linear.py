@@ -143,6 +143,36 @@ def test_backward(act, M, N, K):
     check_back(M, N, K, act, 8, add=True)
 
 
+@pytest.mark.parametrize("scale", [1.0, 1.0390625, -1.6171875])
+def test_gelu_backward_keeps_its_digits_where_its_terms_cancel(scale):
+    """The bias gradient of one row is the unrounded dy gelu'(z).  In parts of 2^-24:
+    two roundings of the value; of dy v^3 the last step and the first coefficient
+    of r (1/4 each, of a value below 1/2) and the smaller ones (1/8 in all); of dy
+    the fit, 0.1."""
+    bits = torch.arange(0x3000, 0x3F80, dtype=torch.int32)
+    z = torch.cat([bits, bits | 0x8000]).to(torch.int16).view(BF16).to(DEV).view(1, -1)
+    x, w = torch.zeros(1, 8, dtype=BF16, device=DEV), torch.zeros(z.shape[1], 8, dtype=BF16, device=DEV)
+    got = ep.linear_backward(torch.full_like(z, scale), x, w, z, "gelu").dbias.double()
+    v = z[0].double()
+    want = scale * (ref.cdf(v) + v * ref.phi(v))
+    off = 2 * want.abs() + abs(scale) * (0.625 * v.abs() ** 3 + 0.1)
+    assert want.abs().min() < 1e-3 * abs(scale)
+    assert ((got - want).abs() <= 2.0 ** -24 * off).all()
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_infinite_gradients_stay_infinite(act):
+    z = torch.tensor([[-2.0, -0.9, -0.7, -0.5, -0.0117, 0.0117, 0.5, 0.75, 0.99, 2.0, 1.0, -1.0, 3.0, 0.125, -0.25, 4.0]],
+                     dtype=BF16, device=DEV)
+    x, w = torch.zeros(1, 8, dtype=BF16, device=DEV), torch.zeros(16, 8, dtype=BF16, device=DEV)
+    v = z.double()
+    slope = ref.activation_back(v, torch.ones_like(v), act)[0]
+    for inf in (float("inf"), -float("inf")):
+        got = ep.linear_backward(torch.full_like(z, inf), x, w, z, act, with_dx=False, with_dw=False).dz
+        live = slope != 0
+        assert torch.equal(got[live].double(), (slope * inf)[live])
+
+
 @pytest.mark.parametrize("M,N,K", [(4000, 64, 512), (5271, 128, 264), (8192, 256, 1032), (9000, 8, 8)])
 def test_weight_gradients_of_rows_in_parts(M, N, K):
     """Few tiles and many rows: the rows are summed in parts."""
