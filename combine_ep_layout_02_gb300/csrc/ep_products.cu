@@ -34,12 +34,17 @@
 // row of dw; 128 bytes of 32 rows go through shared memory to a TMA store.
 //
 // The tensor core truncates where it adds to a sum: over n steps of 16 values
-// the result shrinks by about n / 3 parts in 2^24.  That is nothing beside the
-// rounding of a bf16 output, but fp32 outputs (weight gradients, router logits,
-// the parts of a split sum) would show it, so for those a sum ends after 512
-// values and eight warps add the sums, rounded, in registers (128 a thread:
-// setmaxnreg moves registers from the four issuing warps).  1,024 rows: error
-// 1.1e-6 without, 4.4e-7 with; 1.40 against 1.43-1.48 ms for 3.8 GB of gradients.
+// the result shrinks by about n / 3 parts in 2^24 (operands of one sign, spread over
+// many binades: n).  fp32 outputs (weight gradients, router logits, the parts of a
+// split sum) show it, and in time a bf16 output does (4 million rows: 3 %).  So a sum
+// ends after 512 values and eight warps add the sums, rounded, in registers (128 a
+// thread: setmaxnreg moves registers from the four issuing warps).  1,024 rows to
+// fp32: error 1.1e-6 without, 4.4e-7 with; 1.40 against 1.43-1.48 ms for 3.8 GB of
+// gradients.  bf16 outputs keep whole sums up to 16,384 values, where the loss is 2e-5
+// (7e-5 at most) and the rounding 2e-3 to 4e-3: reading the TMEM every 512 values, and
+// one stage less, cost 2 to 8 % there, through SwiGLU's derivative up to 28 % (8
+// experts, 8,192 rows, 4,096 of 7,168: 286 and 299 us; their weights' gradient of
+// 1,024 rows each 272 and 282).
 //
 // Few tokens per expert: bound by the weights' bytes (4 rows each of 128 experts:
 // 84 us, 6.3 TB/s).  Many: by the tensor pipe, 95 % of its cycles busy (8 experts
@@ -71,7 +76,7 @@ constexpr int kMaxStages = 6;
 constexpr int kABytes = 128 * kBlockK * 2, kBBytes = 128 * kBlockK * 2;  // per block and stage
 constexpr int kStageBytes = kABytes + kBBytes;
 // Warps that write the output: four, or two column shares of four (`eight`:
-// gradients of weights and fp32 outputs).
+// sums in parts).
 __host__ __device__ constexpr int epi_warps(bool eight) { return eight ? 8 : 4; }
 __host__ __device__ constexpr int threads_of(bool eight) { return 128 + 32 * epi_warps(eight); }
 constexpr int kSlot = 32 * 64;   // staging: 32 tokens of 32 channels in bf16
@@ -79,10 +84,18 @@ constexpr int kBox = 32 * 128;   // 32 rows of 128 bytes
 // per warp: two slots, or a box, at the expense of a stage
 __host__ __device__ constexpr int staging(bool eight) { return eight ? kBox : 2 * kSlot; }
 __host__ __device__ constexpr int stage_count(bool eight) { return eight ? 5 : kMaxStages; }
-// fp32 outputs: blocks of the summed index whose sum the tensor core makes, and
-// registers of the first warps and of those that add
+// Sums in parts: blocks of the summed index whose sum the tensor core makes, and
+// registers of the first warps and of those that add.
 constexpr int kSeg = 8;
 constexpr int kIssueRegs = 72, kAddRegs = 216;  // 128 * 72 + 256 * 216 = 384 * 168
+// The sum of a bf16 output stays whole up to this many blocks, 16,384 values.
+constexpr int kWholeBlocks = 256;
+// Forward and input products have an instance for either (CUT).  An expert's rows are
+// known on the device alone: the one instance for bf16 weight gradients does both.
+template <ProductKind KIND, bool F32, bool CUT>
+__device__ __forceinline__ bool in_parts(int blocks) {
+    return KIND == kWeight && !F32 ? blocks > kWholeBlocks : CUT;
+}
 constexpr int kBand = 16;        // channel tiles that share the tokens while they are in L2
 
 struct Shared {
@@ -359,6 +372,37 @@ __device__ __forceinline__ void write_weights(const float (&acc)[8][16], const P
     }
 }
 
+// 64 columns of bf16 gradients of weights: rows n.. of dw (a lane's each), columns from k, of which `cols` exist.
+__device__ __forceinline__ void write_weights_bf16(const float (&v)[4][16], const ProductArgs& p, const CUtensorMap& map,
+                                                   uint32_t box, int e, int n, int k, int cols, int N, int K) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) tma_store_wait<0>();
+    __syncwarp();
+    if (p.add) add_to_box(box, p.add, 2, ((int64_t)e * N + n) * K + k, K, N - n, cols);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t at = box_at(box, lane, h * 2 + j);
+            float q8[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) q8[x] = v[h][8 * j + x];
+            if (p.add) {
+                const uint4 q = ld_shared_v4(at);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    q8[2 * x] += bf16lo_to_f32(w[x]);
+                    q8[2 * x + 1] += bf16hi_to_f32(w[x]);
+                }
+            }
+            st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
+                                        pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
+        }
+    }
+    store_box(box, map, k, n, e);
+}
+
 // fp32 outputs of a dense layer: channels ch.. (a lane's each), `share` columns
 // of the tile from c0.  32 tokens of 32 channels turn in shared memory (a lane's
 // channel in, four channels of a token out), so that a store is 16 bytes a lane.
@@ -412,13 +456,14 @@ __device__ __forceinline__ void write_tokens(const float (&acc)[8][16], const Pr
     }
 }
 
-template <ProductKind KIND, bool SWIGLU, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND == kWeight || F32), 1)
+template <ProductKind KIND, bool SWIGLU, bool F32, bool CUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CUT), 1)
 product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p, int most) {
     constexpr bool kGated = SWIGLU && KIND == kForward;  // two rows of weights per output channel
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    constexpr bool kEight = KIND == kWeight || F32;
+    constexpr bool kEight = CUT;
+    static_assert(CUT || (!F32 && KIND != kWeight), "");
     constexpr int kStages = stage_count(kEight), kStaging = staging(kEight);
     constexpr int kEpiWarps = epi_warps(kEight), kThreads = threads_of(kEight);
     uint8_t* slots = stages + kStages * kStageBytes;
@@ -489,7 +534,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     const uint32_t pair = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < 4) {
-        if (F32) registers_down<kIssueRegs>();
+        if (CUT) registers_down<kIssueRegs>();
         if (warp == 0) {
             // ---- loads: this block's 128 rows of A and its half of B's columns
             const uint32_t bar0 = cluster_addr(full, 0);
@@ -575,12 +620,13 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const Tile t = walk.tile(sh, g, p.E, i);
                 if (t.blocks == 0) continue;
                 uint32_t buf = 0, d = 0;
+                const bool parts = in_parts<KIND, F32, CUT>(t.blocks);
                 const uint32_t instr = bf16_instr_desc(kTileM, t.width, KIND != kForward, KIND == kWeight);
                 for (int kb = 0; kb < t.blocks; ++kb, ++it) {
                     const uint32_t s = it % kStages;
-                    // a new sum: the tile's, or with fp32 outputs a part of it
-                    const bool first = kb == 0 || (F32 && kb % kSeg == 0);
-                    const bool last = kb == t.blocks - 1 || (F32 && kb % kSeg == kSeg - 1);
+                    // a new sum: the tile's, or a part of it
+                    const bool first = kb == 0 || (parts && kb % kSeg == 0);
+                    const bool last = kb == t.blocks - 1 || (parts && kb % kSeg == kSeg - 1);
                     if (first) {
                         buf = done & 1;
                         d = tmem + buf * kTileN;
@@ -647,7 +693,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             }
         }
     } else {
-        if (F32) registers_up<kAddRegs>();
+        if (CUT) registers_up<kAddRegs>();
         // ---- output
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -657,8 +703,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         uint32_t done = 0;
         Walk<KIND> walk;
         if constexpr (F32) {
-            // The tensor core truncates where it adds to a sum, which over 4,096 values costs 4e-6 of the result. So
-            // it makes sums of 512 values, and they are added here, rounded, in registers.
             bool ok = true;
             for (uint64_t i = pair; i < g.total && ok; i += step) {
                 const Tile t = walk.tile(sh, g, p.E, i);
@@ -701,21 +745,107 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     write_tokens(acc, p, slot, t, t.m0 + (int)rank * 128 + quarter * 32, c0, share, g.channels);
             }
             if (KIND == kWeight && lane == 0) tma_store_wait<0>();
-        } else {
-            for (uint64_t i = pair; i < g.total; i += step) {
+        } else if constexpr (KIND == kWeight) {
+            // bf16: a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
+            bool ok = true;
+            for (uint64_t i = pair; i < g.total && ok; i += step) {
                 const Tile t = walk.tile(sh, g, p.E, i);
-                const uint32_t buf = done & 1;
-                const uint32_t src = lanes + buf * kTileN;
-                // forward and input: lanes are channels, columns tokens
+                const int n = t.m0 + (int)rank * 128 + quarter * 32;              // the warp's first row
+                const int cols = min(t.width, K - t.n0);                          // a multiple of 8
+                const int share = t.width / 2, c0 = ((warp >> 2) - 1) * share;    // this warp's columns
+                if (!in_parts<KIND, F32, CUT>(t.blocks)) {
+                    const uint32_t buf = done & 1, src = lanes + buf * kTileN;
+                    if (t.blocks > 0) {
+                        if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
+                        tc_fence_after();
+                        ++done;
+                    }
+                    for (int c = c0; c < c0 + share; c += 64) {
+                        uint32_t v[4][16] = {};
+                        if (t.blocks > 0) {
+                            __syncwarp();
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tmem_load(v[h], src + c + h * 16);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tmem_wait_for(v[h]);
+                            if (c + 64 >= c0 + share) {  // the buffer's last sums are in registers
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                            }
+                        }
+                        float f[4][16];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) as_floats(v[h], f[h]);
+                        if (n < N && c < cols)
+                            write_weights_bf16(f, p, maps.b[1], slot, t.e, n, t.n0 + c, cols - c, N, K);
+                    }
+                    continue;
+                }
+                float acc[8][16];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c][j] = 0.0f;
+                for (int kb = 0; kb < t.blocks; kb += kSeg, ++done) {
+                    const uint32_t buf = done & 1, src = lanes + buf * kTileN + c0;
+                    if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        if (c * 16 >= share) break;
+                        uint32_t v[2][16];
+                        tmem_load(v[0], src + c * 16);
+                        tmem_load(v[1], src + c * 16 + 16);  // of an odd share: columns past it, not used
+                        tmem_wait_for(v[0]);
+                        tmem_wait_for(v[1]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            acc[c][j] += __uint_as_float(v[0][j]);
+                            acc[c + 1][j] += __uint_as_float(v[1][j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 8; c += 4) {
+                    if (c * 16 >= share) break;
+                    float f[4][16];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[h][j] = acc[c + h][j];
+                    const int at = c0 + c * 16;
+                    if (n < N && at < cols)
+                        write_weights_bf16(f, p, maps.b[1], slot, t.e, n, t.n0 + at, cols - at, N, K);
+                }
+            }
+            if (lane == 0) tma_store_wait<0>();
+        } else {
+            // Lanes are channels, columns tokens, read in an mma accumulator's layout.  A whole sum goes from TMEM through
+            // four warps; sums in parts are added here, rounded, by eight, and each four have half of the tile's chunks
+            // of 32 tokens.
+            bool ok = true;
+            for (uint64_t i = pair; i < g.total && ok; i += step) {
+                const Tile t = walk.tile(sh, g, p.E, i);
                 const int span = kGated ? 16 : 32;  // output channels of this warp
                 const int ch = t.m0 + (int)rank * (g.per / 2) + quarter * span;
                 const int chans = min(span, g.channels - ch);
+                const int first = CUT ? (t.width + 32) / 64 * 32 : t.width;  // columns of the first four warps
+                const int c0 = warp < 8 ? 0 : first, end = warp < 8 ? min(t.n, first) : t.n;
                 // What the epilogue reads (a residual, or the pre-activations of gate and up) is asked for a chunk of 32
                 // tokens ahead, the first one before the sums are there.
                 Rows<kReadPieces> ahead[kReads];
                 auto ask = [&](int c) {
-                    if (c >= t.n || chans <= 0) return;
-                    const int tokens = min(32, t.n - c);
+                    if (c >= end || chans <= 0) return;
+                    const int tokens = min(32, end - c);
                     const int64_t row = t.row + c;
                     if (KIND == kInput && SWIGLU) {
                         const uint16_t* z = p.z + row * 2 * K + ch;
@@ -726,69 +856,6 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                                       (int64_t)g.channels * 2, tokens, chans * 2);
                     }
                 };
-                if (KIND != kWeight) ask(0);
-                if (t.blocks > 0) {
-                    if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
-                    tc_fence_after();
-                }
-                auto release = [&]() {  // the buffer's last sums are in registers
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
-                };
-                if (KIND == kWeight) {
-                    // a lane is a row of dw; 128 bytes of each row go through a box in shared memory to a TMA store
-                    const int n = t.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
-                    const int cols = min(t.width, K - t.n0);              // a multiple of 8
-                    const int share = t.width / 2, end = (warp >> 2) * share;  // this warp's columns
-                    for (int c = end - share; c < end; c += 64) {
-                        const bool write = n < N && c < cols;
-                        uint32_t v[4][16] = {};
-                        if (t.blocks > 0) {
-                            __syncwarp();
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) tmem_load(v[h], src + c + h * 16);
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) tmem_wait_for(v[h]);
-                            if (c + 64 >= end) release();
-                        }
-                        if (write) {
-                            if (lane == 0) tma_store_wait<0>();
-                            __syncwarp();
-                            if (p.add) add_to_box(slot, p.add, 2, ((int64_t)t.e * N + n) * K + t.n0 + c, K, N - n, cols - c);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            if (!write) break;
-                            float f[16];
-                            as_floats(v[h], f);
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t at = box_at(slot, lane, h * 2 + j);
-                                float* q8 = f + 8 * j;
-                                if (p.add) {
-                                    const uint4 q = ld_shared_v4(at);
-                                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x) {
-                                        q8[2 * x] += bf16lo_to_f32(w[x]);
-                                        q8[2 * x + 1] += bf16hi_to_f32(w[x]);
-                                    }
-                                }
-                                st_shared_v4(at, make_uint4(pack_bf16x2_rn(q8[0], q8[1]), pack_bf16x2_rn(q8[2], q8[3]),
-                                                            pack_bf16x2_rn(q8[4], q8[5]), pack_bf16x2_rn(q8[6], q8[7])));
-                            }
-                        }
-                        if (write) store_box(slot, maps.b[1], t.n0 + c, n, t.e);
-                    }
-                    if (t.blocks > 0) ++done;
-                    continue;
-                }
-                if (chans <= 0) {
-                    release();
-                    ++done;
-                    continue;
-                }
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // biases of this lane's channels
                 if (KIND == kForward && p.bias) {
 #pragma unroll
@@ -798,19 +865,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         if (kGated || n < g.channels) b[j] = load_typed(p.bias, p.bias_type, n);
                     }
                 }
-                for (int c = 0; c < t.n; c += 32) {
-                    const int tokens = min(32, t.n - c);
+                auto finish = [&](float (&f)[2][16], int c) {  // the sums of tokens c..
+                    const int tokens = min(32, end - c);
                     const int64_t row = t.row + c;
-                    uint32_t v[2][16];
-                    __syncwarp();
-                    tmem_load_16x256(v[0], src + c);
-                    tmem_load_16x256(v[1], src + c + (16u << 16));
-                    tmem_wait_for(v[0]);
-                    tmem_wait_for(v[1]);
-                    if (c + 32 >= t.n) release();
-                    float f[2][16];
-                    as_floats(v[0], f[0]);
-                    as_floats(v[1], f[1]);
                     if (KIND == kForward && p.bias) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -885,10 +942,73 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         put_fragments<4>(slot, 1, f[1]);
                         write_rows<4>(slot, out + at, g.channels, tokens, chans);
                     }
+                };
+                if constexpr (CUT) {
+                    float acc[4][2][16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c][0][j] = acc[c][1][j] = 0.0f;
+                    for (int kb = 0; kb < t.blocks; kb += kSeg, ++done) {
+                        const uint32_t buf = done & 1, src = lanes + buf * kTileN + c0;
+                        if (kb + kSeg >= t.blocks) ask(c0);
+                        if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c0 + c * 32 >= end || chans <= 0) break;
+                            uint32_t v[2][16];
+                            tmem_load_16x256(v[0], src + c * 32);
+                            tmem_load_16x256(v[1], src + c * 32 + (16u << 16));
+                            tmem_wait_for(v[0]);
+                            tmem_wait_for(v[1]);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                acc[c][0][j] += __uint_as_float(v[0][j]);
+                                acc[c][1][j] += __uint_as_float(v[1][j]);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c0 + c * 32 >= end || chans <= 0) break;
+                        finish(acc[c], c0 + c * 32);
+                    }
+                } else {
+                    const uint32_t buf = done & 1, src = lanes + buf * kTileN;
+                    ask(0);
+                    if (!mbar_wait(acc_full + 8 * buf, (done >> 1) & 1, gave_up, tile_limit(t.blocks))) break;
+                    tc_fence_after();
+                    auto release = [&]() {  // the buffer's last sums are in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(bar0 + 8 * buf);
+                    };
+                    if (chans <= 0) release();
+                    for (int c = 0; c < end && chans > 0; c += 32) {
+                        uint32_t v[2][16];
+                        __syncwarp();
+                        tmem_load_16x256(v[0], src + c);
+                        tmem_load_16x256(v[1], src + c + (16u << 16));
+                        tmem_wait_for(v[0]);
+                        tmem_wait_for(v[1]);
+                        if (c + 32 >= end) release();
+                        float f[2][16];
+                        as_floats(v[0], f[0]);
+                        as_floats(v[1], f[1]);
+                        finish(f, c);
+                    }
+                    ++done;
                 }
-                ++done;
             }
-            if (KIND == kWeight && lane == 0) tma_store_wait<0>();
         }
     }
     __syncwarp();
@@ -1041,17 +1161,22 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     if (err != cudaSuccess) return err;
     static std::atomic<int> sm_cache[64];
     const int sms = cached_device_attribute(cudaDevAttrMultiProcessorCount, sm_cache);
-    const bool f32 = p.out_type == EP_TYPE_F32, eight = kind == kWeight || f32;
-    static std::atomic<uint64_t> configured[7];
-    const int which = kind == kForward ? (swiglu ? 1 : f32 ? 2 : 0) : kind == kInput ? 3 + swiglu : 5 + f32;
-    auto kernel = which == 0   ? product_kernel<kForward, false, false>
-                  : which == 1 ? product_kernel<kForward, true, false>
-                  : which == 2 ? product_kernel<kForward, false, true>
-                  : which == 3 ? product_kernel<kInput, false, false>
-                  : which == 4 ? product_kernel<kInput, true, false>
-                  : which == 5 ? product_kernel<kWeight, false, false>
-                               : product_kernel<kWeight, false, true>;
-    const size_t smem = smem_bytes(eight);
+    const bool f32 = p.out_type == EP_TYPE_F32;
+    const bool cut = f32 || kind == kWeight || (kind == kForward ? p.K : p.N) > kBlockK * kWholeBlocks;
+    static std::atomic<uint64_t> configured[11];
+    const int which = kind == kWeight ? f32 : f32 ? 2 : 3 + (kind == kInput) * 4 + swiglu * 2 + cut;
+    auto kernel = which == 0   ? product_kernel<kWeight, false, false, true>
+                  : which == 1 ? product_kernel<kWeight, false, true, true>
+                  : which == 2 ? product_kernel<kForward, false, true, true>
+                  : which == 3 ? product_kernel<kForward, false, false, false>
+                  : which == 4 ? product_kernel<kForward, false, false, true>
+                  : which == 5 ? product_kernel<kForward, true, false, false>
+                  : which == 6 ? product_kernel<kForward, true, false, true>
+                  : which == 7 ? product_kernel<kInput, false, false, false>
+                  : which == 8 ? product_kernel<kInput, false, false, true>
+                  : which == 9 ? product_kernel<kInput, true, false, false>
+                               : product_kernel<kInput, true, false, true>;
+    const size_t smem = smem_bytes(cut);
     err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
@@ -1060,7 +1185,7 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     // TMEM brought a chain of launches to a stop.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads_of(eight));
+    cfg.blockDim = dim3(threads_of(cut));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, kernel, maps, p, most);
