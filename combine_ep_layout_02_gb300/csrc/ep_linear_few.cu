@@ -29,7 +29,9 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kChunk = 32;  // of the summed index: two products
 constexpr int kPrefetch = 8192;  // bytes of a row and warp that are asked for from L2 ahead
-constexpr int kSumChunks = 32;   // after which the products' sums, which truncate, are added up, rounded
+constexpr int kSumChunks = 16;   // 512 values, after which the products' sums, which truncate, are added up, rounded
+// A bf16 output, whose rounding hides more, may have whole sums of 16,384 values per warp.
+constexpr int64_t kWholeWidth = 16384 * kWarps;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -41,13 +43,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // Up to 8 * NT tokens, RT * 16 rows of weights per block at most: `per` output
-// channels.
-template <int NT, int RT, bool GATED, bool AHEAD>
+// channels.  CUT: a warp's sum ends every kSumChunks.
+template <int NT, int RT, bool GATED, bool AHEAD, bool CUT>
 __global__ void __launch_bounds__(kThreads, RT == 1 && NT < 4 && !AHEAD ? 3 : 2)
 linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
     constexpr int kRows = RT * 16, kTokens = NT * 8;
     constexpr int kUnroll = RT == 1 && NT < 4 ? 4 : 2;
-    __shared__ float part[kWarps][kTokens][kRows + 1];
+    alignas(16) __shared__ float part[kWarps][kTokens][kRows + 1];
     __shared__ float total[kTokens][kRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
@@ -91,21 +93,32 @@ linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
     }
     pdl_wait();
     pdl_trigger();
-    // with four times two products per step there are no registers for it (25.9 us
-    // would be 31.9), and a warp's sum stays whole: 1e-6 of the result at 8,192
-    constexpr bool kAddUp = NT * RT < 8;
+    // The products' sums are added up in registers, or, where four times two products
+    // per step leave none (25.9 us would be 31.9), in the warp's share of `part`, a
+    // lane's 16 bytes beside the next one's.
+    constexpr bool kInRegisters = NT * RT < 8;
+    static_assert(kTokens * (kRows + 1) >= RT * NT * 4 * 32 && kTokens * (kRows + 1) % 4 == 0, "");
+    float4* kept = reinterpret_cast<float4*>(part[warp][0]) + lane;
+    bool any = false;
     float acc[RT][NT][4] = {}, sums[RT][NT][4] = {};
     auto add_up = [&]() {
-        if (!kAddUp) return;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j) {
+                if (!kInRegisters) {
+                    float4& at = kept[(r * NT + j) * 32];
+                    float4 v = any ? at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    v.x += acc[r][j][0], v.y += acc[r][j][1], v.z += acc[r][j][2], v.w += acc[r][j][3];
+                    at = v;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sums[r][j][i] += acc[r][j][i];
+                    if (kInRegisters) sums[r][j][i] += acc[r][j][i];
                     acc[r][j][i] = 0.0f;
                 }
+            }
+        any = true;
     };
     struct Operands {
         uint4 a[kUnroll][RT][2], b[kUnroll][NT];
@@ -148,12 +161,27 @@ linear_few_kernel(const __grid_constant__ ProductArgs p, int cluster, int per) {
             if ((c - c0) % kSumChunks == kSumChunks - 2 * kUnroll) add_up();
         }
     } else {
-        for (int c = c0; c < c1; c += kUnroll) {
-            Operands o;
-            load(o, c);
-            multiply(o);
-            if ((c - c0) % kSumChunks == kSumChunks - kUnroll) add_up();
+        const int every = CUT ? kSumChunks : chunks;
+        for (int first = c0; first < c1; first += every) {
+            if (CUT && first > c0) add_up();
+            const int end = CUT ? min(c1, first + every) : c1;
+            for (int c = first; c < end; c += kUnroll) {
+                Operands o;
+                load(o, c);
+                multiply(o);
+            }
         }
+    }
+    if (CUT && !kInRegisters && any) {
+        add_up();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float4 v = kept[(r * NT + j) * 32];
+                acc[r][j][0] = v.x, acc[r][j][1] = v.y, acc[r][j][2] = v.z, acc[r][j][3] = v.w;
+            }
+        __syncwarp();  // the same places get the sums by token and row
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -272,7 +300,12 @@ cudaError_t launch(const ProductArgs& p, int sms, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    auto kernel = gated ? linear_few_kernel<NT, RT, true, AHEAD> : linear_few_kernel<NT, RT, false, AHEAD>;
+    // Adding up costs time where it goes through shared memory (32 tokens, 6,000 rows of
+    // 16,384: 50 us, with it 52; 7,168 of 2,048: 10.9 and 11.3), and nothing elsewhere.
+    constexpr bool kAlways = NT * RT < 8;
+    const bool cut = kAlways || p.out_type == EP_TYPE_F32 || p.K > kWholeWidth;
+    auto kernel = gated ? (cut ? linear_few_kernel<NT, RT, true, AHEAD, true> : linear_few_kernel<NT, RT, true, AHEAD, kAlways>)
+                        : (cut ? linear_few_kernel<NT, RT, false, AHEAD, true> : linear_few_kernel<NT, RT, false, AHEAD, kAlways>);
     return cudaLaunchKernelEx(&cfg, kernel, p, cluster, (int)(rounds > 1 ? per : most));
 }
 

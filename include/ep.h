@@ -516,6 +516,8 @@ EP_API int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int6
  * With EP_ACT_SWIGLU w is [2*N, K] and bias [2*N] (gate rows, then up rows) and
  * act is silu(y[m, n]) * y[m, N + n].  Where z is not NULL it gets bf16_rne(y),
  * which ep_linear_backward() needs.
+ * Sums as above: rounded additions of sums of at most 512 values where out is
+ * float32, at most 16,384 where it is bf16, for any M.
  *
  *  x         [M, K] bf16;  w [N or 2*N, K] bf16, both 16-byte aligned.
  *  bias      float32 or bf16 (bias_type), or NULL.

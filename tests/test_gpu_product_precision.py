@@ -72,6 +72,14 @@ def one(n):
     return torch.tensor([n], dtype=torch.int32, device=DEV), torch.tensor([0, n], dtype=torch.int32, device=DEV)
 
 
+@pytest.mark.parametrize("K", [512, 4096, 7168, 16384, 65536])
+@pytest.mark.parametrize("M,N", [(1, 256), (1, 6000), (8, 256), (8, 6000), (12, 256), (16, 6000), (24, 256), (24, 6000),
+                                 (32, 6000), (40, 256), (300, 256), (300, 6000)])
+def test_dense_float32_outputs(M, N, K):
+    x, w = positive(M, K), positive(N, K, seed=1)
+    check_f32(ep.linear(x, w, dtype=F32), product(x, w), K)
+
+
 @pytest.mark.parametrize("rows", [512, 1000, 4096, 16384, 65536, 1 << 18])
 def test_weight_gradients_in_float32(rows):
     dy, x = positive(rows, 264), positive(rows, 136, seed=1)
@@ -125,3 +133,16 @@ def test_dense_layers_of_a_long_summed_index(M, N, act):
     out = ep.linear(x, w, bias=bias, activation=act, residual=res, z=z)
     want, off, y, dy = ref.linear(x, w, bias, act, res)
     assert ref.close(out, want, off) and ref.close(z, y, dy)
+
+
+@pytest.mark.parametrize("M,rows", [(1, 512), (8, 512), (16, 512), (24, 512), (24, 5120)])
+def test_few_tokens_with_a_very_long_summed_index(M, rows):
+    K = 8 * 16384 + 1032  # beyond the longest sum that is never cut
+    x, w = positive(M, K), positive(rows, K, seed=1)
+    want = product(x, w)
+    z = torch.empty(M, rows, dtype=BF16, device=DEV)
+    check_bf16(ep.linear(x, w, z=z), want, K)
+    check_bf16(z, want, K)
+    check_f32(ep.linear(x, w, dtype=F32), want, K)
+    y, off = ref.gated(want, (PART + (parts(K) + 1) / 2 + 2) * U * want)
+    assert ref.close(ep.linear(x, w, activation="swiglu"), y, off)
