@@ -40,9 +40,10 @@
  *    lets the next kernel launch early.  A caller's own kernel launched right
  *    after one of ours WITH that launch attribute must wait on the grid
  *    dependency (griddepcontrol.wait / cudaGridDependencySynchronize) before
- *    reading our outputs; ordinary launches, copies and events need nothing.
- *    The BF16 products (ep_group_gemm .. ep_group_gemm_wgrad, ep_linear above
- *    EP_LINEAR_FEW_TOKENS, ep_linear_backward) are ordinary launches.
+ *    reading our outputs, after every call: the BF16 products themselves are
+ *    launched without the attribute, but a call whose sums were split
+ *    (ep_linear, ep_linear_backward) ends in a pass that has it.  Ordinary
+ *    launches, copies and events need nothing.
  *  - bf16 tensors are passed as raw 16-bit patterns, row-major.
  *  - dst_row[t*k + j] is the row of the dispatch buffer that receives token t
  *    for its j-th expert, or -1 when the pair is not routed (expert id -1, a
