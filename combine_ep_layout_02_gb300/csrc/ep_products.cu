@@ -65,6 +65,7 @@
 // change: a load takes 100 cycles of a chunk's 1,000); residuals two chunks ahead
 // instead of one (no change); a release at cluster scope
 // behind the tails' zeros (3.49 -> 1.49 ms without).
+#include "ep_product_wait.h"
 #include "ep_products.cuh"
 #include "ep_tcgen05.cuh"
 
@@ -197,10 +198,6 @@ struct Walk {
         return t;
     }
 };
-
-// How long a wait for a whole tile may last: a second, and 2 us per block of the
-// summed index, several times what a block takes.
-__device__ __forceinline__ uint64_t tile_limit(int blocks) { return 1000000000ull + 2000ull * (uint32_t)blocks; }
 
 // ---- the epilogue's pieces ---------------------------------------------------
 
@@ -671,13 +668,16 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             // ---- tails: zeros in the rows behind the segment
             const uint32_t bar0 = cluster_addr(full, 0);
             uint32_t it = 0, phases = 0;  // a stage's bit: the parity of its tail barrier
+            TileWait since;
             Walk<KIND> walk;
             for (uint64_t i = pair; i < g.total; i += step) {
                 const Tile t = walk.tile(sh, g, p.E, i);
                 it += t.blocks;
+                since.enter(t.blocks);
                 if (t.blocks == 0 || t.tail == 0) continue;
                 const uint32_t s = (it - 1) % kStages;
-                if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up, tile_limit(t.blocks))) break;
+                if (!mbar_wait(tail + 8 * s, (phases >> s) & 1, gave_up, since.limit())) break;
+                since.waited();
                 phases ^= 1u << s;
                 uint8_t* a = stages + s * kStageBytes;
                 const int boxes = 2 + t.width / 128;  // of 64 rows x 128 bytes, A's and B's
