@@ -41,6 +41,28 @@ __device__ __forceinline__ Segment expert_segment(int e, const int32_t* __restri
     return s;
 }
 
+// Exclusive scan, by a whole warp, of the experts' tiles of `most` rows into
+// tiles[0..E].  Segments that overlap can make more than 31 bits of them: then
+// there are none, and the answer is false.
+__device__ __forceinline__ bool scan_tiles(const int* count, int E, int most, int* tiles) {
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int64_t n = e0 + lane < E ? ((int64_t)count[e0 + lane] + most - 1) / most : 0;
+        int64_t s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(kFullMask, s, o);
+            if (lane >= o) s += v;
+        }
+        if (e0 + lane < E) tiles[e0 + lane] = (int)(base + s - n);
+        base += __shfl_sync(kFullMask, s, 31);
+    }
+    const bool fits = base <= INT32_MAX;
+    if (lane == 0) tiles[E] = fits ? (int)base : 0;
+    return fits;
+}
+
 // ---- launchers (host) ------------------------------------------------------
 
 // the router's top-k choice

@@ -154,21 +154,8 @@ group_gemm_kernel(const __grid_constant__ CUtensorMap a_map,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {
-        int base = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int n = e0 + lane < E ? (sh.count[e0 + lane] + kRowsM - 1) / kRowsM : 0;
-            int s = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kFullMask, s, o);
-                if (lane >= o) s += v;
-            }
-            if (e0 + lane < E) sh.tiles[e0 + lane] = base + s - n;
-            base += __shfl_sync(kFullMask, s, 31);
-        }
-        if (lane == 0) sh.tiles[E] = base;
-    }
+    if (warp == 0 && !scan_tiles(sh.count, E, kRowsM, sh.tiles) && tid == 0 && blockIdx.x == 0 && status)
+        atomicOr(status, EP_FLAG_BAD_ROW);
     __syncthreads();
 
     const uint32_t tmem = sh.tmem;

@@ -498,21 +498,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (KIND != kWeight && warp == 0) {
-        int base = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int n = e0 + lane < p.E ? (int)(((int64_t)sh.count[e0 + lane] + most - 1) / most) : 0;
-            int s = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kFullMask, s, o);
-                if (lane >= o) s += v;
-            }
-            if (e0 + lane < p.E) sh.tiles[e0 + lane] = base + s - n;
-            base += __shfl_sync(kFullMask, s, 31);
-        }
-        if (lane == 0) sh.tiles[p.E] = base;
-    }
+    if (KIND != kWeight && warp == 0 && !scan_tiles(sh.count, p.E, most, sh.tiles) && tid == 0 && blockIdx.x == 0 &&
+        p.status)
+        atomicOr(p.status, EP_FLAG_BAD_ROW);
     cluster_sync();  // both blocks' barriers are set up
 
     const uint32_t tmem = sh.tmem;

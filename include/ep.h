@@ -344,7 +344,8 @@ EP_API int ep_layout_dispatch_fp8(const int32_t* topk_idx, int64_t T, int k, int
  *            first min(expert_counts[e], capacity) rows from e*capacity
  *            (expert_offsets may be NULL; rows >= E*capacity).
  *            A contiguous segment outside [0, rows) is cut to it and raises
- *            EP_FLAG_BAD_ROW.  Rows of no segment are never written and change no
+ *            EP_FLAG_BAD_ROW; segments that overlap until their tiles pass 31
+ *            bits raise it too, and nothing is computed.  Rows of no segment are never written and change no
  *            result, whatever they hold; up to 31 rows that follow a segment in
  *            the buffer may be read.
  *  out       [rows, N] bf16, 16-byte aligned.
