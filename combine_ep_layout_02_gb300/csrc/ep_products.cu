@@ -215,7 +215,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, const uint4& v) {
 }
 
 // The addend of a box of 32 rows x 128 bytes: `rows` and `cols` exist, the
-// first of them at element `at`, rows ld apart.
+// first of them at element `at`, rows ld apart.  Read box by box, each with its whole
+// latency: 64 experts, 65,536 rows, 2,048 x 7,168, fp32 1.48 ms without and 2.8 with an
+// addend, bf16 1.24 and 1.43; 2,300 rows of 128 experts, 2,048 x 1,024: 188 and 720 us, 93
+// and 327 (3 and 5 times the addend's bytes).
 __device__ __forceinline__ void add_to_box(uint32_t box, const void* add, int size, int64_t at, int64_t ld, int rows,
                                            int cols) {
     const int lane = threadIdx.x & 31, piece = lane & 7;
@@ -1023,7 +1026,8 @@ DensePlan dense_plan(int64_t M, int64_t K, int64_t channels, bool gated, bool sp
     Known& at = known[(uint64_t)(M * 31 + K * 7 + channels * 3 + rest) % 16];
     if (at.M == M && at.K == K && at.channels == channels && at.rest == rest) return at.plan;
     // Cycles of a stage for 32, 64, .. 256 columns, measured on a dense layer of
-    // 4,096 channels: the narrow ones wait for the weights from L2.
+    // 4,096 channels: the narrow ones wait for the weights from L2.  Input products, whose
+    // weights lie the other way, are planned by the same figures.
     static const int stage[8] = {276, 285, 311, 330, 357, 421, 458, 512};
     // the second pass: its launch behind the first (some 3 us), and as much again on the host
     constexpr double kFinishCycles = 9000.0;
@@ -1168,9 +1172,12 @@ cudaError_t launch_product(const ProductArgs& p, ProductKind kind, cudaStream_t 
     err = raise_smem_limit(kernel, smem, configured[which]);
     if (err != cudaSuccess) return err;
     const unsigned grid = sms >= 2 ? (unsigned)(sms & ~1) : 2u;
-    // An ordinary launch, and no early one of what follows: blocks of another
-    // kernel that were started on one SM of a pair while the other still held its
-    // TMEM brought a chain of launches to a stop.
+    // An ordinary launch, and no early one of what follows.  As programmatic launches a
+    // chain elementwise pass, input product, weight product came to a stop.  By reading:
+    // blocks of another kernel were started on one SM of a pair while the other still
+    // released its TMEM.  Mended together, and not told apart: this, the barrier after the
+    // release, the loading warp's wait for the MMAs' last arrivals in the other block, and
+    // a warp's reconvergence before a cluster barrier.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads_of(cut));

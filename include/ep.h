@@ -532,7 +532,7 @@ EP_API int ep_group_gemm_wgrad(const void* dy, const void* x, int64_t rows, int6
  *            may be NULL where the size is 0.
  * Limits: K and N multiples of 8; with EP_ACT_SWIGLU N a multiple of 16 and
  * out_type EP_TYPE_BF16; M < 2^31 - 256, K and the rows of w at most 2^30.
- * M == 0 is valid.
+ * Outputs overlap no input (but residual may be out).  M == 0 is valid.
  */
 EP_API size_t ep_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation);
 EP_API int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t N,
@@ -555,7 +555,8 @@ EP_API int ep_linear(const void* x, int64_t M, int64_t K, const void* w, int64_t
  *            out or NULL;  add as for ep_group_gemm_wgrad.
  *  workspace ep_linear_backward_workspace_bytes(M, K, N, activation) bytes, as for
  *            ep_linear; needed with dw alone.
- *  Alignment and limits as above.  M == 0 gives dw = add (or 0) and dbias = 0.
+ *  Outputs overlap no input (but add may be dw).  Alignment and limits as above.
+ *  M == 0 gives dw = add (or 0) and dbias = 0.
  */
 EP_API size_t ep_linear_backward_workspace_bytes(int64_t M, int64_t K, int64_t N, int activation);
 EP_API int ep_linear_backward(const void* dy, const void* x, const void* w, const void* z,
